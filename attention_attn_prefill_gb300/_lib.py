@@ -34,6 +34,7 @@ class AttnError(RuntimeError):
 _lib = None
 
 c_int, c_float, c_void_p, c_size_t = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+c_ll, c_double = ctypes.c_longlong, ctypes.c_double
 c_u32_p = ctypes.POINTER(ctypes.c_uint32)
 
 _SIGNATURES = {
@@ -60,6 +61,17 @@ _SIGNATURES = {
     "attn_emulated_workspace_bytes": (c_size_t, [c_int] * 4),
     "attn_decode_paged_emulated": (c_int, [c_void_p] * 7 + [c_int] * 9 + [c_float, c_void_p, c_size_t, c_void_p]),
     "attn_merge_emulated": (c_int, [c_int] + [c_void_p] * 3 + [c_int] * 3 + [c_void_p] * 4),
+    "attn_step_tables": (c_int, [c_void_p] * 9 + [c_int] * 6 + [c_void_p]),
+    "attn_rope_table": (c_int, [c_void_p, c_int, c_int, c_double, c_void_p]),
+    "attn_qk_norm_rope": (c_int, [c_void_p, c_ll] * 3 + [c_void_p] * 2 + [c_float] + [c_void_p] * 2 + [c_int] * 3
+                          + [c_void_p, c_ll] * 2 + [c_void_p] * 3 + [c_int] * 6 + [c_void_p]),
+    "attn_cache_q4_record_bytes": (c_size_t, [c_int]),
+    "attn_cache_append_q4": (c_int, [c_void_p, c_ll] * 2 + [c_void_p] * 2 + [c_int] * 5 + [c_void_p]),
+    "attn_cache_gather_q4": (c_int, [c_void_p] * 5 + [c_int] * 6 + [c_void_p]),
+    "attn_decode_q4_workspace_bytes": (c_size_t, [c_int]),
+    "attn_decode_paged_q4": (c_int, [c_void_p] * 6 + [c_int] * 7 + [c_float, c_void_p, c_size_t, c_void_p]),
+    "attn_prefill_q4_workspace_bytes": (c_size_t, [c_int] * 4),
+    "attn_prefill_paged_q4": (c_int, [c_void_p] * 7 + [c_int] * 9 + [c_float, c_int, c_void_p, c_size_t, c_void_p]),
 }
 
 # Decode numerics of other backends (attn_numerics_t).

@@ -14,6 +14,7 @@
 #include "attn.h"
 #include "decode.h"
 #include "prefill.h"
+#include "step.h"
 
 namespace {
 
@@ -600,10 +601,14 @@ attn_status_t attn_merge_emulated(int numerics, const float* part_o, const float
 attn_status_t attn_device_status(uint32_t* code, int clear) {
   if (code == nullptr) return ATTN_ERR_INVALID_ARG;
   if (cudaDeviceSynchronize() != cudaSuccess) return ATTN_ERR_CUDA;
-  uint32_t a = 0, b = 0;
-  if (attn::prefill_status(&a, clear != 0) != cudaSuccess) return ATTN_ERR_CUDA;
-  if (attn::decode_status(&b, clear != 0) != cudaSuccess) return ATTN_ERR_CUDA;
-  *code = a != 0 ? a : b;
+  uint32_t first = 0;
+  for (auto status : {attn::prefill_status, attn::decode_status, attn::step_tables_status, attn::qk_rope_status,
+                      attn::cache_q4_status, attn::decode_q4_status}) {
+    uint32_t word = 0;
+    if (status(&word, clear != 0) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (first == 0) first = word;
+  }
+  *code = first;
   return ATTN_OK;
 }
 

@@ -26,6 +26,9 @@ enum DeviceError : uint32_t {
   kDevBadSplit = 3,          // split geometry inconsistent with the launch
   kDevMisaligned = 4,        // dynamic shared memory not 1 KB-aligned
   kDevBadSeqlens = 5,        // cu_seqlens not increasing, past the tokens, or longer than max_seqlen
+  kDevBadStep = 6,           // a step's lengths do not fit the block table or the token count, or no free page is left
+  kDevBadPosition = 7,       // a position outside the rotation table
+  kDevBadSlot = 8,           // a cache slot past the last page
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -118,6 +121,14 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, uint64_t
       "[%5];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+
+// `bytes` contiguous bytes; both addresses and the size are multiples of 16
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
 __device__ __forceinline__ void tma_store_3d(const void* map, const void* src, int32_t x, int32_t y, int32_t z) {

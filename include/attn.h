@@ -456,13 +456,193 @@ attn_status_t attn_merge_emulated(int numerics, const float* part_o, const float
                                   int rows, int num_splits, int d, float* o_f32, void* o, float* lse, void* stream);
 
 /*
+ * ---- The serving step around the attention calls.
+ *
+ * A step of a serving program: attn_step_tables turns request lengths into
+ * block tables, positions and slots; attn_qk_norm_rope prepares queries and
+ * keys and writes K and V to the paged bf16 cache (or attn_cache_append_q4 to
+ * a 4-bit one); then attn_decode_paged / attn_prefill_paged run on the bf16
+ * cache, attn_decode_paged_q4 / attn_prefill_paged_q4 on the 4-bit one.  A
+ * slot is page * 16 + row: the place of one token in a paged cache.
+ */
+
+/*
+ * Tables of one serving step.
+ *   cached_lens [num_seqs] int32: tokens of each request already in the cache
+ *   new_lens    [num_seqs] int32: tokens the request adds in this step (>= 0);
+ *               the step's tokens are packed, request after request
+ *   free_pages  [num_free] int32: unused physical pages, taken from the front
+ *   block_table [num_seqs, max_blocks_per_seq] int32, in and out: holds the
+ *               pages of the cached tokens; the pages this step takes are
+ *               entered behind them, nothing else is written
+ *   seq_lens    [num_seqs] (output) = cached + new
+ *   cu_seqlens  [num_seqs + 1] (output): exclusive prefix sum of new_lens
+ *   positions   [num_tokens] (output): position of each new token in its sequence
+ *   slots       [num_tokens] (output): block_table[n][position / 16] * 16 + position % 16
+ *   pages_used  [1] (output): pages taken from the front of free_pages
+ * num_tokens >= sum of new_lens; the tokens behind the last request (padding,
+ * for example of a captured graph) get position 0 and slot -1.  num_tokens may
+ * be 0.  Pages go to the requests in order, a request's in the order of its
+ * tokens; a step that is repeated on the same inputs gives the same tables.
+ * A request whose lengths are negative or exceed the block table, for which
+ * the free pages do not suffice, or whose tokens do not fit num_tokens, is
+ * recorded as device status 6: it takes no page, its seq_len stays
+ * cached_len, its tokens get position 0 and slot -1 (and so do those of the
+ * requests after it that need pages, once the pages are used up).  A page id
+ * outside [0, num_blocks) is recorded as 2, the slots on it are -1 and the
+ * table is not written.
+ */
+attn_status_t attn_step_tables(const int32_t* cached_lens, const int32_t* new_lens, const int32_t* free_pages,
+                               int32_t* block_table, int32_t* seq_lens, int32_t* cu_seqlens, int32_t* positions,
+                               int32_t* slots, int32_t* pages_used, int num_seqs, int num_tokens, int num_free,
+                               int page_size, int max_blocks_per_seq, int num_blocks, void* stream);
+
+/*
+ * Rotation table: table [max_positions, rot] f32; row p holds cos(p w_i) for
+ * i = 0 .. rot / 2 - 1, then sin(p w_i), with w_i = theta^(-2 i / rot), the
+ * angle computed in double.  rot is a multiple of 16, at most 256.
+ */
+attn_status_t attn_rope_table(float* table, int max_positions, int rot, double theta, void* stream);
+
+/*
+ * RMS norm of each query and key head and rotation by position, in one pass;
+ * keys and values can be written to the paged cache in the same pass.
+ *   q [num_tokens, Hq, d], k and v [num_tokens, Hkv, d] bf16: the heads of a
+ *     token are dense, tokens are q_stride / k_stride / v_stride elements
+ *     apart (views of one projection's output); strides are multiples of 8.
+ *     d in {64, 128, 256}; Hq need not be a multiple of Hkv here.
+ *   q_weight, k_weight [d] bf16 or NULL: y = x * rsqrt(mean(x^2) + eps) * w;
+ *     NULL: no norm
+ *   the first rot channels (a multiple of 16, 0 .. d; 0: no rotation) are
+ *     turned: (a, b) -> (a cos - b sin, b cos + a sin) with pair i = channels
+ *     (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved != 0, and cos, sin
+ *     from row positions[token] of table (attn_rope_table's layout)
+ *   q_out [num_tokens, Hq, d], k_out [num_tokens, Hkv, d] (or NULL) bf16, with
+ *     token strides of their own; either may be its input (same pointer and
+ *     stride), and overlaps no other tensor of the call
+ *   k_cache, v_cache [num_blocks, 16, Hkv, d] bf16 or both NULL: the result
+ *     for k and v itself go to slots[token]; a token with a negative slot is
+ *     not written.  The non-negative slots of a call are distinct.
+ *   v and slots are read only with a cache; k_out may be NULL only with one.
+ * Arithmetic: float32, one rounding to bf16 (nearest even).  A position
+ * outside [0, max_positions) is recorded as device status 7 (the nearest row
+ * is used), a slot past the last page as 8 (the token is not written).
+ */
+attn_status_t attn_qk_norm_rope(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                                long long v_stride, const void* q_weight, const void* k_weight, float eps,
+                                const int32_t* positions, const float* table, int max_positions, int rot,
+                                int interleaved, void* q_out, long long q_out_stride, void* k_out,
+                                long long k_out_stride, void* k_cache, void* v_cache, const int32_t* slots,
+                                int num_tokens, int Hq, int Hkv, int d, int page_size, int num_blocks, void* stream);
+
+/*
+ * The 4-bit paged cache: [num_blocks, Hkv, 17 d] bytes, one record for each
+ * page and KV head (attn_cache_q4_record_bytes(d) = 17 d for d in {64, 128,
+ * 256}, else 0): 17 / 32 of a byte a value, against 2 in bf16.
+ * Format: a group is 64 consecutive channels of one token's key (or value)
+ * head.  With hi = max(x, 0) and lo = min(x, 0) over the group,
+ *   s = (hi - lo) / 15 rounded up to 4 significant bits (to a multiple of
+ *       2^-129 below 2^-126),
+ *   z = rint(-lo / s), code = clamp(rint(x / s) + z, 0, 15)
+ * and the code stands for s * (code - z): within half a step s of x, and a
+ * bf16 number exactly, so that reading a cache back loses nothing more.  A
+ * group that holds an infinity or NaN, or whose hi - lo overflows float32,
+ * reads back as NaN.  A record holds 16 tokens:
+ *   bytes [0, 8 d): K codes, d / 2 bytes a token; the 32-bit word that holds
+ *     channels 64 e + 16 t + 8 h + (0 .. 7) of a token, channel j in nibble
+ *     j, then rotated left by 3 bits, is word
+ *     (e / P) * 8 P + t * 2 P + (e % P) * 2 + h of its row, P = min(2, d / 64);
+ *   bytes [8 d, 16 d): V codes; channels 2 j (low nibble) and 2 j + 1 of
+ *     token k are byte (32 (j / 32) + 4 (j % 8) + (k % 8) / 2) * 16 +
+ *     4 (j / 8 % 4) + k / 8 + 2 (k % 2);
+ *   bytes [16 d, 16.5 d): K parameters, [16][d / 64] 16-bit words: s as bf16,
+ *     whose lower 4 bits are zero, plus z;
+ *   bytes [16.5 d, 17 d): V parameters, likewise.
+ */
+size_t attn_cache_q4_record_bytes(int d);
+
+/*
+ * Writes new tokens into the 4-bit cache.
+ *   k, v  [num_tokens, Hkv, d] bf16, tokens k_stride / v_stride elements apart
+ *         (multiples of 8), the heads of a token dense
+ *   slots [num_tokens] int32; a token with a negative slot is not written
+ *   cache [num_blocks, Hkv, 17 d] (in and out): only the given tokens' bytes change
+ * The non-negative slots of a call are distinct.  A slot past the last page is
+ * recorded as device status 8 and skipped.
+ */
+attn_status_t attn_cache_append_q4(const void* k, long long k_stride, const void* v, long long v_stride,
+                                   const int32_t* slots, void* cache, int num_tokens, int Hkv, int d, int page_size,
+                                   int num_blocks, void* stream);
+
+/*
+ * Reads sequences of the 4-bit cache back.
+ *   block_table [num_seqs, max_blocks_per_seq], seq_lens [num_seqs] as for
+ *   attn_decode_paged
+ *   k_out, v_out [num_seqs, max_blocks_per_seq * 16, Hkv, d] bf16 (output);
+ *   rows behind a sequence's end are not written
+ * A block-table entry outside [0, num_blocks) is recorded as device status 2
+ * (page 0 is read instead), a seq_len the table cannot cover as 5 (clamped).
+ */
+attn_status_t attn_cache_gather_q4(const void* cache, const int32_t* block_table, const int32_t* seq_lens,
+                                   void* k_out, void* v_out, int num_seqs, int Hkv, int d, int page_size,
+                                   int max_blocks_per_seq, int num_blocks, void* stream);
+
+/*
+ * Bytes of workspace attn_decode_paged_q4 needs on the current device, whatever
+ * the batch: two partials of 8 query heads for each CTA of a grid that fills
+ * the device.  0 for a head dim other than 64, 128, 256 or when no CUDA device
+ * can be queried.
+ */
+size_t attn_decode_q4_workspace_bytes(int d);
+
+/*
+ * attn_decode_paged over the 4-bit cache: q, block_table, seq_lens, o, lse,
+ * scale and the conventions for empty sequences, last pages and block-table
+ * entries out of range are as there.  d in {64, 128, 256}; any number of
+ * query heads per KV head.  The split over the context is chosen on the
+ * device, from the lengths: equal shares of all pages, one a CTA.
+ * Arithmetic: products of the bf16 queries and the codes, which are exact;
+ * float32 scores, sums and accumulators; each probability times its value's
+ * scale enters the product with V as the sum of two bf16 numbers (16 bits).
+ * workspace: device buffer, 16-byte aligned, of at least
+ * attn_decode_q4_workspace_bytes(d) bytes.  What a call reads from it the same
+ * call has written; calls that overlap on the GPU (two streams, two graphs)
+ * need one each.
+ */
+attn_status_t attn_decode_paged_q4(const void* q, const void* cache, const int32_t* block_table,
+                                   const int32_t* seq_lens, void* o, float* lse, int num_seqs, int Hq, int Hkv, int d,
+                                   int page_size, int max_blocks_per_seq, int num_blocks, float scale,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace attn_prefill_paged_q4 needs: keys and values of num_seqs *
+ * max_blocks_per_seq pages in bf16 and their block table, each rounded up to
+ * 256.  0 for invalid arguments (also more than 2^30 token rows).
+ */
+size_t attn_prefill_q4_workspace_bytes(int num_seqs, int Hkv, int d, int max_blocks_per_seq);
+
+/*
+ * attn_prefill_paged over the 4-bit cache: the sequences are read back into
+ * the workspace (256-byte aligned), which loses nothing, and attended there.
+ * Arguments, results and arithmetic are otherwise those of
+ * attn_prefill_paged.  Calls that overlap on the GPU need a workspace each.
+ */
+attn_status_t attn_prefill_paged_q4(const void* q, const void* cache, const int32_t* block_table,
+                                    const int32_t* cu_seqlens_q, const int32_t* seq_lens, void* o, float* lse,
+                                    int num_seqs, int max_seqlen_q, int total_q, int Hq, int Hkv, int d,
+                                    int page_size, int max_blocks_per_seq, int num_blocks, float scale, int causal,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Device-side status: waits for all work on the current device, then stores
  * the first error code any kernel of this library recorded since the last
  * clear (0 = none; 1 = a pipeline wait timed out; 2 = block-table entry out of
  * range; 3 = a seq_len the block table cannot cover; 4 = shared memory not
  * 1 KB-aligned; 5 = cu_seqlens decreasing, past total_tokens or longer than
- * max_seqlen, or a seq_len that does not fit its chunk or block table) and, if
- * `clear` != 0, resets it.
+ * max_seqlen, or a seq_len that does not fit its chunk or block table; 6 = a
+ * step's lengths do not fit its block table or token count, or its free pages
+ * are used up; 7 = a position outside the rotation table; 8 = a cache slot
+ * past the last page) and, if `clear` != 0, resets it.
  */
 attn_status_t attn_device_status(uint32_t* code, int clear);
 

@@ -15,6 +15,9 @@ Modules:
                 the Triton, FlashAttention-2, XQA and TensorRT-LLM decode
                 algorithms, under float32 or exact arithmetic, and the
                 FlashAttention-2 split-count heuristic.
+  step       -- the serving step around the attention calls: tables from request
+                lengths, query/key norm with rotation, the 4-bit cache's number
+                format and record layout.
 
 Parity status: every function here is pinned by closed forms, invariants,
 brute force on tiny inputs or values the pages print (see tests/).
