@@ -6,10 +6,12 @@
 // or (16 + c, exact, its nibble on the upper mantissa bits), and scales and zero points are applied
 // to the 16 scores of a page's token tile and to its 16 probabilities, not to the d values of a token.
 //
-// S = Q K^T has the query heads of a KV head as rows (up to 8 a tile) and tokens as columns; its
-// accumulator layout is that of the right-hand operand of O^T = V^T P^T, so the probabilities go from
-// one product to the next in registers.  p s is split into two bf16 numbers (16 bits together): one
-// alone would add an error as large as the output's own rounding.
+// Both products have the codes as the left operand, S^T = K Q^T and O^T = V^T P^T: their four registers
+// are the decoded words themselves, and 8 columns hold the query heads of a KV head.  With up to four
+// heads the columns take the heads of two pages, so that one step's scores, exponentials and
+// roundings serve both.  p s is split into two bf16 numbers (16 bits together): one alone would add an
+// error as large as the output's own rounding.  Odd tokens of V enter as c - 31 (one exclusive-or
+// instead of the or), so that the offsets of the codes cancel in the running sums.
 //
 // Work: the (sequence, KV head, page) list is cut into equal contiguous shares, one a CTA; the CTA's
 // warps deal its pages among themselves, each with its own ring of bulk copies (a record is one
@@ -34,36 +36,48 @@ namespace {
 using q4::PAGE;
 using q4::Record;
 
-constexpr int TILE = 8;  // query heads a tile
-constexpr float RESCALE_LOG2_THRESHOLD = 8.0f;
 constexpr float LN2 = 0.693147180559945309f;
+constexpr int ROWS = 8;                       // score columns of a warp: query heads, or heads of two pages
 constexpr uint32_t CODE_MASK = 0x00780078u;   // a nibble on mantissa bits 3..6 of both halves
-constexpr uint32_t CODE_MAGIC = 0x41804180u;  // 16.0: with the nibble, 16 + c
-constexpr int MIN_SHARE = 8;                  // pages a CTA takes at least
+constexpr uint32_t K_MAGIC = 0x41804180u;     // 16 + c in both halves
+constexpr uint32_t V_MAGIC = 0xc1f84180u;     // 16 + c in the lower half (an even token), c - 31 in the upper one
+constexpr float P_LIMIT = 256.f;              // a probability above it moves the reference maximum
+constexpr uint32_t Z_MASK = 0x00780000u;      // a zero point on the same bits of a float: 16 + z, z - 31
+constexpr uint32_t Z_EVEN = 0x41800000u, Z_ODD = 0xc1f80000u;
+constexpr int MIN_SHARE = 8;                  // steps a CTA takes at least
 
-template <int D>
+// P: pages a warp takes at a step; ROWS / P query heads.
+template <int D, int P>
 struct Cfg {
-  static constexpr int NW = D == 256 ? 6 : 8;     // warps a CTA
-  static constexpr int NS = D == 256 ? 2 : 3;     // records in flight a warp
-  static constexpr int CTAS = 2;                  // CTAs an SM
-  static constexpr int STAGE = (Record<D>::BYTES + 127) & ~127;
-  static constexpr int OROW = D + 8;              // floats of a head's row in the merge buffer
-  static constexpr int MERGE = 2 * TILE + TILE * OROW;  // floats a warp: m, l, o
-  static constexpr int MERGE_OFF = NW * NS * STAGE;
+  static constexpr int NW = D < 256 ? 7 : P == 2 ? 4 : 5;  // warps that compute (one more loads)
+  static constexpr int NS = D == 256 ? 3 : D == 128 ? 3 : 4;  // pages in flight a warp
+  static constexpr int CTAS = 2;                   // CTAs an SM
+  static constexpr int THREADS = (NW + 1) * 32;
+  static constexpr int TILE = ROWS / P;            // query heads a tile
+  static constexpr int DEPTH = P == 2 ? 2 : NS;    // steps in flight a warp
+  static constexpr int SLOTS = NW * DEPTH;
+  static constexpr int STAGE = (P * Record<D>::BYTES + 127) & ~127;
+  static constexpr int OROW = D + 8;               // floats of a row in the merge buffer
+  static constexpr int MERGE = 2 * ROWS + ROWS * OROW;  // floats a warp: m, l, o
+  static constexpr int MERGE_OFF = SLOTS * STAGE;
   static constexpr int BAR_OFF = MERGE_OFF + NW * MERGE * 4;
-  static constexpr int ALLOC = BAR_OFF + NW * NS * 8;
+  static constexpr int ALLOC = BAR_OFF + 2 * SLOTS * 8;
   static_assert(CTAS * (ALLOC + 1024 + 256) <= 228 * 1024, "shared memory budget");
+  static_assert(CTAS * THREADS * (D == 256 ? 168 : 128) <= 65536, "register budget");
 };
 
 struct Q4Geometry {
   int grid, tiles, units;  // CTAs, head tiles a KV head, (KV head, tile) pairs a sequence
+  // K_MAGIC and V_MAGIC as arguments: a constant that the compiler knows would not stay in a register,
+  // and decoding a word half would take two instructions
+  uint32_t k_magic, v_magic;
 };
 
 // What the workspace holds: the shares' descriptors, then the partials' o, m and l.
 struct Workspace {
   int4* desc;    // [grid]: (sequence, unit, last share, 1) of the cut sequence that starts in share b, or w = 0
-  float* o;      // [2 grid][TILE][d]: index 2 b: continued from the share before, 2 b + 1: starts here
-  float *m, *l;  // [2 grid][TILE]
+  float* o;      // [2 grid][ROWS][d]: index 2 b: continued from the share before, 2 b + 1: starts here
+  float *m, *l;  // [2 grid][ROWS]
 };
 
 template <int D>
@@ -71,8 +85,8 @@ __device__ Workspace carve(void* ws, int grid) {
   Workspace w;
   w.desc = static_cast<int4*>(ws);
   w.o = reinterpret_cast<float*>(w.desc + grid);
-  w.m = w.o + static_cast<size_t>(2) * grid * TILE * D;
-  w.l = w.m + static_cast<size_t>(2) * grid * TILE;
+  w.m = w.o + static_cast<size_t>(2) * grid * ROWS * D;
+  w.l = w.m + static_cast<size_t>(2) * grid * ROWS;
   return w;
 }
 
@@ -84,55 +98,101 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// (w & CODE_MASK) ^ magic
+__device__ __forceinline__ uint32_t decode(uint32_t w, uint32_t magic) {
+  uint32_t x;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(x) : "r"(w), "n"(CODE_MASK), "r"(magic));
+  return x;
+}
+
+// transposes an 8 x 8 tile of 16-bit values held as an accumulator's pairs
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 __device__ __forceinline__ int clamped_len(const int32_t* lens, int n, int max_blocks) {
   const int L = lens[n];
   return L < 0 ? 0 : (L > max_blocks * PAGE ? max_blocks * PAGE : L);
 }
-__device__ __forceinline__ int pages_of(const int32_t* lens, int n, int max_blocks) {
-  return (clamped_len(lens, n, max_blocks) + PAGE - 1) / PAGE;
+// steps of P pages of sequence n
+template <int P>
+__device__ __forceinline__ int steps_of(const int32_t* lens, int n, int max_blocks) {
+  return (clamped_len(lens, n, max_blocks) + P * PAGE - 1) / (P * PAGE);
 }
 
-// Position in the (sequence, unit, page) list.
+// Position in the (sequence, unit, step) list.
+template <int P>
 struct Cursor {
-  int n, u, page, np;
-  __device__ __forceinline__ void advance(int step, const int32_t* lens, int N, int units, int max_blocks) {
-    page += step;
-    while (page >= np) {
-      page -= np;
+  int n, u, step, ns;
+  __device__ __forceinline__ void advance(int by, const int32_t* lens, int N, int units, int max_blocks) {
+    step += by;
+    while (step >= ns) {
+      step -= ns;
       if (++u == units) {
         u = 0;
         do {
           if (++n >= N) {  // past the end of the list: nothing there is read
             n = N;
-            np = 0x7fffffff;
+            ns = 0x7fffffff;
             return;
           }
-          np = pages_of(lens, n, max_blocks);
-        } while (np == 0);
+          ns = steps_of<P>(lens, n, max_blocks);
+        } while (ns == 0);
       }
     }
   }
 };
 
-template <int D>
-__global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS)
+// The 16-bit parameter words of a token's groups.
+template <int NG>
+struct Params {
+  static constexpr int WORDS = (NG + 1) / 2;
+  uint32_t w[WORDS];
+  __device__ __forceinline__ void load(const uint8_t* at) {
+    if constexpr (NG == 1) {
+      w[0] = *reinterpret_cast<const uint16_t*>(at);
+    } else if constexpr (NG == 2) {
+      w[0] = *reinterpret_cast<const uint32_t*>(at);
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(at);
+      w[0] = x.x; w[1] = x.y;
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ float scale(int e) const {
+    return __uint_as_float((e % 2 ? w[e / 2] : w[e / 2] << 16) & 0xfff00000u);
+  }
+  // the zero point z as `magic` makes a float of it: 16 + z or z - 31
+  __device__ __forceinline__ float zero(int e, uint32_t magic) const {
+    return __uint_as_float(((e % 2 ? w[e / 2] << 3 : w[e / 2] << 19) & Z_MASK) ^ magic);
+  }
+};
+
+template <int D, int P>
+__global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
     decode_q4_kernel(const DecodeQ4Params p, const Q4Geometry geo) {
-  using C = Cfg<D>;
+  using C = Cfg<D, P>;
   using R = Record<D>;
-  constexpr int NW = C::NW, NS = C::NS, NG = R::NG, THREADS = NW * 32;
+  constexpr int NW = C::NW, NG = R::NG, THREADS = C::THREADS, TILE = C::TILE, SLOTS = C::SLOTS;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_warp[NW];
+  __shared__ long long s_warp[NW + 1];
   __shared__ long long s_before;
   __shared__ int s_n;
   float* merge = reinterpret_cast<float*>(smem + C::MERGE_OFF);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* empty = full + SLOTS;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int N = p.N, G = p.Hq / p.Hkv, units = geo.units;
 
-  // ---- total pages, and the sequence that holds this share's first page
-  if (lane == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(&bars[warp * NS + i], 1);
+  // ---- total steps, and the sequence that holds this share's first one
+  if (threadIdx.x < SLOTS) {
+    mbar_init(&full[threadIdx.x], 1);
+    mbar_init(&empty[threadIdx.x], 1);
     fence_mbar_init();
   }
   const int chunk = (N + THREADS - 1) / THREADS;
@@ -142,7 +202,7 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS)
   for (int n = n_lo; n < n_hi; ++n) {
     const int L = p.seq_lens[n];
     if (blockIdx.x == 0 && (L < 0 || L > p.max_blocks * PAGE)) set_error(&g_decode_q4_status, kDevBadSplit);
-    mine += pages_of(p.seq_lens, n, p.max_blocks);
+    mine += steps_of<P>(p.seq_lens, n, p.max_blocks);
   }
   long long incl = mine;
 #pragma unroll
@@ -154,7 +214,7 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS)
   __syncthreads();
   long long total = 0;
 #pragma unroll
-  for (int i = 0; i < NW; ++i) {
+  for (int i = 0; i < NW + 1; ++i) {
     if (i < warp) incl += s_warp[i];
     total += s_warp[i];
   }
@@ -163,13 +223,13 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS)
   shares = shares < 1 ? 1 : (shares > geo.grid ? geo.grid : shares);
   const int b = blockIdx.x;
   const long long lo = b < shares ? b * W / shares : W, hi = b < shares ? (b + 1) * W / shares : W;
-  const int npg = static_cast<int>(hi - lo);
+  const int count = static_cast<int>(hi - lo);  // steps of this share
   const long long before_mine = (incl - mine) * units;
-  if (npg > 0 && before_mine <= lo && lo < incl * units) {
+  if (count > 0 && before_mine <= lo && lo < incl * units) {
     long long at = before_mine;
     int n = n_lo;
     for (;; ++n) {
-      const long long w = static_cast<long long>(pages_of(p.seq_lens, n, p.max_blocks)) * units;
+      const long long w = static_cast<long long>(steps_of<P>(p.seq_lens, n, p.max_blocks)) * units;
       if (lo < at + w) break;
       at += w;
     }
@@ -188,262 +248,303 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS)
   // every CTA of this grid is resident: the combine's CTAs may queue up behind them
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Workspace ws = carve<D>(p.workspace, geo.grid);
-  if (npg <= 0) {
+  if (count <= 0) {
     if (threadIdx.x == 0) ws.desc[b] = make_int4(0, 0, 0, 0);
     return;
   }
 
-  Cursor cur;  // the share's first page, then each segment's
+  Cursor<P> cur;  // the share's first step
   cur.n = s_n;
-  cur.np = pages_of(p.seq_lens, cur.n, p.max_blocks);
+  cur.ns = steps_of<P>(p.seq_lens, cur.n, p.max_blocks);
   const long long rel = lo - s_before;
-  cur.u = static_cast<int>(rel / cur.np);
-  cur.page = static_cast<int>(rel % cur.np);
+  cur.u = static_cast<int>(rel / cur.ns);
+  cur.step = static_cast<int>(rel % cur.ns);
 
-  // ---- this warp's ring: page i of the share belongs to warp i % NW
-  uint8_t* stages = smem + warp * NS * C::STAGE;
-  uint64_t* my_bars = bars + warp * NS;
-  const int n_my = npg > warp ? (npg - warp + NW - 1) / NW : 0;
-  Cursor icur = cur;
-  if (warp > 0) icur.advance(warp, p.seq_lens, N, units, p.max_blocks);
-  int pid = 0;  // physical page at icur, fetched one page ahead of its use
-  auto fetch_pid = [&](int k) {
-    if (k < n_my) pid = p.block_table[static_cast<int64_t>(icur.n) * p.max_blocks + icur.page];
-  };
-  auto issue = [&](int k) {
-    int id = pid;
-    if (id < 0 || id >= p.num_blocks) {
-      set_error(&g_decode_q4_status, kDevBadPage);
-      id = 0;
+  if (warp == NW) {
+    // ---------------------------------------------------------- loads
+    // Step i goes to slot i % SLOTS and to computing warp i % NW.  Each lane finds the records of one
+    // of 32 steps (its table entries are read together with the other lanes'), then NW lanes at a
+    // time wait for their slots and request their records, one copy a record.
+    constexpr int ROUND = 32 / NW * NW;
+    bool ok = true;
+    int last = -1;   // this lane's last step whose copy was requested
+    cur.advance(lane, p.seq_lens, N, units, p.max_blocks);
+    for (int base = 0; base < count; base += ROUND) {
+      const int i = base + lane;
+      const bool live = lane < ROUND && i < count;
+      const uint8_t* src[P];
+      int pages = 0;
+      if (live) {
+        const int len = clamped_len(p.seq_lens, cur.n, p.max_blocks);
+        const int32_t* row = p.block_table + static_cast<int64_t>(cur.n) * p.max_blocks + cur.step * P;
+#pragma unroll
+        for (int a = 0; a < P; ++a) {
+          if ((cur.step * P + a) * PAGE >= len) continue;
+          int id = row[a];
+          if (id < 0 || id >= p.num_blocks) {
+            set_error(&g_decode_q4_status, kDevBadPage);
+            id = 0;
+          }
+          src[a] = p.cache + (static_cast<int64_t>(id) * p.Hkv + cur.u / geo.tiles) * R::BYTES;
+          ++pages;
+        }
+      }
+#pragma unroll 1
+      for (int from = 0; from < ROUND && base + from < count; from += NW) {
+        if (live && lane >= from && lane < from + NW) {
+          const int slot = i % SLOTS;
+          if (ok) ok = mbar_wait(&empty[slot], (i / SLOTS & 1) ^ 1);
+          if (ok) {
+            mbar_arrive_expect_tx(&full[slot], pages * R::BYTES);
+            bulk_load(smem + slot * C::STAGE, src[0], R::BYTES, &full[slot]);
+            if (P == 2 && pages == 2) bulk_load(smem + slot * C::STAGE + R::BYTES, src[P - 1], R::BYTES, &full[slot]);
+            last = i;
+          }
+        }
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (!ok) break;
+      cur.advance(ROUND, p.seq_lens, N, units, p.max_blocks);
     }
-    mbar_arrive_expect_tx(&my_bars[k % NS], R::BYTES);
-    bulk_load(stages + k % NS * C::STAGE,
-              p.cache + (static_cast<int64_t>(id) * p.Hkv + icur.u / geo.tiles) * R::BYTES, R::BYTES, &my_bars[k % NS]);
-    icur.advance(NW, p.seq_lens, N, units, p.max_blocks);
-    fetch_pid(k + 1);
-  };
-  if (lane == 0) {
-    fetch_pid(0);
-    for (int k = 0; k < n_my && k < NS; ++k) issue(k);
+    if (!ok) set_error(&g_decode_q4_status, kDevWaitTimeout);
+    // Copies in flight must land before the CTA's shared memory is given back.  Only a slot's newest
+    // copy is of the phase that its barrier is in; an older one was waited for before the newer left.
+    static_assert(ROUND >= SLOTS, "a lane has at most one step among the newest of the slots");
+    const int end = __reduce_max_sync(0xffffffffu, last) + 1;
+    if (last >= 0 && last >= end - SLOTS) mbar_wait(&full[last % SLOTS], last / SLOTS & 1);
+    return;
   }
-  __syncwarp();
 
+  // ------------------------------------------------------------ attention
+  const int g = lane >> 2, t = lane & 3;
+  const int q_row = P == 2 ? g & 3 : g;     // the query head of the tile that this lane loads: column g
+  const int my_page = P == 2 ? t >> 1 : 0;  // columns 2 t and 2 t + 1 are two heads of this page of the step
+  const uint32_t z_magic = g & 1 ? Z_ODD : Z_EVEN;  // of tokens g and g + 8 of V
   const float c2 = p.scale_log2;
   bool ok = true;
-  int k = 0;       // pages this warp has taken
-  int landed = 0;  // of which the copy was seen to land
-  int i = warp;    // share index of its next page
+  int i = warp;    // share index of this warp's next step
   int4 cut = make_int4(0, 0, 0, 0);
-  for (int seg = 0; seg < npg;) {
-    const int seg_n = cur.n, seg_u = cur.u, first_page = cur.page;
-    const int seg_pages = cur.np - first_page < npg - seg ? cur.np - first_page : npg - seg;
-    const int seg_end = seg + seg_pages;
+  for (int seg = 0; seg < count;) {
+    const int seg_n = cur.n, seg_u = cur.u, first_step = cur.step;
+    const int seg_steps = cur.ns - first_step < count - seg ? cur.ns - first_step : count - seg;
+    const int seg_end = seg + seg_steps;
     const int len = clamped_len(p.seq_lens, seg_n, p.max_blocks);
     const int kvh = seg_u / geo.tiles, h0 = seg_u % geo.tiles * TILE;
     const int heads = G - h0 < TILE ? G - h0 : TILE;
     const __nv_bfloat16* q_head = p.q + (static_cast<int64_t>(seg_n) * p.Hq + kvh * G + h0) * D;
 
-    // ---- queries: row g of the tile; channels 64 e + 16 t + 8 h .. + 7, paired as the K words pair them
-    uint32_t qa[NG][2][4];
-    float qsum[NG];
+    // ---- queries: channels 64 e + 16 t + 8 h .. + 7, paired as the K words pair them
+    uint32_t qb[NG][2][4];
+    float nqsum[NG][2];  // minus the sum over a group, of columns 2 t and 2 t + 1
 #pragma unroll
     for (int e = 0; e < NG; ++e) {
-      qsum[e] = 0.f;
+      float sum = 0.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (g < heads) x = *reinterpret_cast<const uint4*>(q_head + g * D + 64 * e + 16 * t + 8 * h);
-        qa[e][h][0] = __byte_perm(x.x, x.z, 0x5410);  // channels 0, 4
-        qa[e][h][1] = __byte_perm(x.x, x.z, 0x7632);  // 1, 5
-        qa[e][h][2] = __byte_perm(x.y, x.w, 0x5410);  // 2, 6
-        qa[e][h][3] = __byte_perm(x.y, x.w, 0x7632);  // 3, 7
+        if (q_row < heads) x = *reinterpret_cast<const uint4*>(q_head + q_row * D + 64 * e + 16 * t + 8 * h);
+        qb[e][h][0] = __byte_perm(x.x, x.z, 0x5410);  // channels 0, 4
+        qb[e][h][1] = __byte_perm(x.x, x.z, 0x7632);  // 1, 5
+        qb[e][h][2] = __byte_perm(x.y, x.w, 0x5410);  // 2, 6
+        qb[e][h][3] = __byte_perm(x.y, x.w, 0x7632);  // 3, 7
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) qsum[e] += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xffff0000u);
+        for (int j = 0; j < 4; ++j) sum -= __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xffff0000u);
       }
-      qsum[e] += __shfl_xor_sync(0xffffffffu, qsum[e], 1);
-      qsum[e] += __shfl_xor_sync(0xffffffffu, qsum[e], 2);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      nqsum[e][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
+      nqsum[e][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
     }
 
-    float m = -INFINITY, l = 0.f;  // of head g: raw-score max that o and l refer to, this lane's share of the sum
-    float o[D / 16][4];            // channels 16 i + 2 g (0, 1) and + 1 (2, 3) of heads 2 t and 2 t + 1
-    float base[NG];                // sum of p s (16 + z) of head g over this lane's tokens
+    float mc[2] = {-1e38f, -1e38f};  // of columns 2 t, 2 t + 1: the reference maximum, in log2 units
+    float l[2] = {0.f, 0.f};         // this lane's share of the sum of probabilities
+    float base[NG][2];               // sum of p s (16 + z) or p s (z - 31) over this lane's tokens
+    float o[D / 16][4];              // channels 16 i + 2 g (0, 1) and + 1 (2, 3) of columns 2 t and 2 t + 1
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
 #pragma unroll
-    for (int e = 0; e < NG; ++e) base[e] = 0.f;
-    bool first = true;
+    for (int e = 0; e < NG; ++e) base[e][0] = base[e][1] = 0.f;
 
-    for (; i < seg_end; i += NW, ++k) {
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&my_bars[k % NS], (k / NS) & 1));
+    for (; i < seg_end; i += NW) {
+      const int slot = i % SLOTS;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], i / SLOTS & 1));
       if (!ok) continue;
-      landed = k + 1;
-      const uint8_t* rec = stages + k % NS * C::STAGE;
-      const int token0 = (first_page + i - seg) * PAGE;
-      const int valid = len - token0 < PAGE ? len - token0 : PAGE;
+      const uint8_t* stage = smem + slot * C::STAGE;
+      const uint8_t* mine_rec = stage + my_page * R::BYTES;
+      // tokens of this lane's page that the sequence has; the last step's second page may have none
+      const int valid = len - ((first_step + i - seg) * P + my_page) * PAGE;
 
-      // ---- S: tokens 2 t, 2 t + 1 (tile 0) and + 8 (tile 1) of head g; K words of tokens g and g + 8
-      float sc[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+      // ---- S^T: rows are tokens g (0, 1) and g + 8 (2, 3), columns 2 t and 2 t + 1
+      float sc[4] = {0.f, 0.f, 0.f, 0.f};
+      Params<NG> kp[2], vp[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        kp[j].load(mine_rec + R::KP_OFF + (g + 8 * j) * (2 * NG));
+        vp[j].load(mine_rec + R::VP_OFF + (g + 8 * j) * (2 * NG));
+      }
 #pragma unroll
       for (int pr = 0; pr < NG / R::PAIR; ++pr) {
-        uint32_t kw[2][2 * R::PAIR];
+        float acc[R::PAIR][P][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const uint8_t* row = rec + R::K_OFF + (g + 8 * nt) * (D / 2) + pr * (32 * R::PAIR) + t * (8 * R::PAIR);
-          if constexpr (R::PAIR == 2) {
-            const uint4 x = *reinterpret_cast<const uint4*>(row);
-            kw[nt][0] = x.x; kw[nt][1] = x.y; kw[nt][2] = x.z; kw[nt][3] = x.w;
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(row);
-            kw[nt][0] = x.x; kw[nt][1] = x.y;
+        for (int a = 0; a < P; ++a) {
+          uint32_t kw[2][2 * R::PAIR];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint8_t* row =
+                stage + a * R::BYTES + R::K_OFF + (g + 8 * j) * (D / 2) + pr * (32 * R::PAIR) + t * (8 * R::PAIR);
+            if constexpr (R::PAIR == 2) {
+              const uint4 x = *reinterpret_cast<const uint4*>(row);
+              kw[j][0] = x.x; kw[j][1] = x.y; kw[j][2] = x.z; kw[j][3] = x.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(row);
+              kw[j][0] = x.x; kw[j][1] = x.y;
+            }
+          }
+#pragma unroll
+          for (int ee = 0; ee < R::PAIR; ++ee) {
+            const int e = pr * R::PAIR + ee;
+            acc[ee][a][0] = acc[ee][a][1] = acc[ee][a][2] = acc[ee][a][3] = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t w0 = kw[0][ee * 2 + h], w1 = kw[1][ee * 2 + h];
+              mma_16816(acc[ee][a], decode(w0, geo.k_magic), decode(w1, geo.k_magic),
+                        decode(__funnelshift_r(w0, w0, 4), geo.k_magic),
+                        decode(__funnelshift_r(w1, w1, 4), geo.k_magic), qb[e][h][0], qb[e][h][1]);
+              mma_16816(acc[ee][a], decode(__funnelshift_r(w0, w0, 8), geo.k_magic),
+                        decode(__funnelshift_r(w1, w1, 8), geo.k_magic),
+                        decode(__funnelshift_r(w0, w0, 12), geo.k_magic),
+                        decode(__funnelshift_r(w1, w1, 12), geo.k_magic), qb[e][h][2], qb[e][h][3]);
+            }
           }
         }
 #pragma unroll
         for (int ee = 0; ee < R::PAIR; ++ee) {
           const int e = pr * R::PAIR + ee;
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int j = 0; j < 2; ++j) {
+            const float s = kp[j].scale(e), z = kp[j].zero(e, Z_EVEN);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t w = kw[nt][ee * 2 + h];
-              const uint32_t b0 = (w & CODE_MASK) | CODE_MAGIC;
-              const uint32_t b1 = (__funnelshift_r(w, w, 4) & CODE_MASK) | CODE_MAGIC;
-              const uint32_t b2 = (__funnelshift_r(w, w, 8) & CODE_MASK) | CODE_MAGIC;
-              const uint32_t b3 = (__funnelshift_r(w, w, 12) & CODE_MASK) | CODE_MAGIC;
-              mma_16816(acc, qa[e][h][0], 0u, qa[e][h][1], 0u, b0, b1);
-              mma_16816(acc, qa[e][h][2], 0u, qa[e][h][3], 0u, b2, b3);
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t par =
-                  reinterpret_cast<const uint16_t*>(rec + R::KP_OFF)[(8 * nt + 2 * t + j) * NG + e];
-              const float s = __uint_as_float((par & 0xfff0u) << 16);
-              const float z16 = __uint_as_float(0x41800000u | (par & 15u) << 19);  // 16 + z
-              sc[nt][j] = fmaf(s, fmaf(-z16, qsum[e], acc[j]), sc[nt][j]);
+            for (int c = 0; c < 2; ++c) {
+              const float x = P == 2 && my_page ? acc[ee][P - 1][2 * j + c] : acc[ee][0][2 * j + c];
+              sc[2 * j + c] = fmaf(s, fmaf(z, nqsum[e][c], x), sc[2 * j + c]);
             }
           }
         }
       }
-      // ---- online softmax of row g
-      if (valid < PAGE) {
+      if (__any_sync(0xffffffffu, valid < PAGE)) {
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (8 * nt + 2 * t + j >= valid) sc[nt][j] = -INFINITY;
+        for (int j = 0; j < 2; ++j)
+          if (g + 8 * j >= valid) {
+            sc[2 * j] = sc[2 * j + 1] = -INFINITY;
+            vp[j].clear();  // whatever lies past the sequence is not to be multiplied with: 0 * NaN is not 0
+          }
       }
-      float mx = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      if (first) {
-        m = mx;
-        first = false;
-      } else {
-        const bool grow = (mx - m) * c2 > RESCALE_LOG2_THRESHOLD;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? ex2_approx((m - mx) * c2) : 1.f;
-          if (grow) m = mx;
-          l *= f;
+      // ---- online softmax against the reference; a probability past the limit moves it to the maximum
+      float pr[4];
 #pragma unroll
-          for (int e = 0; e < NG; ++e) base[e] *= f;
-          const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+      for (int x = 0; x < 4; ++x) pr[x] = ex2_approx(fmaf(sc[x], c2, -mc[x & 1]));
+      if (__any_sync(0xffffffffu, fmaxf(fmaxf(pr[0], pr[1]), fmaxf(pr[2], pr[3])) > P_LIMIT)) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float mx = fmaxf(sc[c], sc[2 + c]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float to = fmaxf(mc[c], mx * c2), f = ex2_approx(mc[c] - to);
+          mc[c] = to;
+          l[c] *= f;
+#pragma unroll
+          for (int e = 0; e < NG; ++e) base[e][c] *= f;
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {
-            o[x][0] *= f0; o[x][1] *= f1;
-            o[x][2] *= f0; o[x][3] *= f1;
+            o[x][c] *= f;
+            o[x][2 + c] *= f;
           }
+          pr[c] = ex2_approx(fmaf(sc[c], c2, -to));
+          pr[2 + c] = ex2_approx(fmaf(sc[2 + c], c2, -to));
         }
       }
-      const float mc = m * c2;
-      float pr[2][2];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          pr[nt][j] = ex2_approx(fmaf(sc[nt][j], c2, -mc));
-          l += pr[nt][j];
-        }
-      // ---- O^T += V^T (p s)^T
+      l[0] += pr[0] + pr[2];
+      l[1] += pr[1] + pr[3];
+      // ---- O^T += V^T (p s)^T.  A page's product takes its own columns' probabilities, zeros for the other's.
 #pragma unroll
       for (int e = 0; e < NG; ++e) {
-        uint32_t hi[2], lo_[2];
+        uint32_t ph[2], pl[2];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          float x[2];
+        for (int j = 0; j < 2; ++j) {
+          const float s = vp[j].scale(e), z = vp[j].zero(e, z_magic);
+          const float x0 = pr[2 * j] * s, x1 = pr[2 * j + 1] * s;
+          base[e][0] = fmaf(x0, z, base[e][0]);
+          base[e][1] = fmaf(x1, z, base[e][1]);
+          const uint32_t hi = pack_bf16x2(x0, x1);
+          ph[j] = transpose_8x8(hi);
+          pl[j] = transpose_8x8(
+              pack_bf16x2(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u)));
+        }
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int token = 8 * nt + 2 * t + j;
-            uint32_t par = reinterpret_cast<const uint16_t*>(rec + R::VP_OFF)[token * NG + e];
-            if (token >= valid) par = 0;  // whatever lies past the sequence: 0 * NaN is not 0
-            x[j] = pr[nt][j] * __uint_as_float((par & 0xfff0u) << 16);
-            base[e] = fmaf(x[j], __uint_as_float(0x41800000u | (par & 15u) << 19), base[e]);
+        for (int a = 0; a < P; ++a) {
+          const bool on = P == 1 || (g >> 2) == a;  // as an operand, this lane holds column g
+          const uint32_t h0_ = on ? ph[0] : 0u, h1_ = on ? ph[1] : 0u, l0_ = on ? pl[0] : 0u, l1_ = on ? pl[1] : 0u;
+          const uint4 vw = *reinterpret_cast<const uint4*>(stage + a * R::BYTES + R::V_OFF + (e * 32 + lane) * 16);
+          const uint32_t w4[4] = {vw.x, vw.y, vw.z, vw.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w = w4[j];
+            const uint32_t a0 = decode(w << 3, geo.v_magic), a1 = decode(w >> 1, geo.v_magic);
+            const uint32_t a2 = decode(w >> 5, geo.v_magic), a3 = decode(w >> 9, geo.v_magic);
+            mma_16816(o[e * 4 + j], a0, a1, a2, a3, h0_, h1_);
+            mma_16816(o[e * 4 + j], a0, a1, a2, a3, l0_, l1_);
           }
-          hi[nt] = pack_bf16x2(x[0], x[1]);
-          lo_[nt] = pack_bf16x2(x[0] - __uint_as_float(hi[nt] << 16), x[1] - __uint_as_float(hi[nt] & 0xffff0000u));
-        }
-        const uint4 vw = *reinterpret_cast<const uint4*>(rec + R::V_OFF + (e * 32 + lane) * 16);
-        const uint32_t w4[4] = {vw.x, vw.y, vw.z, vw.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t w = w4[j];
-          const uint32_t a0 = ((w << 3) & CODE_MASK) | CODE_MAGIC;
-          const uint32_t a1 = ((w >> 1) & CODE_MASK) | CODE_MAGIC;
-          const uint32_t a2 = ((w >> 5) & CODE_MASK) | CODE_MAGIC;
-          const uint32_t a3 = ((w >> 9) & CODE_MASK) | CODE_MAGIC;
-          mma_16816(o[e * 4 + j], a0, a1, a2, a3, hi[0], hi[1]);
-          mma_16816(o[e * 4 + j], a0, a1, a2, a3, lo_[0], lo_[1]);
         }
       }
       __syncwarp();
-      if (lane == 0 && k + NS < n_my) {
-        fence_proxy_async_smem();
-        issue(k + NS);
-      }
-      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[slot]);
     }
 
     // ---- this warp's state to shared memory, then the CTA's to global memory
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
 #pragma unroll
-    for (int e = 0; e < NG; ++e) {
-      base[e] += __shfl_xor_sync(0xffffffffu, base[e], 1);
-      base[e] += __shfl_xor_sync(0xffffffffu, base[e], 2);
-    }
-    float* my = merge + warp * C::MERGE;
-    if (t == 0) {
-      my[g] = first ? -INFINITY : m * c2;
-      my[TILE + g] = l;
-    }
+    for (int off = 4; off < 32; off <<= 1) {
 #pragma unroll
-    for (int e = 0; e < NG; ++e) {
-      const float b0 = __shfl_sync(0xffffffffu, base[e], 8 * t), b1 = __shfl_sync(0xffffffffu, base[e], 8 * t + 4);
+      for (int c = 0; c < 2; ++c) {
+        l[c] += __shfl_xor_sync(0xffffffffu, l[c], off);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int x = e * 4 + j;
-        float* at = my + 2 * TILE + 2 * t * C::OROW + 16 * x + 2 * g;
-        *reinterpret_cast<float2*>(at) = make_float2(o[x][0] - b0, o[x][2] - b0);
-        *reinterpret_cast<float2*>(at + C::OROW) = make_float2(o[x][1] - b1, o[x][3] - b1);
+        for (int e = 0; e < NG; ++e) base[e][c] += __shfl_xor_sync(0xffffffffu, base[e][c], off);
       }
     }
-    __syncthreads();
-    const bool starts = first_page == 0, ends = first_page + seg_pages == cur.np;
+    float* my = merge + warp * C::MERGE;
+    if (g == 0) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        my[2 * t + c] = l[c] == 0.f ? -INFINITY : mc[c];  // no tokens: no part in the maximum
+        my[ROWS + 2 * t + c] = l[c];
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < D / 16; ++x) {
+      float* at = my + 2 * ROWS + 2 * t * C::OROW + 16 * x + 2 * g;
+      *reinterpret_cast<float2*>(at) = make_float2(o[x][0] - base[x / 4][0], o[x][2] - base[x / 4][0]);
+      *reinterpret_cast<float2*>(at + C::OROW) = make_float2(o[x][1] - base[x / 4][1], o[x][3] - base[x / 4][1]);
+    }
+    named_barrier_sync(1, NW * 32);
+    const bool starts = first_step == 0, ends = first_step + seg_steps == cur.ns;
     const int64_t slot = 2 * b + (starts ? 1 : 0);
-    for (int w = threadIdx.x; w < heads * (D / 4); w += THREADS) {
+    for (int w = threadIdx.x; w < heads * (D / 4); w += NW * 32) {
       const int r = w / (D / 4), x = w % (D / 4) * 4;
       float M = -INFINITY;
 #pragma unroll
-      for (int v = 0; v < NW; ++v) M = fmaxf(M, merge[v * C::MERGE + r]);
+      for (int v = 0; v < NW * P; ++v) M = fmaxf(M, merge[v / P * C::MERGE + v % P * TILE + r]);
       float L = 0.f;
       float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int v = 0; v < NW; ++v) {
-        const float* src = merge + v * C::MERGE;
-        const float wl = src[TILE + r];
-        if (wl == 0.f) continue;  // a warp without pages
-        const float f = ex2_approx(src[r] - M);
-        const float4 y = *reinterpret_cast<const float4*>(src + 2 * TILE + r * C::OROW + x);
+      for (int v = 0; v < NW * P; ++v) {
+        const float* src = merge + v / P * C::MERGE;
+        const int vr = v % P * TILE + r;
+        const float wl = src[ROWS + vr];
+        if (wl == 0.f) continue;  // a row without tokens
+        const float f = ex2_approx(src[vr] - M);
+        const float4 y = *reinterpret_cast<const float4*>(src + 2 * ROWS + vr * C::OROW + x);
         L = fmaf(wl, f, L);
         O.x = fmaf(y.x, f, O.x); O.y = fmaf(y.y, f, O.y);
         O.z = fmaf(y.z, f, O.z); O.w = fmaf(y.w, f, O.w);
@@ -455,35 +556,34 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS)
         *reinterpret_cast<uint2*>(p.o + row * D + x) = make_uint2(pack_bf16x2(O.x, O.y), pack_bf16x2(O.z, O.w));
         if (x == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(L)) * LN2;
       } else {
-        *reinterpret_cast<float4*>(ws.o + (slot * TILE + r) * D + x) = O;
+        *reinterpret_cast<float4*>(ws.o + (slot * ROWS + r) * D + x) = O;
         if (x == 0) {
-          ws.m[slot * TILE + r] = M;
-          ws.l[slot * TILE + r] = L;
+          ws.m[slot * ROWS + r] = M;
+          ws.l[slot * ROWS + r] = L;
         }
       }
     }
     if (starts && !ends) {
-      // the share that holds the sequence's last page: unit x lies in share ((x + 1) shares - 1) / W
-      const long long past = lo + seg + cur.np;
+      // the share that holds the sequence's last step: step x lies in share ((x + 1) shares - 1) / W
+      const long long past = lo + seg + cur.ns;
       cut = make_int4(seg_n, seg_u, static_cast<int>((past * shares - 1) / W), 1);
     }
     seg = seg_end;
-    if (seg < npg) cur.advance(seg_pages, p.seq_lens, N, units, p.max_blocks);
-    __syncthreads();  // the merge buffer is free again
+    if (seg < count) {
+      cur.advance(seg_steps, p.seq_lens, N, units, p.max_blocks);
+      named_barrier_sync(1, NW * 32);  // the merge buffer is free again
+    }
   }
   if (threadIdx.x == 0) ws.desc[b] = cut;
-  if (!ok && lane == 0) {
-    set_error(&g_decode_q4_status, kDevWaitTimeout);
-    // copies in flight must land before the CTA's shared memory is given back
-    for (int j = landed; j < n_my && j < landed + NS; ++j) mbar_wait(&my_bars[j % NS], (j / NS) & 1);
-  }
+  if (!ok && lane == 0) set_error(&g_decode_q4_status, kDevWaitTimeout);
 }
 
 // One CTA a share: merges the partials of the cut sequence that starts there, if there is one.
 // RS groups of threads take every RS-th partial.
-template <int D>
+template <int D, int P>
 __global__ void __launch_bounds__(1024) combine_q4_kernel(const DecodeQ4Params p, const Q4Geometry geo) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int TILE = ROWS / P;
   constexpr int COLS = TILE * D / 4;  // threads that cover the outputs, 4 columns each
   constexpr int RS = 1024 / COLS;
   __shared__ float4 s_o[RS > 1 ? RS - 1 : 1][COLS];
@@ -498,7 +598,7 @@ __global__ void __launch_bounds__(1024) combine_q4_kernel(const DecodeQ4Params p
   const int first = blockIdx.x;
   const int count = d.z - first + 1;
   // partial j: the cut sequence's start, then the shares that continue it
-  auto slot_of = [&](int j) { return static_cast<int64_t>(j == 0 ? 2 * first + 1 : 2 * (first + j)) * TILE + r; };
+  auto slot_of = [&](int j) { return static_cast<int64_t>(j == 0 ? 2 * first + 1 : 2 * (first + j)) * ROWS + r; };
   float M = -INFINITY, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
   if (r < heads) {
@@ -535,24 +635,28 @@ __global__ void __launch_bounds__(1024) combine_q4_kernel(const DecodeQ4Params p
   if (x == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(L)) * LN2;
 }
 
-int grid_of_device(int d) {
+// CTAs of the grid: every SM filled (the same count for each variant)
+int grid_of_device() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return sms * (d == 64 ? Cfg<64>::CTAS : d == 128 ? Cfg<128>::CTAS : Cfg<256>::CTAS);
+  return sms * Cfg<128, 1>::CTAS;
 }
 
-template <int D>
+template <int D, int P>
 cudaError_t launch(const DecodeQ4Params& p, cudaStream_t stream) {
+  using C = Cfg<D, P>;
   Q4Geometry geo;
-  geo.grid = grid_of_device(D);
+  geo.grid = grid_of_device();
   if (geo.grid <= 0) return cudaErrorInvalidDevice;
-  geo.tiles = (p.Hq / p.Hkv + TILE - 1) / TILE;
+  geo.tiles = (p.Hq / p.Hkv + C::TILE - 1) / C::TILE;
   geo.units = p.Hkv * geo.tiles;
-  auto kern = decode_q4_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::ALLOC);
+  geo.k_magic = K_MAGIC;
+  geo.v_magic = V_MAGIC;
+  auto kern = decode_q4_kernel<D, P>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
   if (e != cudaSuccess) return e;
-  kern<<<geo.grid, Cfg<D>::NW * 32, Cfg<D>::ALLOC, stream>>>(p, geo);
+  kern<<<geo.grid, C::THREADS, C::ALLOC, stream>>>(p, geo);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -563,20 +667,25 @@ cudaError_t launch(const DecodeQ4Params& p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_q4_kernel<D>, p, geo);
+  return cudaLaunchKernelEx(&cfg, combine_q4_kernel<D, P>, p, geo);
+}
+
+template <int D>
+cudaError_t launch_for(const DecodeQ4Params& p, cudaStream_t stream) {
+  return p.Hq / p.Hkv <= ROWS / 2 ? launch<D, 2>(p, stream) : launch<D, 1>(p, stream);
 }
 
 }  // namespace
 
 size_t decode_q4_workspace_bytes(int d) {
-  const size_t grid = static_cast<size_t>(grid_of_device(d));
-  return grid * 16 + 2 * grid * TILE * (static_cast<size_t>(d) + 2) * sizeof(float);
+  const size_t grid = static_cast<size_t>(grid_of_device());
+  return grid * 16 + 2 * grid * ROWS * (static_cast<size_t>(d) + 2) * sizeof(float);
 }
 
 cudaError_t decode_q4_launch(int d, const DecodeQ4Params& p, cudaStream_t stream) {
-  if (d == 64) return launch<64>(p, stream);
-  if (d == 128) return launch<128>(p, stream);
-  if (d == 256) return launch<256>(p, stream);
+  if (d == 64) return launch_for<64>(p, stream);
+  if (d == 128) return launch_for<128>(p, stream);
+  if (d == 256) return launch_for<256>(p, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -363,12 +363,18 @@ def _check_decode(o, lse, q, lens, k, v, scale, what=""):
     ([0, 33, 0, 0, 1], 8, 2, 128), ([127, 128, 129, 130], 8, 8, 128), ([1009], 32, 8, 128), ([1000, 3], 5, 1, 128),
     ([300, 77], 16, 2, 256), ([4100], 8, 1, 256), ([500], 11, 1, 64), ([700, 20], 32, 2, 128), ([90], 17, 1, 256),
     ([60] * 40, 4, 2, 128), ([5] * 700, 2, 1, 64), ([9000, 1, 250], 6, 2, 64), ([20000], 4, 1, 128),
+    ([40000, 100, 30000], 16, 4, 64), ([30000, 20001], 8, 2, 128), ([9000] * 9, 8, 1, 128), ([20000], 8, 4, 256),
 ])
 def test_decode_q4(attn, gpu, lens, Hq, Hkv, d):
     cache, table, sl, k, v = _filled(attn, lens, Hkv, d, 3 + d, gpu)
     q = _randn((len(lens), Hq, d), 7, gpu)
     scale = 1 / math.sqrt(d)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in "ab")
+    start.record()
     o, lse = attn.decode_paged_q4(q, cache, table, sl)
+    end.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(end) < 500                      # no wait ran into its limit of 2 s
     _check_decode(o, lse, q, lens, k, v, scale, f"{lens[:4]} {Hq}/{Hkv} d={d}")
     again, lse2 = attn.decode_paged_q4(q, cache, table, sl)
     assert torch.equal(o, again) and torch.equal(lse, lse2)
