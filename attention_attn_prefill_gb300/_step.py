@@ -7,7 +7,6 @@ pointers.  A call runs on the device its tensors live on, on that device's curre
 """
 from __future__ import annotations
 
-import math
 from typing import NamedTuple
 
 import torch
@@ -17,53 +16,61 @@ from ._lib import PAGE_TOKENS, _check, lib
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 
 
-def _ptr(t: torch.Tensor, dtype, name: str, device) -> int:
-    """Pointer of a dense tensor on the call's device."""
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+# A call here takes a few microseconds on the GPU, about what the interpreter needs for it, so the checks
+# are one expression a call over the tensors that were given; _explain finds which of them failed.
+_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream().cuda_stream without the Stream object
+_current_device = torch._C._cuda_getDevice
+_entry = {}
 
 
-def _device(t, name: str):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+def _explain(dev: int, *tensors) -> None:
+    """Raises for the first of (tensor, dtype, name) that is not a dense tensor of its type on the call's device."""
+    for t, dtype, name in tensors:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a tensor")
+        if dev < 0:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on cuda:{dev}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{tensors[0][2]} has another shape or device than the call needs")
 
 
-def _rows(t: torch.Tensor, name: str, device) -> tuple[int, int]:
-    """(pointer, token stride) of bf16 rows [T, H, d] whose heads are dense."""
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype != _BF16:
-        raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
+def _stride(t: torch.Tensor, name: str, dev: int) -> int:
+    """Token stride of bf16 rows [T, H, d] whose heads are dense."""
+    if t.dtype is not _BF16 or t.get_device() != dev:
+        _explain(dev, (t, _BF16, name))
     T, H, d = t.shape
     token, head, channel = t.stride()
     if channel != 1 or (head != d and H > 1):
         raise ValueError(f"the heads of a token of {name} must be dense")
-    return t.data_ptr(), token if T > 1 else H * d
+    return token if T > 1 else H * d
 
 
-def _run(fn: str, device, stream, args, made=()) -> None:
-    """Calls the C entry point with the stream appended, with `device` current."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _run(fn, device, stream, args, made)
+def _run(fn: str, dev: int, stream, made, *args) -> None:
+    """Calls the C entry point with the stream appended, with device `dev` current."""
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return _run(fn, dev, stream, made, *args)
+    call = _entry.get(fn)
+    if call is None:
+        call = _entry[fn] = getattr(lib(), fn)
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
-    elif hasattr(stream, "cuda_stream"):
-        handle = stream.cuda_stream
-    else:
-        handle = int(stream)
-    _check(getattr(lib(), fn)(*args, handle), fn)
-    if stream is not None:
-        # memory allocated here belongs to the current stream: it may not be reused before `stream` is done
-        on = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=device)
-        for t in made:
-            t.record_stream(on)
+        status = call(*args, _raw_stream(dev))
+        if status:
+            _check(status, fn)
+        return
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    _check(call(*args, handle), fn)
+    # memory allocated here belongs to the current stream: it may not be reused before `stream` is done
+    on = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=dev)
+    for t in made:
+        t.record_stream(on)
 
 
 class StepTables(NamedTuple):
@@ -79,24 +86,34 @@ def step_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: t
                 stream=None) -> StepTables:
     """Tables of one serving step from request lengths [N]; `block_table` [N, max_blocks] is extended in
     place by pages from the front of `free_pages`.  All int32.  `num_tokens` >= sum(new_lens)."""
-    device = _device(cached_lens, "cached_lens")
-    N = cached_lens.numel()
+    dev, N = cached_lens.get_device(), cached_lens.numel()
+    if (dev < 0 or new_lens.get_device() != dev or free_pages.get_device() != dev or block_table.get_device() != dev
+            or cached_lens.dtype is not _I32 or new_lens.dtype is not _I32 or free_pages.dtype is not _I32
+            or block_table.dtype is not _I32 or not cached_lens.is_contiguous() or not new_lens.is_contiguous()
+            or not free_pages.is_contiguous() or not block_table.is_contiguous()):
+        _explain(dev, (cached_lens, _I32, "cached_lens"), (new_lens, _I32, "new_lens"),
+                 (free_pages, _I32, "free_pages"), (block_table, _I32, "block_table"))
     if cached_lens.dim() != 1 or new_lens.shape != (N,) or free_pages.dim() != 1:
         raise ValueError("cached_lens and new_lens must be [N], free_pages [num_free]")
     if block_table.dim() != 2 or block_table.shape[0] != N:
         raise ValueError("block_table must be [N, max_blocks]")
     made = ()
     if out is None:
-        buf = torch.empty(2 * num_tokens + 2 * N + 2, dtype=_I32, device=device)  # one allocation for all five
-        out = StepTables(*buf.split([N, N + 1, num_tokens, num_tokens, 1]))
-        made = (buf,)
-    elif [t.shape for t in out] != [(N,), (N + 1,), (num_tokens,), (num_tokens,), (1,)]:
-        raise ValueError("out must have the shapes of StepTables for these lengths")
-    args = [_ptr(cached_lens, _I32, "cached_lens", device), _ptr(new_lens, _I32, "new_lens", device),
-            _ptr(free_pages, _I32, "free_pages", device), _ptr(block_table, _I32, "block_table", device),
-            *(_ptr(t, _I32, "out", device) for t in out), N, int(num_tokens), free_pages.numel(), PAGE_TOKENS,
-            block_table.shape[1], int(num_blocks)]
-    _run("attn_step_tables", device, stream, args, made)
+        made = (torch.empty(2 * (num_tokens + N + 1), dtype=_I32, device=dev),)  # one allocation for all five
+        sl = made[0].data_ptr()
+        cu, pos = sl + 4 * N, sl + 4 * (2 * N + 1)
+        slots = pos + 4 * num_tokens
+        used = slots + 4 * num_tokens
+        out = StepTables(*torch.split_with_sizes(made[0], (N, N + 1, num_tokens, num_tokens, 1)))
+    else:
+        if [t.shape for t in out] != [(N,), (N + 1,), (num_tokens,), (num_tokens,), (1,)]:
+            raise ValueError("out must have the shapes of StepTables for these lengths")
+        if any(t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous() for t in out):
+            _explain(dev, *((t, _I32, "out") for t in out))
+        sl, cu, pos, slots, used = (t.data_ptr() for t in out)
+    _run("attn_step_tables", dev, stream, made, cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
+         block_table.data_ptr(), sl, cu, pos, slots, used, N, num_tokens, free_pages.numel(), PAGE_TOKENS,
+         block_table.shape[1], num_blocks)
     return out
 
 
@@ -106,7 +123,7 @@ def rope_table(max_positions: int, rot: int, theta: float = 10000.0, device=None
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
     table = torch.empty((max_positions, rot), dtype=_F32, device=device)
-    _run("attn_rope_table", device, stream, [table.data_ptr(), int(max_positions), int(rot), float(theta)], (table,))
+    _run("attn_rope_table", device.index, stream, (table,), table.data_ptr(), max_positions, rot, float(theta))
     return table
 
 
@@ -122,31 +139,54 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor | Non
     of 8).  With k_cache and v_cache [num_blocks,16,Hkv,d], v and slots [T], K and V are written to the
     paged cache as well; k_out is then None unless given.  q_out and k_out may be q and k themselves.
     """
-    device = _device(q, "q")
+    dev = q.get_device()
     T, Hq, d = q.shape
     Hkv = k.shape[1]
-    if k.shape != (T, Hkv, d):
-        raise ValueError("k must be [T, Hkv, d] matching q")
+    qs, ks = _stride(q, "q", dev), _stride(k, "k", dev)
+    if dev < 0 or k.shape != (T, Hkv, d):
+        raise ValueError("q must be a CUDA tensor [T, Hq, d] and k [T, Hkv, d]")
     paged = k_cache is not None or v_cache is not None
     made = []
     if q_out is None:
-        q_out = torch.empty((T, Hq, d), dtype=_BF16, device=device)
+        q_out, qos = torch.empty((T, Hq, d), dtype=_BF16, device=dev), Hq * d
         made.append(q_out)
+    else:
+        qos = _stride(q_out, "q_out", dev)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+    kop = kos = 0
     if k_out is None and not paged:
-        k_out = torch.empty((T, Hkv, d), dtype=_BF16, device=device)
+        k_out, kos = torch.empty((T, Hkv, d), dtype=_BF16, device=dev), Hkv * d
         made.append(k_out)
-    if q_out.shape != q.shape or (k_out is not None and k_out.shape != k.shape):
-        raise ValueError("q_out and k_out must have the shapes of q and k")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and w.shape != (d,):
-            raise ValueError(f"{name} must be [d]")
-    rot = max_positions = 0
+        kop = k_out.data_ptr()
+    elif k_out is not None:
+        kop, kos = k_out.data_ptr(), _stride(k_out, "k_out", dev)
+        if k_out.shape != k.shape:
+            raise ValueError("k_out must have the shape of k")
+    qwp = kwp = 0
+    if q_weight is not None:
+        if q_weight.dtype is not _BF16 or q_weight.get_device() != dev or not q_weight.is_contiguous():
+            _explain(dev, (q_weight, _BF16, "q_weight"))
+        if q_weight.shape != (d,):
+            raise ValueError("q_weight must be [d]")
+        qwp = q_weight.data_ptr()
+    if k_weight is not None:
+        if k_weight.dtype is not _BF16 or k_weight.get_device() != dev or not k_weight.is_contiguous():
+            _explain(dev, (k_weight, _BF16, "k_weight"))
+        if k_weight.shape != (d,):
+            raise ValueError("k_weight must be [d]")
+        kwp = k_weight.data_ptr()
+    rot = max_positions = pp = tp = 0
     if table is not None:
         if table.dim() != 2 or positions is None or positions.shape != (T,):
             raise ValueError("table must be [max_positions, rot] and positions [T]")
+        if (positions.dtype is not _I32 or table.dtype is not _F32 or positions.get_device() != dev
+                or table.get_device() != dev or not positions.is_contiguous() or not table.is_contiguous()):
+            _explain(dev, (positions, _I32, "positions"), (table, _F32, "table"))
         max_positions, rot = table.shape
+        pp, tp = positions.data_ptr(), table.data_ptr()
     num_blocks, page = 0, PAGE_TOKENS
-    vp = (None, 0)
+    vptr = vs = kcp = vcp = sp = 0
     if paged:
         if v is None or slots is None or k_cache is None or v_cache is None:
             raise ValueError("writing to a cache takes v, slots, k_cache and v_cache")
@@ -155,18 +195,15 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor | Non
             raise ValueError("caches must be [num_blocks, page, Hkv, d] matching k")
         if v.shape != k.shape or slots.shape != (T,):
             raise ValueError("v must have the shape of k and slots be [T]")
-        vp = _rows(v, "v", device)
-    args = [*_rows(q, "q", device), *_rows(k, "k", device), *vp,
-            None if q_weight is None else _ptr(q_weight, _BF16, "q_weight", device),
-            None if k_weight is None else _ptr(k_weight, _BF16, "k_weight", device), float(eps),
-            None if table is None else _ptr(positions, _I32, "positions", device),
-            None if table is None else _ptr(table, _F32, "table", device), max_positions, rot,
-            1 if interleaved else 0, *_rows(q_out, "q_out", device),
-            *((None, 0) if k_out is None else _rows(k_out, "k_out", device)),
-            *((_ptr(k_cache, _BF16, "k_cache", device), _ptr(v_cache, _BF16, "v_cache", device),
-               _ptr(slots, _I32, "slots", device)) if paged else (None, None, None)),
-            T, Hq, Hkv, d, page, num_blocks]
-    _run("attn_qk_norm_rope", device, stream, args, made)
+        vptr, vs = v.data_ptr(), _stride(v, "v", dev)
+        if (slots.dtype is not _I32 or k_cache.dtype is not _BF16 or v_cache.dtype is not _BF16
+                or slots.get_device() != dev or k_cache.get_device() != dev or v_cache.get_device() != dev
+                or not slots.is_contiguous() or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+            _explain(dev, (k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache"), (slots, _I32, "slots"))
+        kcp, vcp, sp = k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr()
+    _run("attn_qk_norm_rope", dev, stream, made, q.data_ptr(), qs, k.data_ptr(), ks, vptr, vs, qwp, kwp, eps, pp, tp,
+         max_positions, rot, 1 if interleaved else 0, q_out.data_ptr(), qos, kop, kos, kcp, vcp, sp, T, Hq, Hkv, d,
+         page, num_blocks)
     return q_out, k_out
 
 
@@ -178,58 +215,80 @@ def cache_q4_empty(num_blocks: int, Hkv: int, d: int, device=None) -> torch.Tens
     return torch.zeros((num_blocks, Hkv, size), dtype=_U8, device="cuda" if device is None else device)
 
 
-def _cache(cache: torch.Tensor, d: int, device) -> tuple[int, int, int]:
-    """(pointer, num_blocks, Hkv) of a 4-bit cache."""
-    if not isinstance(cache, torch.Tensor) or cache.dim() != 3 or cache.shape[2] != 17 * d:
-        raise ValueError("cache must be [num_blocks, Hkv, 17 d]")
-    return _ptr(cache, _U8, "cache", device), cache.shape[0], cache.shape[1]
-
-
 def cache_append_q4(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, stream=None) -> None:
     """Writes k, v [T,Hkv,d] bf16 (heads dense, any token stride that is a multiple of 8) into the 4-bit
     cache at slots [T] int32 (negative: not written)."""
-    device = _device(cache, "cache")
+    dev = cache.get_device()
+    if (dev < 0 or cache.dtype is not _U8 or slots.dtype is not _I32 or slots.get_device() != dev
+            or not cache.is_contiguous() or not slots.is_contiguous()):
+        _explain(dev, (cache, _U8, "cache"), (slots, _I32, "slots"))
     T, Hkv, d = k.shape
-    ptr, num_blocks, heads = _cache(cache, d, device)
-    if heads != Hkv or v.shape != k.shape or slots.shape != (T,):
-        raise ValueError("k and v must be [T, Hkv, d] with the cache's Hkv, and slots [T]")
-    args = [*_rows(k, "k", device), *_rows(v, "v", device), _ptr(slots, _I32, "slots", device), ptr, T, Hkv, d,
-            PAGE_TOKENS, num_blocks]
-    _run("attn_cache_append_q4", device, stream, args)
+    if cache.dim() != 3 or cache.shape[1:] != (Hkv, 17 * d):
+        raise ValueError("cache must be [num_blocks, Hkv, 17 d] matching k")
+    if v.shape != k.shape or slots.shape != (T,):
+        raise ValueError("k and v must be [T, Hkv, d] and slots [T]")
+    _run("attn_cache_append_q4", dev, stream, (), k.data_ptr(), _stride(k, "k", dev), v.data_ptr(),
+         _stride(v, "v", dev), slots.data_ptr(), cache.data_ptr(), T, Hkv, d, PAGE_TOKENS, cache.shape[0])
 
 
-def _paged(cache, block_table, seq_lens, d, device):
-    ptr, num_blocks, Hkv = _cache(cache, d, device)
-    N = seq_lens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != N or seq_lens.dim() != 1:
+def _check_paged(dev, d, cache, block_table, seq_lens, N):
+    """(num_blocks, Hkv, max_blocks) of a 4-bit cache and the tables that address it."""
+    if (dev < 0 or cache.dtype is not _U8 or block_table.dtype is not _I32 or seq_lens.dtype is not _I32
+            or cache.get_device() != dev or block_table.get_device() != dev or seq_lens.get_device() != dev
+            or not cache.is_contiguous() or not block_table.is_contiguous() or not seq_lens.is_contiguous()):
+        _explain(dev, (cache, _U8, "cache"), (block_table, _I32, "block_table"), (seq_lens, _I32, "seq_lens"))
+    if cache.dim() != 3 or cache.shape[2] != 17 * d:
+        raise ValueError("cache must be [num_blocks, Hkv, 17 d]")
+    if block_table.dim() != 2 or block_table.shape[0] != N or seq_lens.shape != (N,):
         raise ValueError("block_table must be [N, max_blocks] and seq_lens [N]")
-    return (ptr, _ptr(block_table, _I32, "block_table", device), _ptr(seq_lens, _I32, "seq_lens", device), N, Hkv,
-            block_table.shape[1], num_blocks)
+    num_blocks, Hkv, _ = cache.shape
+    return num_blocks, Hkv, block_table.shape[1]
 
 
 def cache_gather_q4(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
                     k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, stream=None):
     """Reads sequences back: (k, v) [N, max_blocks * 16, Hkv, d] bf16; rows behind a sequence's end are
     left as they were (uninitialised if allocated here)."""
-    device = _device(cache, "cache")
-    if cache.dim() != 3 or cache.shape[2] % 17:
-        raise ValueError("cache must be [num_blocks, Hkv, 17 d]")
-    d = cache.shape[2] // 17
-    cp, bt, sl, N, Hkv, max_blocks, num_blocks = _paged(cache, block_table, seq_lens, d, device)
+    dev, N = cache.get_device(), seq_lens.numel()
+    d = cache.shape[-1] // 17
+    num_blocks, Hkv, max_blocks = _check_paged(dev, d, cache, block_table, seq_lens, N)
     shape = (N, max_blocks * PAGE_TOKENS, Hkv, d)
     made = []
     if k_out is None:
-        k_out = torch.empty(shape, dtype=_BF16, device=device)
+        k_out = torch.empty(shape, dtype=_BF16, device=dev)
         made.append(k_out)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=_BF16, device=device)
+        v_out = torch.empty(shape, dtype=_BF16, device=dev)
         made.append(v_out)
     if k_out.shape != shape or v_out.shape != shape:
         raise ValueError("k_out and v_out must be [N, max_blocks * 16, Hkv, d]")
-    args = [cp, bt, sl, _ptr(k_out, _BF16, "k_out", device), _ptr(v_out, _BF16, "v_out", device), N, Hkv, d,
-            PAGE_TOKENS, max_blocks, num_blocks]
-    _run("attn_cache_gather_q4", device, stream, args, made)
+    if (k_out.dtype is not _BF16 or v_out.dtype is not _BF16 or k_out.get_device() != dev
+            or v_out.get_device() != dev or not k_out.is_contiguous() or not v_out.is_contiguous()):
+        _explain(dev, (k_out, _BF16, "k_out"), (v_out, _BF16, "v_out"))
+    _run("attn_cache_gather_q4", dev, stream, made, cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+         k_out.data_ptr(), v_out.data_ptr(), N, Hkv, d, PAGE_TOKENS, max_blocks, num_blocks)
     return k_out, v_out
+
+
+def _outputs(dev, q, out, lse, lse_shape, return_lse, workspace, need, made):
+    """(out, lse, workspace), allocated where not given."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=_BF16, device=dev)
+        made.append(out)
+    elif out.shape != q.shape or out.dtype is not _BF16 or out.get_device() != dev or not out.is_contiguous():
+        _explain(dev, (out, _BF16, "out (of q's shape)"))
+    if lse is not None:
+        if lse.shape != lse_shape or lse.dtype is not _F32 or lse.get_device() != dev or not lse.is_contiguous():
+            _explain(dev, (lse, _F32, f"lse (of shape {list(lse_shape)})"))
+    elif return_lse:
+        lse = torch.empty(lse_shape, dtype=_F32, device=dev)
+        made.append(lse)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=_U8, device=dev)
+        made.append(workspace)
+    elif workspace.dtype is not _U8 or workspace.get_device() != dev or not workspace.is_contiguous():
+        _explain(dev, (workspace, _U8, "workspace"))
+    return out, lse, workspace
 
 
 _decode_ws: dict[tuple[int, int], int] = {}
@@ -237,7 +296,9 @@ _decode_ws: dict[tuple[int, int], int] = {}
 
 def decode_q4_workspace_bytes(d: int, device=None) -> int:
     """Bytes of workspace decode_paged_q4 needs on a device (the current one if not given)."""
-    index = torch.cuda.current_device() if device is None or device.index is None else device.index
+    index = device if isinstance(device, int) else None if device is None else torch.device(device).index
+    if index is None:
+        index = torch.cuda.current_device()
     if (index, d) not in _decode_ws:
         with torch.cuda.device(index):
             _decode_ws[index, d] = int(lib().attn_decode_q4_workspace_bytes(d))
@@ -248,28 +309,17 @@ def decode_paged_q4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
                     scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                     return_lse: bool = True, workspace: torch.Tensor | None = None, stream=None):
     """Single-token attention over the 4-bit cache: q [N,Hq,d] bf16 -> (o [N,Hq,d], lse [N,Hq])."""
-    device = _device(q, "q")
+    dev = q.get_device()
     N, Hq, d = q.shape
-    cp, bt, sl, num_seqs, Hkv, max_blocks, num_blocks = _paged(cache, block_table, seq_lens, d, device)
-    if num_seqs != N:
-        raise ValueError("seq_lens must be [N] matching q")
+    num_blocks, Hkv, max_blocks = _check_paged(dev, d, cache, block_table, seq_lens, N)
+    if q.dtype is not _BF16 or not q.is_contiguous():
+        _explain(dev, (q, _BF16, "q"))
     made = []
-    if out is None:
-        out = torch.empty((N, Hq, d), dtype=_BF16, device=device)
-        made.append(out)
-    if lse is None and return_lse:
-        lse = torch.empty((N, Hq), dtype=_F32, device=device)
-        made.append(lse)
-    if out.shape != q.shape or (lse is not None and lse.shape != (N, Hq)):
-        raise ValueError("out must be [N, Hq, d] and lse [N, Hq]")
-    if workspace is None:
-        workspace = torch.empty(decode_q4_workspace_bytes(d, device), dtype=_U8, device=device)
-        made.append(workspace)
-    args = [_ptr(q, _BF16, "q", device), cp, bt, sl, _ptr(out, _BF16, "out", device),
-            None if lse is None else _ptr(lse, _F32, "lse", device), N, Hq, Hkv, d, PAGE_TOKENS, max_blocks,
-            num_blocks, 1.0 / math.sqrt(d) if scale is None else float(scale),
-            _ptr(workspace, _U8, "workspace", device), workspace.numel()]
-    _run("attn_decode_paged_q4", device, stream, args, made)
+    out, lse, workspace = _outputs(dev, q, out, lse, (N, Hq), return_lse, workspace,
+                                   _decode_ws.get((dev, d)) or decode_q4_workspace_bytes(d, dev), made)
+    _run("attn_decode_paged_q4", dev, stream, made, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
+         seq_lens.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), N, Hq, Hkv, d, PAGE_TOKENS,
+         max_blocks, num_blocks, d ** -0.5 if scale is None else scale, workspace.data_ptr(), workspace.numel())
     return out, lse
 
 
@@ -283,27 +333,20 @@ def prefill_paged_q4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
                      workspace: torch.Tensor | None = None, stream=None):
     """Chunked prefill over the 4-bit cache: new tokens q [T,Hq,d] (their K/V already appended) against
     all cached tokens of their sequences -> (o [T,Hq,d], lse [Hq,T])."""
-    device = _device(q, "q")
+    dev, N = q.get_device(), seq_lens.numel()
     T, Hq, d = q.shape
-    cp, bt, sl, N, Hkv, max_blocks, num_blocks = _paged(cache, block_table, seq_lens, d, device)
+    num_blocks, Hkv, max_blocks = _check_paged(dev, d, cache, block_table, seq_lens, N)
+    if q.dtype is not _BF16 or not q.is_contiguous():
+        _explain(dev, (q, _BF16, "q"))
+    if cu_seqlens_q.dtype is not _I32 or cu_seqlens_q.get_device() != dev or not cu_seqlens_q.is_contiguous():
+        _explain(dev, (cu_seqlens_q, _I32, "cu_seqlens_q"))
     if cu_seqlens_q.shape != (N + 1,):
         raise ValueError("cu_seqlens_q must be [N + 1]")
     made = []
-    if out is None:
-        out = torch.empty((T, Hq, d), dtype=_BF16, device=device)
-        made.append(out)
-    if lse is None and return_lse:
-        lse = torch.empty((Hq, T), dtype=_F32, device=device)
-        made.append(lse)
-    if out.shape != q.shape or (lse is not None and lse.shape != (Hq, T)):
-        raise ValueError("out must be [T, Hq, d] and lse [Hq, T]")
-    if workspace is None:
-        workspace = torch.empty(max(1, prefill_q4_workspace_bytes(N, Hkv, d, max_blocks)), dtype=_U8, device=device)
-        made.append(workspace)
-    args = [_ptr(q, _BF16, "q", device), cp, bt, _ptr(cu_seqlens_q, _I32, "cu_seqlens_q", device), sl,
-            _ptr(out, _BF16, "out", device), None if lse is None else _ptr(lse, _F32, "lse", device), N,
-            int(max_seqlen_q), T, Hq, Hkv, d, PAGE_TOKENS, max_blocks, num_blocks,
-            1.0 / math.sqrt(d) if scale is None else float(scale), 1 if causal else 0,
-            _ptr(workspace, _U8, "workspace", device), workspace.numel()]
-    _run("attn_prefill_paged_q4", device, stream, args, made)
+    out, lse, workspace = _outputs(dev, q, out, lse, (Hq, T), return_lse, workspace,
+                                   max(1, prefill_q4_workspace_bytes(N, Hkv, d, max_blocks)), made)
+    _run("attn_prefill_paged_q4", dev, stream, made, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
+         cu_seqlens_q.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), N,
+         max_seqlen_q, T, Hq, Hkv, d, PAGE_TOKENS, max_blocks, num_blocks, d ** -0.5 if scale is None else scale,
+         1 if causal else 0, workspace.data_ptr(), workspace.numel())
     return out, lse

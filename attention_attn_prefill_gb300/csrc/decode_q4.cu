@@ -44,7 +44,6 @@ constexpr uint32_t V_MAGIC = 0xc1f84180u;     // 16 + c in the lower half (an ev
 constexpr float P_LIMIT = 256.f;              // a probability above it moves the reference maximum
 constexpr uint32_t Z_MASK = 0x00780000u;      // a zero point on the same bits of a float: 16 + z, z - 31
 constexpr uint32_t Z_EVEN = 0x41800000u, Z_ODD = 0xc1f80000u;
-constexpr int MIN_SHARE = 8;                  // steps a CTA takes at least
 
 // P: pages a warp takes at a step; ROWS / P query heads.
 template <int D, int P>
@@ -65,6 +64,14 @@ struct Cfg {
   static_assert(CTAS * (ALLOC + 1024 + 256) <= 228 * 1024, "shared memory budget");
   static_assert(CTAS * THREADS * (D == 256 ? 168 : 128) <= 65536, "register budget");
 };
+
+// a * b / c with c > 0; the quotient is below 2^63.  64-bit division costs over a hundred instructions,
+// and the shares of all but the largest batches are counted in 32 bits.
+__device__ __forceinline__ long long mul_div(long long a, long long b, long long c) {
+  const long long n = a * b;
+  if ((n | c) >> 32 == 0) return static_cast<uint32_t>(n) / static_cast<uint32_t>(c);
+  return n / c;
+}
 
 struct Q4Geometry {
   int grid, tiles, units;  // CTAs, head tiles a KV head, (KV head, tile) pairs a sequence
@@ -219,10 +226,10 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
     total += s_warp[i];
   }
   const long long W = total * units;
-  long long shares = W / MIN_SHARE;
-  shares = shares < 1 ? 1 : (shares > geo.grid ? geo.grid : shares);
+  // at least a step for each warp of a share
+  const long long shares = W >= static_cast<long long>(geo.grid) * NW ? geo.grid : W < NW ? 1 : static_cast<int>(W) / NW;
   const int b = blockIdx.x;
-  const long long lo = b < shares ? b * W / shares : W, hi = b < shares ? (b + 1) * W / shares : W;
+  const long long lo = b < shares ? mul_div(b, W, shares) : W, hi = b < shares ? mul_div(b + 1, W, shares) : W;
   const int count = static_cast<int>(hi - lo);  // steps of this share
   const long long before_mine = (incl - mine) * units;
   if (count > 0 && before_mine <= lo && lo < incl * units) {
@@ -257,8 +264,8 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
   cur.n = s_n;
   cur.ns = steps_of<P>(p.seq_lens, cur.n, p.max_blocks);
   const long long rel = lo - s_before;
-  cur.u = static_cast<int>(rel / cur.ns);
-  cur.step = static_cast<int>(rel % cur.ns);
+  cur.u = static_cast<int>(mul_div(rel, 1, cur.ns));
+  cur.step = static_cast<int>(rel - static_cast<long long>(cur.u) * cur.ns);
 
   if (warp == NW) {
     // ---------------------------------------------------------- loads
@@ -566,7 +573,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
     if (starts && !ends) {
       // the share that holds the sequence's last step: step x lies in share ((x + 1) shares - 1) / W
       const long long past = lo + seg + cur.ns;
-      cut = make_int4(seg_n, seg_u, static_cast<int>((past * shares - 1) / W), 1);
+      cut = make_int4(seg_n, seg_u, static_cast<int>(mul_div(past * shares - 1, 1, W)), 1);
     }
     seg = seg_end;
     if (seg < count) {
