@@ -104,7 +104,7 @@ def step_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: t
         cu, pos = sl + 4 * N, sl + 4 * (2 * N + 1)
         slots = pos + 4 * num_tokens
         used = slots + 4 * num_tokens
-        out = StepTables(*torch.split_with_sizes(made[0], (N, N + 1, num_tokens, num_tokens, 1)))
+        out = StepTables(*torch.unsafe_split_with_sizes(made[0], (N, N + 1, num_tokens, num_tokens, 1)))
     else:
         if [t.shape for t in out] != [(N,), (N + 1,), (num_tokens,), (num_tokens,), (1,)]:
             raise ValueError("out must have the shapes of StepTables for these lengths")

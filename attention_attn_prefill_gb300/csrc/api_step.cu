@@ -102,6 +102,9 @@ attn_status_t attn_qk_norm_rope(const void* q, long long q_stride, const void* k
   if (rot < 0 || rot > d) return ATTN_ERR_INVALID_ARG;
   if (rot % 16 != 0) return ATTN_ERR_UNSUPPORTED;
   if (rot > 0 && (!given(positions, 4) || !given(table, 16) || max_positions < 1)) return ATTN_ERR_INVALID_ARG;
+  // the kernel numbers its threads, one for 32 values, in 32 bits
+  if (static_cast<int64_t>(num_tokens) * ((Hq + 3) / 4 + 2 * ((Hkv + 3) / 4)) * (d / 8) >= (int64_t(1) << 31))
+    return ATTN_ERR_INVALID_ARG;
   const bool paged = k_cache != nullptr || v_cache != nullptr;
   if (!paged && k_out == nullptr) return ATTN_ERR_INVALID_ARG;
   if (paged) {

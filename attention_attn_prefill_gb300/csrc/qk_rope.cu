@@ -6,15 +6,18 @@
 // from a float32 table.  Everything is computed in float32 and rounded to bf16 once.
 //
 // Bound by HBM: 2 bytes in and 2 bytes out a value, a few flops each.  A thread holds 8 consecutive
-// channels (16 bytes), d / 8 threads a row, so a row's sum of squares is a few shuffles.  With pairs
-// (i, i + rot / 2) a thread's partners are 8 channels of another thread of the row: the four words
-// of raw bf16 pairs are exchanged, not eight float32 results, since the partner's norm factor is the
-// row's.  A thread keeps its cosines and sines in registers over the rows (heads) of a token.
+// channels (16 bytes) of a row and d / 8 threads a row, so a row's sum of squares is a few shuffles.
+// Such a group takes ROWS rows (heads) of one token, whose loads are all in flight before the first
+// is used: one load a thread would leave 16 KB an SM in flight, a third of what HBM needs.  With
+// a = w cos of its own channels and b = +-w' sin of their partners', both made once for the rows of a
+// kind, an output is r (x a + y b), r the row's norm factor.  With pairs (i, i + rot / 2) the partners
+// are 8 channels of another thread of the row, exchanged as four words of raw bf16 pairs.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
+#include "prefill.h"  // FastDiv
 #include "sm103.cuh"
 #include "step.h"
 
@@ -25,130 +28,162 @@ __device__ uint32_t g_qk_rope_status;
 namespace {
 
 constexpr int THREADS = 256;
+constexpr int ROWS = 4;  // rows a group of threads takes, their loads in flight together
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+// eight bf16 values as four pairs of floats
+__device__ __forceinline__ void unpack8(const uint4& u, uint64_t (&x)[4]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint32_t pack2(uint64_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  return pack_bf16x2(a, b);
 }
 
-// A CTA takes THREADS / (D / 8) / lanes tokens; `lanes` groups of D / 8 threads share a token and walk
-// its rows (query heads, key heads, and value heads where they are copied to the cache).
-template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(THREADS) qk_rope_kernel(const QkRopeParams p, int lanes) {
+__device__ __forceinline__ uint64_t f2_swap(uint64_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  return f2_pack(b, a);
+}
+
+// Group gid (D / 8 threads) takes part gid % parts of token gid / parts: up to ROWS query heads in the
+// first q_parts parts, key heads in the next k_parts, value heads (copied to the cache) in the rest.
+// NORM: there is a weight for queries or keys.
+template <int D, bool INTERLEAVED, bool NORM>
+__global__ void __launch_bounds__(THREADS)
+    qk_rope_kernel(const QkRopeParams p, int q_parts, int k_parts, uint32_t parts, FastDiv div_parts) {
   constexpr int LPR = D / 8;  // threads a row
   const int sub = threadIdx.x % LPR;
-  const int grp = threadIdx.x / LPR;
-  const int tokens = THREADS / LPR / lanes;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * tokens + grp / lanes;
-  // whole groups fall out together; the shuffles below name the LPR threads of a row only
-  if (grp / lanes >= tokens || t >= p.T) return;
+  const uint32_t gid = (blockIdx.x * THREADS + threadIdx.x) / LPR;
+  const uint32_t token = div_parts.div(gid);
+  if (token >= static_cast<uint32_t>(p.T)) return;  // whole groups fall out together
+  const int64_t t = token;
+  const int part = static_cast<int>(gid - token * parts);
   const int row_lane0 = threadIdx.x & 31 & ~(LPR - 1);
   const unsigned row_mask = LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u) << row_lane0;
-  const int rows = p.Hq + p.Hkv * (p.v_cache != nullptr ? 2 : 1);
-
-  int64_t slot = -1;
-  if (p.k_cache != nullptr) {
-    slot = p.slots[t];
-    if (slot >= p.num_slots) {
-      if (grp % lanes == 0 && sub == 0) set_error(&g_qk_rope_status, kDevBadSlot);
-      slot = -1;
-    }
-  }
   const int c0 = sub * 8;
+  const bool is_q = part < q_parts, is_v = part >= q_parts + k_parts;
+  const int h0 = (is_q ? part : is_v ? part - q_parts - k_parts : part - q_parts) * ROWS;
+  const int n = min(ROWS, (is_q ? p.Hq : p.Hkv) - h0);
+  const __nv_bfloat16* src =
+      (is_q ? p.q + t * p.q_stride : is_v ? p.v + t * p.v_stride : p.k + t * p.k_stride) + h0 * D + c0;
   const bool turns = c0 < p.rot;
+  int pos = turns && !is_v ? p.positions[t] : 0;
+  int64_t slot = !is_q && p.k_cache != nullptr ? p.slots[t] : -1;
+
+  uint4 raw[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (i < n) raw[i] = __ldcs(reinterpret_cast<const uint4*>(src + i * D));
+  }
+  if (slot >= p.num_slots) {
+    if (h0 == 0 && sub == 0) set_error(&g_qk_rope_status, kDevBadSlot);
+    slot = -1;
+  }
+  __nv_bfloat16* cache = nullptr;
+  if (slot >= 0) cache = (is_v ? p.v_cache : p.k_cache) + (slot * p.Hkv + h0) * D + c0;
+  if (is_v) {
+    if (cache != nullptr) {
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i)
+        if (i < n) *reinterpret_cast<uint4*>(cache + i * D) = raw[i];
+    }
+    return;
+  }
+  __nv_bfloat16* out = is_q ? p.q_out + t * p.q_out_stride + h0 * D + c0
+                            : p.k_out != nullptr ? p.k_out + t * p.k_out_stride + h0 * D + c0 : nullptr;
+
+  // an output is r (x * own + y * other), y the partner channel's value
   const int half = p.rot / 2;
-  float cs[INTERLEAVED ? 4 : 8], sn[INTERLEAVED ? 4 : 8];
+  const int partner = INTERLEAVED || !turns ? sub : (c0 < half ? sub + half / 8 : sub - half / 8);
+  uint64_t own[4], other[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    own[j] = f2_pack(1.f, 1.f);
+    other[j] = f2_pack(0.f, 0.f);
+  }
   if (turns) {
-    int pos = p.positions[t];
     if (pos < 0 || pos >= p.max_positions) {
-      if (grp % lanes == 0 && sub == 0) set_error(&g_qk_rope_status, kDevBadPosition);
+      if (h0 == 0 && sub == 0) set_error(&g_qk_rope_status, kDevBadPosition);
       pos = pos < 0 ? 0 : p.max_positions - 1;
     }
     const int pair = INTERLEAVED ? c0 / 2 : (c0 < half ? c0 : c0 - half);
     const float* row = p.table + static_cast<int64_t>(pos) * p.rot + pair;
+    if constexpr (INTERLEAVED) {
+      const float4 c = *reinterpret_cast<const float4*>(row), s = *reinterpret_cast<const float4*>(row + half);
+      own[0] = f2_pack(c.x, c.x); own[1] = f2_pack(c.y, c.y); own[2] = f2_pack(c.z, c.z); own[3] = f2_pack(c.w, c.w);
+      other[0] = f2_pack(-s.x, s.x); other[1] = f2_pack(-s.y, s.y);
+      other[2] = f2_pack(-s.z, s.z); other[3] = f2_pack(-s.w, s.w);
+    } else {
+      const float sign = c0 < half ? -1.f : 1.f;
+      const uint64_t sign2 = f2_pack(sign, sign);
 #pragma unroll
-    for (int i = 0; i < (INTERLEAVED ? 1 : 2); ++i) {
-      const float4 a = reinterpret_cast<const float4*>(row)[i];
-      const float4 b = reinterpret_cast<const float4*>(row + half)[i];
-      cs[4 * i] = a.x; cs[4 * i + 1] = a.y; cs[4 * i + 2] = a.z; cs[4 * i + 3] = a.w;
-      sn[4 * i] = b.x; sn[4 * i + 1] = b.y; sn[4 * i + 2] = b.z; sn[4 * i + 3] = b.w;
+      for (int i = 0; i < 2; ++i) {
+        const float4 c = reinterpret_cast<const float4*>(row)[i], s = reinterpret_cast<const float4*>(row + half)[i];
+        own[2 * i] = f2_pack(c.x, c.y); own[2 * i + 1] = f2_pack(c.z, c.w);
+        other[2 * i] = f2_mul(f2_pack(s.x, s.y), sign2); other[2 * i + 1] = f2_mul(f2_pack(s.z, s.w), sign2);
+      }
     }
   }
-  // the thread of the row that holds the other halves of this thread's pairs
-  const int partner = !turns ? sub : (c0 < half ? sub + half / 8 : sub - half / 8);
-
-  for (int r = grp % lanes; r < rows; r += lanes) {
-    const bool is_q = r < p.Hq, is_v = r >= p.Hq + p.Hkv;
-    const int h = is_q ? r : (is_v ? r - p.Hq - p.Hkv : r - p.Hq);
-    const __nv_bfloat16* src = is_q ? p.q + t * p.q_stride : (is_v ? p.v + t * p.v_stride : p.k + t * p.k_stride);
-    const uint4 raw = *reinterpret_cast<const uint4*>(src + h * D + c0);
-    const int64_t cache_at = (slot * p.Hkv + h) * D + c0;
-    if (is_v) {
-      if (slot >= 0) *reinterpret_cast<uint4*>(p.v_cache + cache_at) = raw;
-      continue;
-    }
-    float x[8];
-    unpack8(raw, x);
-    const __nv_bfloat16* weight = is_q ? p.q_weight : p.k_weight;
-    float inv = 1.f;
-    if (weight != nullptr) {
-      float ss = 0.f;
+  const __nv_bfloat16* weight = is_q ? p.q_weight : p.k_weight;
+  if (NORM && weight != nullptr) {
+    uint64_t w[4], v[4];
+    unpack8(*reinterpret_cast<const uint4*>(weight + c0), w);
+    if constexpr (INTERLEAVED) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+      for (int j = 0; j < 4; ++j) v[j] = f2_swap(w[j]);
+    } else {
+      unpack8(*reinterpret_cast<const uint4*>(weight + partner * 8), v);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      own[j] = f2_mul(own[j], w[j]);
+      other[j] = f2_mul(other[j], v[j]);
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    if (i >= n) break;
+    uint64_t x[4], y[4];
+    unpack8(raw[i], x);
+    if constexpr (INTERLEAVED) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = turns ? f2_swap(x[j]) : 0;  // not y * 0: an infinity would give NaN
+    } else {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (p.rot > 0) {
+        const int from = row_lane0 + partner;
+        u.x = __shfl_sync(row_mask, raw[i].x, from);
+        u.y = __shfl_sync(row_mask, raw[i].y, from);
+        u.z = __shfl_sync(row_mask, raw[i].z, from);
+        u.w = __shfl_sync(row_mask, raw[i].w, from);
+        if (!turns) u = make_uint4(0, 0, 0, 0);
+      }
+      unpack8(u, y);
+    }
+    uint64_t r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = f2_fma(x[j], own[j], f2_mul(y[j], other[j]));
+    if (NORM && weight != nullptr) {
+      const uint64_t sq = f2_fma(x[3], x[3], f2_fma(x[2], x[2], f2_fma(x[1], x[1], f2_mul(x[0], x[0]))));
+      float ss, ss_hi;
+      f2_unpack(sq, ss, ss_hi);
+      ss += ss_hi;
 #pragma unroll
       for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(row_mask, ss, off);
-      inv = rsqrtf(ss * (1.f / D) + p.eps);
-      float w[8];
-      unpack8(*reinterpret_cast<const uint4*>(weight + c0), w);
+      const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+      const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= inv * w[i];
+      for (int j = 0; j < 4; ++j) r[j] = f2_mul(r[j], inv2);
     }
-    if constexpr (INTERLEAVED) {
-      if (turns) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[2 * i], b = x[2 * i + 1];
-          x[2 * i] = a * cs[i] - b * sn[i];
-          x[2 * i + 1] = b * cs[i] + a * sn[i];
-        }
-      }
-    } else if (p.rot > 0) {
-      const int from = row_lane0 + partner;
-      uint4 other;
-      other.x = __shfl_sync(row_mask, raw.x, from);
-      other.y = __shfl_sync(row_mask, raw.y, from);
-      other.z = __shfl_sync(row_mask, raw.z, from);
-      other.w = __shfl_sync(row_mask, raw.w, from);
-      if (turns) {
-        float y[8];
-        unpack8(other, y);
-        if (weight != nullptr) {
-          float w[8];
-          unpack8(*reinterpret_cast<const uint4*>(weight + partner * 8), w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] *= inv * w[i];
-        }
-        const float sign = c0 < half ? -1.f : 1.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * cs[i] + sign * (y[i] * sn[i]);
-      }
-    }
-    const uint4 out = pack8(x);
-    if (is_q) {
-      *reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + h * D + c0) = out;
-    } else {
-      if (p.k_out != nullptr) *reinterpret_cast<uint4*>(p.k_out + t * p.k_out_stride + h * D + c0) = out;
-      if (slot >= 0) *reinterpret_cast<uint4*>(p.k_cache + cache_at) = out;
-    }
+    const uint4 packed = make_uint4(pack2(r[0]), pack2(r[1]), pack2(r[2]), pack2(r[3]));
+    if (out != nullptr) *reinterpret_cast<uint4*>(out + i * D) = packed;
+    if (cache != nullptr) *reinterpret_cast<uint4*>(cache + i * D) = packed;
   }
 }
 
@@ -171,15 +206,19 @@ __global__ void rope_table_kernel(float* table, int max_positions, int rot, doub
 
 template <int D>
 cudaError_t launch(const QkRopeParams& p, cudaStream_t stream) {
-  constexpr int groups = THREADS / (D / 8);
-  const int rows = p.Hq + p.Hkv * (p.v_cache != nullptr ? 2 : 1);
-  const int lanes = rows < groups ? rows : groups;
-  const int tokens = groups / lanes;
-  const int grid = (p.T + tokens - 1) / tokens;
-  if (p.interleaved)
-    qk_rope_kernel<D, true><<<grid, THREADS, 0, stream>>>(p, lanes);
+  const int q_parts = (p.Hq + ROWS - 1) / ROWS, k_parts = (p.Hkv + ROWS - 1) / ROWS;
+  const uint32_t parts = static_cast<uint32_t>(q_parts + k_parts * (p.v_cache != nullptr ? 2 : 1));
+  const FastDiv div = FastDiv::make(parts);
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.T) * parts * (D / 8) + THREADS - 1) / THREADS);
+  const bool norm = p.q_weight != nullptr || p.k_weight != nullptr;
+  if (p.interleaved && norm)
+    qk_rope_kernel<D, true, true><<<grid, THREADS, 0, stream>>>(p, q_parts, k_parts, parts, div);
+  else if (p.interleaved)
+    qk_rope_kernel<D, true, false><<<grid, THREADS, 0, stream>>>(p, q_parts, k_parts, parts, div);
+  else if (norm)
+    qk_rope_kernel<D, false, true><<<grid, THREADS, 0, stream>>>(p, q_parts, k_parts, parts, div);
   else
-    qk_rope_kernel<D, false><<<grid, THREADS, 0, stream>>>(p, lanes);
+    qk_rope_kernel<D, false, false><<<grid, THREADS, 0, stream>>>(p, q_parts, k_parts, parts, div);
   return cudaGetLastError();
 }
 
