@@ -36,6 +36,11 @@ attn_status_t check_paged_q4(const void* cache, const int32_t* block_table, cons
   return ATTN_OK;
 }
 
+// the read-back numbers a sequence's records in 32 bits
+bool records_fit(int max_blocks_per_seq, int Hkv) {
+  return static_cast<int64_t>(max_blocks_per_seq) * Hkv <= (int64_t(1) << 31) - 1;
+}
+
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
@@ -102,8 +107,8 @@ attn_status_t attn_qk_norm_rope(const void* q, long long q_stride, const void* k
   if (rot < 0 || rot > d) return ATTN_ERR_INVALID_ARG;
   if (rot % 16 != 0) return ATTN_ERR_UNSUPPORTED;
   if (rot > 0 && (!given(positions, 4) || !given(table, 16) || max_positions < 1)) return ATTN_ERR_INVALID_ARG;
-  // the kernel numbers its threads, one for 32 values, in 32 bits
-  if (static_cast<int64_t>(num_tokens) * ((Hq + 3) / 4 + 2 * ((Hkv + 3) / 4)) * (d / 8) >= (int64_t(1) << 31))
+  // the kernel numbers its threads, one for 64 values, in 32 bits
+  if (static_cast<int64_t>(num_tokens) * ((Hq + 7) / 8 + 2 * ((Hkv + 7) / 8)) * (d / 8) >= (int64_t(1) << 31))
     return ATTN_ERR_INVALID_ARG;
   const bool paged = k_cache != nullptr || v_cache != nullptr;
   if (!paged && k_out == nullptr) return ATTN_ERR_INVALID_ARG;
@@ -176,7 +181,7 @@ attn_status_t attn_cache_gather_q4(const void* cache, const int32_t* block_table
   const attn_status_t chk =
       check_paged_q4(cache, block_table, seq_lens, num_seqs, Hkv, d, page_size, max_blocks_per_seq, num_blocks);
   if (chk != ATTN_OK) return chk;
-  if (!given(k_out, 16) || !given(v_out, 16)) return ATTN_ERR_INVALID_ARG;
+  if (!given(k_out, 16) || !given(v_out, 16) || !records_fit(max_blocks_per_seq, Hkv)) return ATTN_ERR_INVALID_ARG;
   attn::GatherQ4Params p;
   p.cache = static_cast<const uint8_t*>(cache);
   p.block_table = block_table;
@@ -228,7 +233,7 @@ attn_status_t attn_decode_paged_q4(const void* q, const void* cache, const int32
 
 size_t attn_prefill_q4_workspace_bytes(int num_seqs, int Hkv, int d, int max_blocks_per_seq) {
   if (num_seqs < 1 || Hkv < 1 || Hkv > 65535 || !head_dim(d) || max_blocks_per_seq < 1 ||
-      static_cast<int64_t>(num_seqs) * max_blocks_per_seq * kPage > kMaxTokens)
+      !records_fit(max_blocks_per_seq, Hkv) || static_cast<int64_t>(num_seqs) * max_blocks_per_seq * kPage > kMaxTokens)
     return 0;
   const size_t pages = static_cast<size_t>(num_seqs) * max_blocks_per_seq;
   return 2 * up256(pages * kPage * Hkv * d * 2) + up256(pages * 4);

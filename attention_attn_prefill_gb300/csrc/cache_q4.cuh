@@ -54,15 +54,13 @@ __device__ __forceinline__ uint32_t rotl3(uint32_t w) { return __funnelshift_l(w
 
 constexpr uint32_t PARAM_NAN = 0x7fc0;  // the group's values read back as NaN
 
-// Scale and zero point of a group with maximum hi >= 0 and minimum lo <= 0, as a parameter word.  Both
-// roundings go up, and so does the last one, to a coarser grid: together they are one rounding up of
-// the exact quotient.
-__device__ __forceinline__ uint32_t make_param(float hi, float lo, float& scale, float& zero) {
-  const float step = __fdiv_ru(__fsub_ru(hi, lo), 15.f);
-  const uint32_t bits = (__float_as_uint(step) + 0xfffffu) & 0xfff00000u;
-  scale = __uint_as_float(bits);
-  zero = scale > 0.f ? rintf(__fdiv_rn(-lo, scale)) : 0.f;
-  return (bits >> 16) | static_cast<uint32_t>(zero);
+// Scale of a group with maximum hi >= 0 and minimum lo <= 0: the smallest s of 4 significant bits with
+// 15 s >= hi - lo.  The difference is rounded up, which a 15 s (8 bits) never falls below for; the
+// quotient is taken a little low and 15 s, exact, decides.
+__device__ __forceinline__ float make_scale(float hi, float lo) {
+  const float span = __fsub_ru(hi, lo);
+  const uint32_t bits = (__float_as_uint(span * 0.06666666f) + 0xfffffu) & 0xfff00000u;
+  return __uint_as_float(__uint_as_float(bits) * 15.f < span ? bits + 0x100000u : bits);
 }
 
 }  // namespace q4

@@ -27,8 +27,10 @@ __device__ uint32_t g_qk_rope_status;
 
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int ROWS = 4;  // rows a group of threads takes, their loads in flight together
+// Measured on 32749 tokens of 16 + 2 heads, d = 256 (604 MB): 64 threads a CTA 103 us, 128 107 us, 256
+// 122 us (fewer warps wait for the slowest of their CTA); 8 rows a group 103 us, 4 108 us, 2 133 us.
+constexpr int THREADS = 64;
+constexpr int ROWS = 8;  // rows a group of threads takes, their loads in flight together
 
 // eight bf16 values as four pairs of floats
 __device__ __forceinline__ void unpack8(const uint4& u, uint64_t (&x)[4]) {

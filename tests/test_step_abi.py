@@ -53,7 +53,7 @@ ROPE = dict(q=FAKE, qs=1024, k=FAKE, ks=256, v=FAKE, vs=256, qw=FAKE, kw=FAKE, e
     (dict(table=None), 1), (dict(maxp=0), 1), (dict(kc=None), 1), (dict(vc=None), 1), (dict(v=None), 1),
     (dict(slots=None), 1), (dict(nblocks=0), 1), (dict(page=8), 2),
     (dict(kc=None, vc=None, ko=None), 1),                    # nowhere to put K
-    (dict(T=1 << 26), 1),
+    (dict(T=1 << 27), 1),
 ])
 def test_qk_norm_rope_refusals(attn, over, want):
     assert _call(attn, "attn_qk_norm_rope", ROPE, over) == want
