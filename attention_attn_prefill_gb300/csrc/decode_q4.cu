@@ -7,17 +7,20 @@
 // to the 16 scores of a page's token tile and to its 16 probabilities, not to the d values of a token.
 //
 // Both products have the codes as the left operand, S^T = K Q^T and O^T = V^T P^T: their four registers
-// are the decoded words themselves, and 8 columns hold the query heads of a KV head.  With up to four
-// heads the columns take the heads of two pages, so that one step's scores, exponentials and
-// roundings serve both.  p s is split into two bf16 numbers (16 bits together): one alone would add an
-// error as large as the output's own rounding.  Odd tokens of V enter as c - 31 (one exclusive-or
+// are the decoded words themselves, and 8 columns hold the query heads of a KV head.  p s is split into
+// two bf16 numbers (16 bits together): one alone would add an error as large as the output's own
+// rounding.  With up to four heads, a step takes two pages: the score columns hold the heads of both,
+// so that one round of exponentials and roundings serves both, and the columns of a page's product with
+// V hold the upper parts of p s and the lower ones.  Odd tokens of V enter as c - 31 (one exclusive-or
 // instead of the or), so that the offsets of the codes cancel in the running sums.
 //
-// Work: the (sequence, KV head, page) list is cut into equal contiguous shares, one a CTA; the CTA's
-// warps deal its pages among themselves, each with its own ring of bulk copies (a record is one
-// copy).  Where a share's end cuts a sequence, the CTA leaves a partial (normalised output, max, sum);
-// a second kernel, launched as a programmatic dependent, merges the partials of each cut sequence.
-// At most two partials a CTA, so the workspace does not depend on the batch.
+// Work: the (sequence, KV head, step) list is cut into contiguous shares of equal weight, one a CTA; the
+// CTA's computing warps deal its steps among themselves.  One more warp requests the records (one
+// bulk copy each) into the warps' rings, and merges the warps' states of a sequence when all have left
+// it, so that the computing warps never wait for each other.  Where a share's end cuts a sequence, the
+// CTA leaves a partial (normalised output, max, sum); a second kernel, launched as a programmatic
+// dependent, merges the partials of each cut sequence.  At most two partials a CTA, so the workspace
+// does not depend on the batch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -37,6 +40,11 @@ using q4::PAGE;
 using q4::Record;
 
 constexpr float LN2 = 0.693147180559945309f;
+#ifndef TSEG
+#define TSEG 4
+#endif
+constexpr int SEGMENT = TSEG;
+constexpr int COMBINE_THREADS = 512;
 constexpr int ROWS = 8;                       // score columns of a warp: query heads, or heads of two pages
 constexpr uint32_t CODE_MASK = 0x00780078u;   // a nibble on mantissa bits 3..6 of both halves
 constexpr uint32_t K_MAGIC = 0x41804180u;     // 16 + c in both halves
@@ -48,21 +56,31 @@ constexpr uint32_t Z_EVEN = 0x41800000u, Z_ODD = 0xc1f80000u;
 // P: pages a warp takes at a step; ROWS / P query heads.
 template <int D, int P>
 struct Cfg {
-  static constexpr int NW = D < 256 ? 7 : P == 2 ? 4 : 5;  // warps that compute (one more loads)
-  static constexpr int NS = D == 256 ? 3 : D == 128 ? 3 : 4;  // pages in flight a warp
+#ifndef TNW
+#define TNW 7
+#endif
+#ifndef TSLEEP
+#define TSLEEP 100
+#endif
+#ifndef TPIPE
+#define TPIPE 0
+#endif
+#ifndef TDEPTH
+#define TDEPTH 3
+#endif
+  static constexpr int NW = D == 256 ? 5 : D == 128 ? TNW : 7;  // warps that compute (one more loads)
   static constexpr int CTAS = 2;                   // CTAs an SM
   static constexpr int THREADS = (NW + 1) * 32;
   static constexpr int TILE = ROWS / P;            // query heads a tile
-  static constexpr int DEPTH = P == 2 ? 2 : NS;    // steps in flight a warp
+  static constexpr int DEPTH = D == 256 ? (P == 2 ? 2 : 3) : D == 128 ? TDEPTH : 3;             // steps in flight a warp
   static constexpr int SLOTS = NW * DEPTH;
   static constexpr int STAGE = (P * Record<D>::BYTES + 127) & ~127;
   static constexpr int OROW = D + 8;               // floats of a row in the merge buffer
-  static constexpr int MERGE = 2 * ROWS + ROWS * OROW;  // floats a warp: m, l, o
+  static constexpr int MERGE = 2 * ROWS + TILE * OROW;  // floats a warp: m, l, o
   static constexpr int MERGE_OFF = SLOTS * STAGE;
   static constexpr int BAR_OFF = MERGE_OFF + NW * MERGE * 4;
-  static constexpr int ALLOC = BAR_OFF + 2 * SLOTS * 8;
+  static constexpr int ALLOC = BAR_OFF + (2 * SLOTS + 2) * 8;
   static_assert(CTAS * (ALLOC + 1024 + 256) <= 228 * 1024, "shared memory budget");
-  static_assert(CTAS * THREADS * (D == 256 ? 168 : 128) <= 65536, "register budget");
 };
 
 // a * b / c with c > 0; the quotient is below 2^63.  64-bit division costs over a hundred instructions,
@@ -99,7 +117,7 @@ __device__ Workspace carve(void* ws, int grid) {
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -132,7 +150,11 @@ __device__ __forceinline__ int steps_of(const int32_t* lens, int n, int max_bloc
 // Position in the (sequence, unit, step) list.
 template <int P>
 struct Cursor {
-  int n, u, step, ns;
+  int n, u, step, ns, pages;  // ns steps and `pages` pages of sequence n
+  __device__ __forceinline__ void enter(const int32_t* lens, int max_blocks) {
+    pages = (clamped_len(lens, n, max_blocks) + PAGE - 1) / PAGE;
+    ns = (pages + P - 1) / P;
+  }
   __device__ __forceinline__ void advance(int by, const int32_t* lens, int N, int units, int max_blocks) {
     step += by;
     while (step >= ns) {
@@ -145,7 +167,7 @@ struct Cursor {
             ns = 0x7fffffff;
             return;
           }
-          ns = steps_of<P>(lens, n, max_blocks);
+          enter(lens, max_blocks);
         } while (ns == 0);
       }
     }
@@ -187,12 +209,13 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
   using R = Record<D>;
   constexpr int NW = C::NW, NG = R::NG, THREADS = C::THREADS, TILE = C::TILE, SLOTS = C::SLOTS;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_warp[NW + 1];
-  __shared__ long long s_before;
-  __shared__ int s_n;
+  __shared__ long long s_weight[NW + 1], s_steps[NW + 1], s_end[2], s_at;
+  __shared__ int3 s_start;
   float* merge = reinterpret_cast<float*>(smem + C::MERGE_OFF);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
   uint64_t* empty = full + SLOTS;
+  uint64_t* rec_full = empty + SLOTS;  // every computing warp's state of a segment is in the merge buffer
+  uint64_t* rec_free = rec_full + 1;   // the loading warp has read them
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int N = p.N, G = p.Hq / p.Hkv, units = geo.units;
 
@@ -200,48 +223,79 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
   if (threadIdx.x < SLOTS) {
     mbar_init(&full[threadIdx.x], 1);
     mbar_init(&empty[threadIdx.x], 1);
+    if (threadIdx.x == 0) {
+      mbar_init(rec_full, NW);
+      mbar_init(rec_free, 1);
+    }
     fence_mbar_init();
   }
+  // The list is cut by weight: a (sequence, unit) weighs its steps and SEGMENT more, what starting on it and
+  // leaving its result cost.
   const int chunk = (N + THREADS - 1) / THREADS;
   const int n_lo = static_cast<int>(threadIdx.x) * chunk < N ? threadIdx.x * chunk : N;
   const int n_hi = n_lo + chunk < N ? n_lo + chunk : N;
-  long long mine = 0;
+  long long my_weight = 0, my_steps = 0;
   for (int n = n_lo; n < n_hi; ++n) {
     const int L = p.seq_lens[n];
     if (blockIdx.x == 0 && (L < 0 || L > p.max_blocks * PAGE)) set_error(&g_decode_q4_status, kDevBadSplit);
-    mine += steps_of<P>(p.seq_lens, n, p.max_blocks);
+    const int ns = steps_of<P>(p.seq_lens, n, p.max_blocks);
+    my_steps += ns;
+    my_weight += ns > 0 ? ns + SEGMENT : 0;
   }
-  long long incl = mine;
+  long long to_weight = my_weight, to_steps = my_steps;  // inclusive sums
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const long long a = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += a;
+    const long long a = __shfl_up_sync(0xffffffffu, to_weight, off), c = __shfl_up_sync(0xffffffffu, to_steps, off);
+    if (lane >= off) {
+      to_weight += a;
+      to_steps += c;
+    }
   }
-  if (lane == 31) s_warp[warp] = incl;
+  if (lane == 31) {
+    s_weight[warp] = to_weight;
+    s_steps[warp] = to_steps;
+  }
   __syncthreads();
-  long long total = 0;
+  long long weight = 0, steps = 0;
 #pragma unroll
   for (int i = 0; i < NW + 1; ++i) {
-    if (i < warp) incl += s_warp[i];
-    total += s_warp[i];
+    if (i < warp) {
+      to_weight += s_weight[i];
+      to_steps += s_steps[i];
+    }
+    weight += s_weight[i];
+    steps += s_steps[i];
   }
-  const long long W = total * units;
+  const long long W = weight * units;
   // at least a step for each warp of a share
-  const long long shares = W >= static_cast<long long>(geo.grid) * NW ? geo.grid : W < NW ? 1 : static_cast<int>(W) / NW;
+  const long long most = steps * units / NW;
+  const long long shares = most >= geo.grid ? geo.grid : most < 1 ? 1 : most;
   const int b = blockIdx.x;
   const long long lo = b < shares ? mul_div(b, W, shares) : W, hi = b < shares ? mul_div(b + 1, W, shares) : W;
-  const int count = static_cast<int>(hi - lo);  // steps of this share
-  const long long before_mine = (incl - mine) * units;
-  if (count > 0 && before_mine <= lo && lo < incl * units) {
-    long long at = before_mine;
-    int n = n_lo;
+  if (threadIdx.x == 0) s_end[0] = s_end[1] = steps * units;  // where the share's end is the list's
+  __syncthreads();
+  // the sequences in which the share begins and ends
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    const long long x = side ? hi : lo;
+    if (x < (to_weight - my_weight) * units || x >= to_weight * units) continue;
+    long long at = (to_weight - my_weight) * units, before = (to_steps - my_steps) * units;
+    int n = n_lo, ns = 0;
     for (;; ++n) {
-      const long long w = static_cast<long long>(steps_of<P>(p.seq_lens, n, p.max_blocks)) * units;
-      if (lo < at + w) break;
+      ns = steps_of<P>(p.seq_lens, n, p.max_blocks);
+      const long long w = ns > 0 ? static_cast<long long>(ns + SEGMENT) * units : 0;
+      if (x < at + w) break;
       at += w;
+      before += static_cast<long long>(ns) * units;
     }
-    s_n = n;
-    s_before = at;
+    const int u = static_cast<int>(mul_div(x - at, 1, ns + SEGMENT));
+    const int in = static_cast<int>(x - at - static_cast<long long>(u) * (ns + SEGMENT));
+    const int step = in > SEGMENT ? in - SEGMENT : 0;
+    s_end[side] = before + static_cast<long long>(u) * ns + step;  // steps before x
+    if (side == 0) {
+      s_start = make_int3(n, u, step);
+      s_at = at + static_cast<long long>(u) * (ns + SEGMENT);
+    }
   }
   // empty sequences: this CTA's part of them
   for (int n = b; n < N; n += gridDim.x) {
@@ -255,71 +309,137 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
   // every CTA of this grid is resident: the combine's CTAs may queue up behind them
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Workspace ws = carve<D>(p.workspace, geo.grid);
+  const int count = static_cast<int>(s_end[1] - s_end[0]);  // steps of this share
   if (count <= 0) {
     if (threadIdx.x == 0) ws.desc[b] = make_int4(0, 0, 0, 0);
     return;
   }
 
   Cursor<P> cur;  // the share's first step
-  cur.n = s_n;
-  cur.ns = steps_of<P>(p.seq_lens, cur.n, p.max_blocks);
-  const long long rel = lo - s_before;
-  cur.u = static_cast<int>(mul_div(rel, 1, cur.ns));
-  cur.step = static_cast<int>(rel - static_cast<long long>(cur.u) * cur.ns);
+  cur.n = s_start.x;
+  cur.u = s_start.y;
+  cur.step = s_start.z;
+  cur.enter(p.seq_lens, p.max_blocks);
 
   if (warp == NW) {
-    // ---------------------------------------------------------- loads
-    // Step i goes to slot i % SLOTS and to computing warp i % NW.  Each lane finds the records of one
-    // of 32 steps (its table entries are read together with the other lanes'), then NW lanes at a
-    // time wait for their slots and request their records, one copy a record.
-    constexpr int ROUND = 32 / NW * NW;
+    // ---------------------------------------------------------- loads, and results
+    // Lane w serves computing warp w: step i of the share belongs to warp i % NW and goes through that
+    // warp's ring.  The lanes poll their rings together, so that no warp waits for another's slot, and
+    // each reads the block table a step ahead of the copy that needs it.  When all warps have left
+    // their states of a segment (the share's part of a sequence and unit), this warp merges them and
+    // writes the result, while the others are at the next segment.
     bool ok = true;
-    int last = -1;   // this lane's last step whose copy was requested
-    cur.advance(lane, p.seq_lens, N, units, p.max_blocks);
-    for (int base = 0; base < count; base += ROUND) {
-      const int i = base + lane;
-      const bool live = lane < ROUND && i < count;
-      const uint8_t* src[P];
-      int pages = 0;
-      if (live) {
-        const int len = clamped_len(p.seq_lens, cur.n, p.max_blocks);
-        const int32_t* row = p.block_table + static_cast<int64_t>(cur.n) * p.max_blocks + cur.step * P;
+    Cursor<P> seg = cur;    // the segment to merge next ...
+    long long at = s_at;    // ... the weight before its (sequence, unit) ...
+    int seg_i = 0;          // ... its first step's share index
+    uint32_t seg_phase = 0;
+    int4 cut = make_int4(0, 0, 0, 0);
+    int i = lane;      // this lane's next step, with the pages' table entries
+    int ids[P] = {};
+    int stage_k = 0;
+    uint32_t phase = 1;  // a slot's first use waits for nothing
+    auto fetch = [&]() {
+      const int32_t* row = p.block_table + static_cast<int64_t>(cur.n) * p.max_blocks + cur.step * P;
+      ids[0] = row[0];
+      if (P == 2 && cur.step * P + 1 < cur.pages) ids[P - 1] = row[1];
+    };
+    if (lane > 0) cur.advance(lane, p.seq_lens, N, units, p.max_blocks);
+    const bool serves = lane < NW;
+    if (serves && i < count) fetch();
+    uint64_t since = global_timer_ns();
+    while (ok && seg_i < count) {
+      const int slot = lane + NW * stage_k;
+      const bool go = serves && i < count && mbar_test_wait(&empty[slot], phase);
+      if (go) {
+        const int pages = P == 2 && cur.step * P + 1 < cur.pages ? 2 : 1;
+        mbar_arrive_expect_tx(&full[slot], pages * R::BYTES);
 #pragma unroll
         for (int a = 0; a < P; ++a) {
-          if ((cur.step * P + a) * PAGE >= len) continue;
-          int id = row[a];
+          if (a >= pages) break;
+          int id = ids[a];
           if (id < 0 || id >= p.num_blocks) {
             set_error(&g_decode_q4_status, kDevBadPage);
             id = 0;
           }
-          src[a] = p.cache + (static_cast<int64_t>(id) * p.Hkv + cur.u / geo.tiles) * R::BYTES;
-          ++pages;
+          bulk_load(smem + slot * C::STAGE + a * R::BYTES,
+                    p.cache + (static_cast<int64_t>(id) * p.Hkv + cur.u / geo.tiles) * R::BYTES, R::BYTES, &full[slot]);
+        }
+        if (++stage_k == C::DEPTH) {
+          stage_k = 0;
+          phase ^= 1;
+        }
+        i += NW;
+        if (i < count) {
+          cur.advance(NW, p.seq_lens, N, units, p.max_blocks);
+          fetch();
         }
       }
-#pragma unroll 1
-      for (int from = 0; from < ROUND && base + from < count; from += NW) {
-        if (live && lane >= from && lane < from + NW) {
-          const int slot = i % SLOTS;
-          if (ok) ok = mbar_wait(&empty[slot], (i / SLOTS & 1) ^ 1);
-          if (ok) {
-            mbar_arrive_expect_tx(&full[slot], pages * R::BYTES);
-            bulk_load(smem + slot * C::STAGE, src[0], R::BYTES, &full[slot]);
-            if (P == 2 && pages == 2) bulk_load(smem + slot * C::STAGE + R::BYTES, src[P - 1], R::BYTES, &full[slot]);
-            last = i;
+      const bool merge_now = __all_sync(0xffffffffu, mbar_test_wait(rec_full, seg_phase));
+      if (merge_now) {
+        seg_phase ^= 1;
+        const int seg_steps = seg.ns - seg.step < count - seg_i ? seg.ns - seg.step : count - seg_i;
+        const bool starts = seg.step == 0, ends = seg.step + seg_steps == seg.ns;
+        const int kvh = seg.u / geo.tiles, h0 = seg.u % geo.tiles * TILE;
+        const int heads = G - h0 < TILE ? G - h0 : TILE;
+        const int64_t part = 2 * b + (starts ? 1 : 0);
+        for (int w = lane; w < heads * (D / 4); w += 32) {
+          const int r = w / (D / 4), x = w % (D / 4) * 4;
+          float M = -INFINITY;
+#pragma unroll
+          for (int v = 0; v < NW; ++v) M = fmaxf(M, merge[v * C::MERGE + r]);
+          float L = 0.f;
+          float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int v = 0; v < NW; ++v) {
+            const float* src = merge + v * C::MERGE;
+            const float wl = src[ROWS + r];
+            if (wl == 0.f) continue;  // a warp without tokens
+            const float f = ex2_approx(src[r] - M);
+            const float4 y = *reinterpret_cast<const float4*>(src + 2 * ROWS + r * C::OROW + x);
+            L = fmaf(wl, f, L);
+            O.x = fmaf(y.x, f, O.x); O.y = fmaf(y.y, f, O.y);
+            O.z = fmaf(y.z, f, O.z); O.w = fmaf(y.w, f, O.w);
+          }
+          const float inv = 1.f / L;
+          O.x *= inv; O.y *= inv; O.z *= inv; O.w *= inv;
+          if (starts && ends) {
+            const int64_t row = static_cast<int64_t>(seg.n) * p.Hq + kvh * G + h0 + r;
+            *reinterpret_cast<uint2*>(p.o + row * D + x) = make_uint2(pack_bf16x2(O.x, O.y), pack_bf16x2(O.z, O.w));
+            if (x == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(L)) * LN2;
+          } else {
+            *reinterpret_cast<float4*>(ws.o + (part * ROWS + r) * D + x) = O;
+            if (x == 0) {
+              ws.m[part * ROWS + r] = M;
+              ws.l[part * ROWS + r] = L;
+            }
           }
         }
         __syncwarp();
-        ok = __all_sync(0xffffffffu, ok);
+        if (lane == 0) mbar_arrive(rec_free);
+        if (starts && !ends) {
+          // the share that holds the last step: weight x lies in share ((x + 1) shares - 1) / W
+          const long long past = at + SEGMENT + seg.ns;
+          cut = make_int4(seg.n, seg.u, static_cast<int>(mul_div(past * shares - 1, 1, W)), 1);
+        }
+        at += SEGMENT + seg.ns;
+        seg_i += seg_steps;
+        if (seg_i < count) seg.advance(seg_steps, p.seq_lens, N, units, p.max_blocks);
       }
-      if (!ok) break;
-      cur.advance(ROUND, p.seq_lens, N, units, p.max_blocks);
+      if (__any_sync(0xffffffffu, go) || merge_now) {
+        since = global_timer_ns();
+      } else {
+        __nanosleep(50);
+        ok = __all_sync(0xffffffffu, global_timer_ns() - since < ATTN_WAIT_LIMIT_NS);
+      }
     }
-    if (!ok) set_error(&g_decode_q4_status, kDevWaitTimeout);
-    // Copies in flight must land before the CTA's shared memory is given back.  Only a slot's newest
-    // copy is of the phase that its barrier is in; an older one was waited for before the newer left.
-    static_assert(ROUND >= SLOTS, "a lane has at most one step among the newest of the slots");
-    const int end = __reduce_max_sync(0xffffffffu, last) + 1;
-    if (last >= 0 && last >= end - SLOTS) mbar_wait(&full[last % SLOTS], last / SLOTS & 1);
+    if (lane == 0) {
+      ws.desc[b] = cut;
+      if (!ok) set_error(&g_decode_q4_status, kDevWaitTimeout);
+    }
+    // Copies in flight must land before the CTA's shared memory is given back: the newest of each slot.
+    const int issued = serves ? (i - lane) / NW : 0;
+    for (int k = issued > C::DEPTH ? issued - C::DEPTH : 0; k < issued; ++k)
+      mbar_wait(&full[lane + NW * (k % C::DEPTH)], k / C::DEPTH & 1);
     return;
   }
 
@@ -331,7 +451,9 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
   const float c2 = p.scale_log2;
   bool ok = true;
   int i = warp;    // share index of this warp's next step
-  int4 cut = make_int4(0, 0, 0, 0);
+  int stage_k = 0;         // its ring stage: slot warp + NW stage_k ...
+  uint32_t phase = 0;      // ... and the parity of that slot's barriers
+  uint32_t free_phase = 0;
   for (int seg = 0; seg < count;) {
     const int seg_n = cur.n, seg_u = cur.u, first_step = cur.step;
     const int seg_steps = cur.ns - first_step < count - seg ? cur.ns - first_step : count - seg;
@@ -374,58 +496,47 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
 #pragma unroll
     for (int e = 0; e < NG; ++e) base[e][0] = base[e][1] = 0.f;
 
-    for (; i < seg_end; i += NW) {
-      const int slot = i % SLOTS;
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], i / SLOTS & 1));
-      if (!ok) continue;
-      const uint8_t* stage = smem + slot * C::STAGE;
-      const uint8_t* mine_rec = stage + my_page * R::BYTES;
-      // tokens of this lane's page that the sequence has; the last step's second page may have none
-      const int valid = len - ((first_step + i - seg) * P + my_page) * PAGE;
-
-      // ---- S^T: rows are tokens g (0, 1) and g + 8 (2, 3), columns 2 t and 2 t + 1
-      float sc[4] = {0.f, 0.f, 0.f, 0.f};
-      Params<NG> kp[2], vp[2];
+    // S^T of a step whose records are at `stage`: rows are tokens g (0, 1) and g + 8 (2, 3), columns 2 t and
+    // 2 t + 1
+    auto scores = [&](const uint8_t* stage, float (&sc)[4]) {
+      sc[0] = sc[1] = sc[2] = sc[3] = 0.f;
+      Params<NG> kp[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        kp[j].load(mine_rec + R::KP_OFF + (g + 8 * j) * (2 * NG));
-        vp[j].load(mine_rec + R::VP_OFF + (g + 8 * j) * (2 * NG));
-      }
+      for (int j = 0; j < 2; ++j) kp[j].load(stage + my_page * R::BYTES + R::KP_OFF + (g + 8 * j) * (2 * NG));
 #pragma unroll
       for (int pr = 0; pr < NG / R::PAIR; ++pr) {
         float acc[R::PAIR][P][4];
+        uint32_t kw[P][2][2 * R::PAIR];
 #pragma unroll
         for (int a = 0; a < P; ++a) {
-          uint32_t kw[2][2 * R::PAIR];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint8_t* row =
                 stage + a * R::BYTES + R::K_OFF + (g + 8 * j) * (D / 2) + pr * (32 * R::PAIR) + t * (8 * R::PAIR);
             if constexpr (R::PAIR == 2) {
               const uint4 x = *reinterpret_cast<const uint4*>(row);
-              kw[j][0] = x.x; kw[j][1] = x.y; kw[j][2] = x.z; kw[j][3] = x.w;
+              kw[a][j][0] = x.x; kw[a][j][1] = x.y; kw[a][j][2] = x.z; kw[a][j][3] = x.w;
             } else {
               const uint2 x = *reinterpret_cast<const uint2*>(row);
-              kw[j][0] = x.x; kw[j][1] = x.y;
-            }
-          }
-#pragma unroll
-          for (int ee = 0; ee < R::PAIR; ++ee) {
-            const int e = pr * R::PAIR + ee;
-            acc[ee][a][0] = acc[ee][a][1] = acc[ee][a][2] = acc[ee][a][3] = 0.f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t w0 = kw[0][ee * 2 + h], w1 = kw[1][ee * 2 + h];
-              mma_16816(acc[ee][a], decode(w0, geo.k_magic), decode(w1, geo.k_magic),
-                        decode(__funnelshift_r(w0, w0, 4), geo.k_magic),
-                        decode(__funnelshift_r(w1, w1, 4), geo.k_magic), qb[e][h][0], qb[e][h][1]);
-              mma_16816(acc[ee][a], decode(__funnelshift_r(w0, w0, 8), geo.k_magic),
-                        decode(__funnelshift_r(w1, w1, 8), geo.k_magic),
-                        decode(__funnelshift_r(w0, w0, 12), geo.k_magic),
-                        decode(__funnelshift_r(w1, w1, 12), geo.k_magic), qb[e][h][2], qb[e][h][3]);
+              kw[a][j][0] = x.x; kw[a][j][1] = x.y;
             }
           }
         }
+        // consecutive products go to different accumulators: each would wait for the one before otherwise
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int a = 0; a < P; ++a)
+#pragma unroll
+            for (int ee = 0; ee < R::PAIR; ++ee) {
+              const int e = pr * R::PAIR + ee, h = k / 2, s = k % 2 * 2;
+              const uint32_t w0 = kw[a][0][ee * 2 + h], w1 = kw[a][1][ee * 2 + h];
+              if (k == 0) acc[ee][a][0] = acc[ee][a][1] = acc[ee][a][2] = acc[ee][a][3] = 0.f;
+              mma_16816(acc[ee][a], decode(__funnelshift_r(w0, w0, 4 * s), geo.k_magic),
+                        decode(__funnelshift_r(w1, w1, 4 * s), geo.k_magic),
+                        decode(__funnelshift_r(w0, w0, 4 * s + 4), geo.k_magic),
+                        decode(__funnelshift_r(w1, w1, 4 * s + 4), geo.k_magic), qb[e][h][s], qb[e][h][s + 1]);
+            }
 #pragma unroll
         for (int ee = 0; ee < R::PAIR; ++ee) {
           const int e = pr * R::PAIR + ee;
@@ -440,6 +551,38 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
           }
         }
       }
+    };
+    // the stage of this warp's next step, once its copy has landed
+    auto next_stage = [&]() {
+      const int slot = warp + NW * stage_k;
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[slot], phase));
+      if (++stage_k == C::DEPTH) {
+        stage_k = 0;
+        phase ^= 1;
+      }
+      return slot;
+    };
+
+    float sc[4];
+    int slot = 0;
+    if (TPIPE && i < seg_end) {
+      slot = next_stage();
+      if (ok) scores(smem + slot * C::STAGE, sc);
+    }
+    for (; i < seg_end; i += NW) {
+      // the next step's scores are computed beside this step's product with V, whose operand waits for a
+      // chain of short steps (exponential, rounding, transpose); after the last step they are not used
+      int ahead = slot;
+      if (TPIPE) { if (i + NW < seg_end) ahead = next_stage(); }
+      else slot = next_stage();
+      if (!ok) continue;
+      if (!TPIPE) scores(smem + slot * C::STAGE, sc);
+      const uint8_t* stage = smem + slot * C::STAGE;
+      // tokens of this lane's page that the sequence has; the last step's second page may have none
+      const int valid = len - ((first_step + i - seg) * P + my_page) * PAGE;
+      Params<NG> vp[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) vp[j].load(stage + my_page * R::BYTES + R::VP_OFF + (g + 8 * j) * (2 * NG));
       if (__any_sync(0xffffffffu, valid < PAGE)) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -459,6 +602,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          if (P == 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));  // a head's two pages share the reference
           const float to = fmaxf(mc[c], mx * c2), f = ex2_approx(mc[c] - to);
           mc[c] = to;
           l[c] *= f;
@@ -475,25 +619,29 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
       }
       l[0] += pr[0] + pr[2];
       l[1] += pr[1] + pr[3];
-      // ---- O^T += V^T (p s)^T.  A page's product takes its own columns' probabilities, zeros for the other's.
+      if (TPIPE) scores(smem + ahead * C::STAGE, sc);
+      // ---- O^T += V^T (p s)^T.  Two pages: columns 0 .. 3 of a page's product are its upper parts, 4 .. 7
+      // its lower ones, which the lanes of columns 4 .. 7 and 0 .. 3 swap.
 #pragma unroll
       for (int e = 0; e < NG; ++e) {
-        uint32_t ph[2], pl[2];
+        uint32_t pb[2][2];  // [page, or upper and lower part][tokens 0 .. 7, 8 .. 15]
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float s = vp[j].scale(e), z = vp[j].zero(e, z_magic);
           const float x0 = pr[2 * j] * s, x1 = pr[2 * j + 1] * s;
           base[e][0] = fmaf(x0, z, base[e][0]);
           base[e][1] = fmaf(x1, z, base[e][1]);
-          const uint32_t hi = pack_bf16x2(x0, x1);
-          ph[j] = transpose_8x8(hi);
-          pl[j] = transpose_8x8(
-              pack_bf16x2(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u)));
+          uint32_t hi = pack_bf16x2(x0, x1);
+          uint32_t lo_ = pack_bf16x2(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
+          if (P == 2) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, my_page ? hi : lo_, 2);
+            if (my_page) hi = got; else lo_ = got;
+          }
+          pb[0][j] = transpose_8x8(hi);
+          pb[1][j] = transpose_8x8(lo_);
         }
 #pragma unroll
         for (int a = 0; a < P; ++a) {
-          const bool on = P == 1 || (g >> 2) == a;  // as an operand, this lane holds column g
-          const uint32_t h0_ = on ? ph[0] : 0u, h1_ = on ? ph[1] : 0u, l0_ = on ? pl[0] : 0u, l1_ = on ? pl[1] : 0u;
           const uint4 vw = *reinterpret_cast<const uint4*>(stage + a * R::BYTES + R::V_OFF + (e * 32 + lane) * 16);
           const uint32_t w4[4] = {vw.x, vw.y, vw.z, vw.w};
 #pragma unroll
@@ -501,18 +649,20 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
             const uint32_t w = w4[j];
             const uint32_t a0 = decode(w << 3, geo.v_magic), a1 = decode(w >> 1, geo.v_magic);
             const uint32_t a2 = decode(w >> 5, geo.v_magic), a3 = decode(w >> 9, geo.v_magic);
-            mma_16816(o[e * 4 + j], a0, a1, a2, a3, h0_, h1_);
-            mma_16816(o[e * 4 + j], a0, a1, a2, a3, l0_, l1_);
+            mma_16816(o[e * 4 + j], a0, a1, a2, a3, pb[a][0], pb[a][1]);
+            if (P == 1) mma_16816(o[e * 4 + j], a0, a1, a2, a3, pb[1][0], pb[1][1]);
           }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[slot]);
+      if (TPIPE) slot = ahead;
     }
 
-    // ---- this warp's state to shared memory, then the CTA's to global memory
+    // ---- this warp's state to shared memory, then the CTA's to global memory.  With two pages, a head's
+    // sums are in columns c and c + 4, two lanes apart.
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
+    for (int off = P == 2 ? 2 : 4; off < 32; off <<= 1) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         l[c] += __shfl_xor_sync(0xffffffffu, l[c], off);
@@ -520,81 +670,53 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
         for (int e = 0; e < NG; ++e) base[e][c] += __shfl_xor_sync(0xffffffffu, base[e][c], off);
       }
     }
+    if (P == 2) {
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[x][j] += __shfl_xor_sync(0xffffffffu, o[x][j], 2);
+    }
+    // the loading warp has merged the segment before this one
+    if (seg > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(rec_free, free_phase)) && ok;
+      free_phase ^= 1;
+    }
     float* my = merge + warp * C::MERGE;
-    if (g == 0) {
+    if (2 * t < TILE) {
+      if (g == 0) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        my[2 * t + c] = l[c] == 0.f ? -INFINITY : mc[c];  // no tokens: no part in the maximum
-        my[ROWS + 2 * t + c] = l[c];
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < D / 16; ++x) {
-      float* at = my + 2 * ROWS + 2 * t * C::OROW + 16 * x + 2 * g;
-      *reinterpret_cast<float2*>(at) = make_float2(o[x][0] - base[x / 4][0], o[x][2] - base[x / 4][0]);
-      *reinterpret_cast<float2*>(at + C::OROW) = make_float2(o[x][1] - base[x / 4][1], o[x][3] - base[x / 4][1]);
-    }
-    named_barrier_sync(1, NW * 32);
-    const bool starts = first_step == 0, ends = first_step + seg_steps == cur.ns;
-    const int64_t slot = 2 * b + (starts ? 1 : 0);
-    for (int w = threadIdx.x; w < heads * (D / 4); w += NW * 32) {
-      const int r = w / (D / 4), x = w % (D / 4) * 4;
-      float M = -INFINITY;
-#pragma unroll
-      for (int v = 0; v < NW * P; ++v) M = fmaxf(M, merge[v / P * C::MERGE + v % P * TILE + r]);
-      float L = 0.f;
-      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int v = 0; v < NW * P; ++v) {
-        const float* src = merge + v / P * C::MERGE;
-        const int vr = v % P * TILE + r;
-        const float wl = src[ROWS + vr];
-        if (wl == 0.f) continue;  // a row without tokens
-        const float f = ex2_approx(src[vr] - M);
-        const float4 y = *reinterpret_cast<const float4*>(src + 2 * ROWS + vr * C::OROW + x);
-        L = fmaf(wl, f, L);
-        O.x = fmaf(y.x, f, O.x); O.y = fmaf(y.y, f, O.y);
-        O.z = fmaf(y.z, f, O.z); O.w = fmaf(y.w, f, O.w);
-      }
-      const float inv = 1.f / L;
-      O.x *= inv; O.y *= inv; O.z *= inv; O.w *= inv;
-      if (starts && ends) {
-        const int64_t row = static_cast<int64_t>(seg_n) * p.Hq + kvh * G + h0 + r;
-        *reinterpret_cast<uint2*>(p.o + row * D + x) = make_uint2(pack_bf16x2(O.x, O.y), pack_bf16x2(O.z, O.w));
-        if (x == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(L)) * LN2;
-      } else {
-        *reinterpret_cast<float4*>(ws.o + (slot * ROWS + r) * D + x) = O;
-        if (x == 0) {
-          ws.m[slot * ROWS + r] = M;
-          ws.l[slot * ROWS + r] = L;
+        for (int c = 0; c < 2; ++c) {
+          my[2 * t + c] = l[c] == 0.f ? -INFINITY : mc[c];  // no tokens: no part in the maximum
+          my[ROWS + 2 * t + c] = l[c];
         }
       }
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        float* at = my + 2 * ROWS + 2 * t * C::OROW + 16 * x + 2 * g;
+        *reinterpret_cast<float2*>(at) = make_float2(o[x][0] - base[x / 4][0], o[x][2] - base[x / 4][0]);
+        *reinterpret_cast<float2*>(at + C::OROW) = make_float2(o[x][1] - base[x / 4][1], o[x][3] - base[x / 4][1]);
+      }
     }
-    if (starts && !ends) {
-      // the share that holds the sequence's last step: step x lies in share ((x + 1) shares - 1) / W
-      const long long past = lo + seg + cur.ns;
-      cut = make_int4(seg_n, seg_u, static_cast<int>(mul_div(past * shares - 1, 1, W)), 1);
-    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(rec_full);
     seg = seg_end;
-    if (seg < count) {
-      cur.advance(seg_steps, p.seq_lens, N, units, p.max_blocks);
-      named_barrier_sync(1, NW * 32);  // the merge buffer is free again
-    }
+    if (seg < count) cur.advance(seg_steps, p.seq_lens, N, units, p.max_blocks);
   }
-  if (threadIdx.x == 0) ws.desc[b] = cut;
   if (!ok && lane == 0) set_error(&g_decode_q4_status, kDevWaitTimeout);
 }
 
-// One CTA a share: merges the partials of the cut sequence that starts there, if there is one.
-// RS groups of threads take every RS-th partial.
+// One CTA a share: merges the partials of the cut sequence that starts there, if there is one.  Each
+// group of threads merges every RS-th partial, a running maximum with it, so that the loads of its
+// partials are in flight together; then the groups' sums are merged.
 template <int D, int P>
-__global__ void __launch_bounds__(1024) combine_q4_kernel(const DecodeQ4Params p, const Q4Geometry geo) {
+__global__ void __launch_bounds__(COMBINE_THREADS) combine_q4_kernel(const DecodeQ4Params p, const Q4Geometry geo) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int TILE = ROWS / P;
   constexpr int COLS = TILE * D / 4;  // threads that cover the outputs, 4 columns each
-  constexpr int RS = 1024 / COLS;
-  __shared__ float4 s_o[RS > 1 ? RS - 1 : 1][COLS];
-  __shared__ float s_l[RS > 1 ? RS - 1 : 1][COLS];
+  constexpr int RS = COMBINE_THREADS / COLS;
+  constexpr int U = 4;                // partials in flight a thread
+  __shared__ float4 s_o[RS][COLS];
+  __shared__ float s_m[RS][COLS], s_l[RS][COLS];
   const Workspace ws = carve<D>(p.workspace, geo.grid);
   const int4 d = ws.desc[blockIdx.x];
   if (d.w == 0) return;
@@ -604,34 +726,53 @@ __global__ void __launch_bounds__(1024) combine_q4_kernel(const DecodeQ4Params p
   const int r = col / (D / 4), x = col % (D / 4) * 4;
   const int first = blockIdx.x;
   const int count = d.z - first + 1;
-  // partial j: the cut sequence's start, then the shares that continue it
-  auto slot_of = [&](int j) { return static_cast<int64_t>(j == 0 ? 2 * first + 1 : 2 * (first + j)) * ROWS + r; };
   float M = -INFINITY, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float m, float l, const float4& y) {
+    const float to = fmaxf(M, m);
+    // a group without partials, M = m = -inf, has nothing to scale; a maximum of -inf otherwise comes of NaN
+    const float fo = M == -INFINITY ? 0.f : ex2_approx(M - to), fn = m == -INFINITY ? l : l * ex2_approx(m - to);
+    M = to;
+    L = fmaf(L, fo, fn);
+    O.x = fmaf(O.x, fo, y.x * fn); O.y = fmaf(O.y, fo, y.y * fn);
+    O.z = fmaf(O.z, fo, y.z * fn); O.w = fmaf(O.w, fo, y.w * fn);
+  };
   if (r < heads) {
-    for (int j = 0; j < count; ++j) M = fmaxf(M, ws.m[slot_of(j)]);
-#pragma unroll 4
-    for (int j = grp; j < count; j += RS) {
-      const int64_t s = slot_of(j);
-      const float f = ws.l[s] * ex2_approx(ws.m[s] - M);
-      const float4 y = *reinterpret_cast<const float4*>(ws.o + s * D + x);
-      L += f;
-      O.x = fmaf(y.x, f, O.x); O.y = fmaf(y.y, f, O.y);
-      O.z = fmaf(y.z, f, O.z); O.w = fmaf(y.w, f, O.w);
+    for (int j0 = grp; j0 < count; j0 += RS * U) {
+      float m[U], l[U];
+      float4 y[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int j = j0 + k * RS;
+        if (j >= count) break;
+        // partial j: the cut sequence's start, then the shares that continue it
+        const int64_t s = static_cast<int64_t>(j == 0 ? 2 * first + 1 : 2 * (first + j)) * ROWS + r;
+        m[k] = ws.m[s];
+        l[k] = ws.l[s];
+        y[k] = *reinterpret_cast<const float4*>(ws.o + s * D + x);
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (j0 + k * RS < count) add(m[k], l[k], y[k]);
     }
   }
   if constexpr (RS > 1) {
-    if (grp > 0) {
-      s_o[grp - 1][col] = O;
-      s_l[grp - 1][col] = L;
-    }
+    s_m[grp][col] = M;
+    s_l[grp][col] = L;
+    // the groups' sums are not normalised: they enter with weight 1 at their maximum
+    s_o[grp][col] = O;
     __syncthreads();
     if (grp > 0) return;
 #pragma unroll
-    for (int j = 0; j < RS - 1; ++j) {
-      const float4 y = s_o[j][col];
-      L += s_l[j][col];
-      O.x += y.x; O.y += y.y; O.z += y.z; O.w += y.w;
+    for (int k = 1; k < RS; ++k) {
+      if (k >= count) break;
+      const float m = s_m[k][col], to = fmaxf(M, m);
+      const float fo = ex2_approx(M - to), fn = ex2_approx(m - to);
+      const float4 y = s_o[k][col];
+      M = to;
+      L = L * fo + s_l[k][col] * fn;
+      O.x = O.x * fo + y.x * fn; O.y = O.y * fo + y.y * fn;
+      O.z = O.z * fo + y.z * fn; O.w = O.w * fo + y.w * fn;
     }
   }
   if (r >= heads) return;
@@ -670,7 +811,7 @@ cudaError_t launch(const DecodeQ4Params& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(geo.grid);
-  cfg.blockDim = dim3(1024);
+  cfg.blockDim = dim3(COMBINE_THREADS);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
