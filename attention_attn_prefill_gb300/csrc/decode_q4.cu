@@ -41,7 +41,7 @@ using q4::Record;
 
 constexpr float LN2 = 0.693147180559945309f;
 #ifndef TSEG
-#define TSEG 4
+#define TSEG 10
 #endif
 constexpr int SEGMENT = TSEG;
 constexpr int COMBINE_THREADS = 512;
@@ -59,16 +59,16 @@ struct Cfg {
 #ifndef TNW
 #define TNW 7
 #endif
-#ifndef TSLEEP
-#define TSLEEP 100
+#ifndef TNW256
+#define TNW256 5
 #endif
-#ifndef TPIPE
-#define TPIPE 0
+#ifndef TQ
+#define TQ 0
 #endif
 #ifndef TDEPTH
 #define TDEPTH 3
 #endif
-  static constexpr int NW = D == 256 ? 5 : D == 128 ? TNW : 7;  // warps that compute (one more loads)
+  static constexpr int NW = D == 256 ? (P == 2 ? 4 : TNW256) : D == 128 ? TNW : 7;  // warps that compute (one more loads)
   static constexpr int CTAS = 2;                   // CTAs an SM
   static constexpr int THREADS = (NW + 1) * 32;
   static constexpr int TILE = ROWS / P;            // query heads a tile
@@ -552,31 +552,16 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
         }
       }
     };
-    // the stage of this warp's next step, once its copy has landed
-    auto next_stage = [&]() {
+    for (; i < seg_end; i += NW) {
       const int slot = warp + NW * stage_k;
       ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[slot], phase));
       if (++stage_k == C::DEPTH) {
         stage_k = 0;
         phase ^= 1;
       }
-      return slot;
-    };
-
-    float sc[4];
-    int slot = 0;
-    if (TPIPE && i < seg_end) {
-      slot = next_stage();
-      if (ok) scores(smem + slot * C::STAGE, sc);
-    }
-    for (; i < seg_end; i += NW) {
-      // the next step's scores are computed beside this step's product with V, whose operand waits for a
-      // chain of short steps (exponential, rounding, transpose); after the last step they are not used
-      int ahead = slot;
-      if (TPIPE) { if (i + NW < seg_end) ahead = next_stage(); }
-      else slot = next_stage();
       if (!ok) continue;
-      if (!TPIPE) scores(smem + slot * C::STAGE, sc);
+      float sc[4];
+      scores(smem + slot * C::STAGE, sc);
       const uint8_t* stage = smem + slot * C::STAGE;
       // tokens of this lane's page that the sequence has; the last step's second page may have none
       const int valid = len - ((first_step + i - seg) * P + my_page) * PAGE;
@@ -619,7 +604,6 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
       }
       l[0] += pr[0] + pr[2];
       l[1] += pr[1] + pr[3];
-      if (TPIPE) scores(smem + ahead * C::STAGE, sc);
       // ---- O^T += V^T (p s)^T.  Two pages: columns 0 .. 3 of a page's product are its upper parts, 4 .. 7
       // its lower ones, which the lanes of columns 4 .. 7 and 0 .. 3 swap.
 #pragma unroll
@@ -656,7 +640,6 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[slot]);
-      if (TPIPE) slot = ahead;
     }
 
     // ---- this warp's state to shared memory, then the CTA's to global memory.  With two pages, a head's
