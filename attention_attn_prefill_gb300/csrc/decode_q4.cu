@@ -2,17 +2,21 @@
 //
 // With K = s_g (c - z_g) and V likewise, per group g of 64 channels,
 //   score = sum_g s_g (q . c - z_g sum q),     O = sum_tokens p s c - sum_tokens p s z,
-// so the codes themselves are the matrix operands: a code becomes a bf16 number by one mask and one
-// or (16 + c, exact, its nibble on the upper mantissa bits), and scales and zero points are applied
-// to the 16 scores of a page's token tile and to its 16 probabilities, not to the d values of a token.
+// so the codes themselves are the matrix operands, and scales and zero points are applied to the scores of
+// a page's 16 tokens and to their probabilities, not to the d values of a token.  Decoding is what the
+// arithmetic pipe is busy with; a word of eight codes costs
+//   K, as bf16 (the queries are): a mask and an or each, the nibble on the upper mantissa bits of 16.0,
+//     and three rotations;
+//   V, as fp16: a mask and an or each on 1024 or 64, whose mantissas take two nibbles without a shift,
+//     one shift, and a subtraction in the float pipe, which leaves c - 8.
+// p s enters that product as one fp16 number: 11 bits, off by 2^-12 at most, an eighth of the output's own
+// rounding (a bf16 one would double the output's error).  fp16's range is kept by a power of two common
+// to a warp's columns, moved when a scale grows past it, as the reference maximum is for p.
 //
 // Both products have the codes as the left operand, S^T = K Q^T and O^T = V^T P^T: their four registers
-// are the decoded words themselves, and 8 columns hold the query heads of a KV head.  p s is split into
-// two bf16 numbers (16 bits together): one alone would add an error as large as the output's own
-// rounding.  With up to four heads, a step takes two pages: the score columns hold the heads of both,
-// so that one round of exponentials and roundings serves both, and the columns of a page's product with
-// V hold the upper parts of p s and the lower ones.  Odd tokens of V enter as c - 31 (one exclusive-or
-// instead of the or), so that the offsets of the codes cancel in the running sums.
+// are the decoded words themselves, and 8 columns hold the query heads of a KV head.  With up to four
+// heads, a step takes two pages and the columns hold the heads of both, so that one round of
+// exponentials and roundings serves both; a page's product with V has zeros in the other page's columns.
 //
 // Work: the (sequence, KV head, step) list is cut into contiguous shares of equal weight, one a CTA; the
 // CTA's computing warps deal its steps among themselves.  One more warp requests the records (one
@@ -22,6 +26,7 @@
 // dependent, merges the partials of each cut sequence.  At most two partials a CTA, so the workspace
 // does not depend on the batch.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -40,6 +45,9 @@ using q4::PAGE;
 using q4::Record;
 
 constexpr float LN2 = 0.693147180559945309f;
+#ifndef TSL
+#define TSL 50
+#endif
 #ifndef TSEG
 #define TSEG 10
 #endif
@@ -48,10 +56,11 @@ constexpr int COMBINE_THREADS = 512;
 constexpr int ROWS = 8;                       // score columns of a warp: query heads, or heads of two pages
 constexpr uint32_t CODE_MASK = 0x00780078u;   // a nibble on mantissa bits 3..6 of both halves
 constexpr uint32_t K_MAGIC = 0x41804180u;     // 16 + c in both halves
-constexpr uint32_t V_MAGIC = 0xc1f84180u;     // 16 + c in the lower half (an even token), c - 31 in the upper one
+constexpr uint32_t V_MASK0 = 0x000f000fu, V_MAGIC0 = 0x64006400u;  // fp16: 1024 + c
+constexpr uint32_t V_MASK1 = 0x00f000f0u, V_MAGIC1 = 0x54005400u;  // 64 + c
+constexpr uint32_t V_ROOM = 6;                // powers of two a scale may grow by before the common one moves
 constexpr float P_LIMIT = 256.f;              // a probability above it moves the reference maximum
-constexpr uint32_t Z_MASK = 0x00780000u;      // a zero point on the same bits of a float: 16 + z, z - 31
-constexpr uint32_t Z_EVEN = 0x41800000u, Z_ODD = 0xc1f80000u;
+constexpr uint32_t Z_MASK = 0x00780000u, Z_MAGIC = 0x41800000u;  // a zero point on the same bits of a float: 16 + z
 
 // P: pages a warp takes at a step; ROWS / P query heads.
 template <int D, int P>
@@ -93,9 +102,9 @@ __device__ __forceinline__ long long mul_div(long long a, long long b, long long
 
 struct Q4Geometry {
   int grid, tiles, units;  // CTAs, head tiles a KV head, (KV head, tile) pairs a sequence
-  // K_MAGIC and V_MAGIC as arguments: a constant that the compiler knows would not stay in a register,
-  // and decoding a word half would take two instructions
-  uint32_t k_magic, v_magic;
+  // the magic numbers as arguments: a constant that the compiler knows would not stay in a register, and
+  // decoding would take two instructions for the mask and the or
+  uint32_t k_magic, v_magic0, v_magic1;
 };
 
 // What the workspace holds: the shares' descriptors, then the partials' o, m and l.
@@ -115,19 +124,36 @@ __device__ Workspace carve(void* ws, int grid) {
   return w;
 }
 
+template <bool F16>
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// (w & CODE_MASK) ^ magic
-__device__ __forceinline__ uint32_t decode(uint32_t w, uint32_t magic) {
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t mask_or(uint32_t w, uint32_t magic) {
   uint32_t x;
-  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(x) : "r"(w), "n"(CODE_MASK), "r"(magic));
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w), "n"(MASK), "r"(magic));
   return x;
+}
+
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t x, uint32_t y) {
+  uint32_t d;
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(y));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
 }
 
 // transposes an 8 x 8 tile of 16-bit values held as an accumulator's pairs
@@ -196,9 +222,16 @@ struct Params {
   __device__ __forceinline__ float scale(int e) const {
     return __uint_as_float((e % 2 ? w[e / 2] : w[e / 2] << 16) & 0xfff00000u);
   }
-  // the zero point z as `magic` makes a float of it: 16 + z or z - 31
-  __device__ __forceinline__ float zero(int e, uint32_t magic) const {
-    return __uint_as_float(((e % 2 ? w[e / 2] << 3 : w[e / 2] << 19) & Z_MASK) ^ magic);
+  // the zero point, 16 + z
+  __device__ __forceinline__ float zero(int e) const {
+    return __uint_as_float(((e % 2 ? w[e / 2] << 3 : w[e / 2] << 19) & Z_MASK) | Z_MAGIC);
+  }
+  // the largest word of a finite scale, compared as the scales are (the zero point below them)
+  __device__ __forceinline__ uint32_t largest() const {
+    uint32_t m = w[0];
+#pragma unroll
+    for (int i = 1; i < WORDS; ++i) m = __vmaxu2(m, w[i]);
+    return max(m >> 16, m & 0xffffu);
   }
 };
 
@@ -428,7 +461,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
       if (__any_sync(0xffffffffu, go) || merge_now) {
         since = global_timer_ns();
       } else {
-        __nanosleep(50);
+        __nanosleep(TSL);
         ok = __all_sync(0xffffffffu, global_timer_ns() - since < ATTN_WAIT_LIMIT_NS);
       }
     }
@@ -447,7 +480,6 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
   const int g = lane >> 2, t = lane & 3;
   const int q_row = P == 2 ? g & 3 : g;     // the query head of the tile that this lane loads: column g
   const int my_page = P == 2 ? t >> 1 : 0;  // columns 2 t and 2 t + 1 are two heads of this page of the step
-  const uint32_t z_magic = g & 1 ? Z_ODD : Z_EVEN;  // of tokens g and g + 8 of V
   const float c2 = p.scale_log2;
   bool ok = true;
   int i = warp;    // share index of this warp's next step
@@ -489,7 +521,10 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
 
     float mc[2] = {-1e38f, -1e38f};  // of columns 2 t, 2 t + 1: the reference maximum, in log2 units
     float l[2] = {0.f, 0.f};         // this lane's share of the sum of probabilities
-    float base[NG][2];               // sum of p s (16 + z) or p s (z - 31) over this lane's tokens
+    float base[NG][2];               // sum of p s (z - 8) over this lane's tokens
+    float v_unit = 0.f;              // s enters o and base times this power of two, 2^(127 - v_exp)
+    uint32_t v_exp = 0;
+    uint32_t v_most = 15;            // the largest parameter word that fits it (none at first)
     float o[D / 16][4];              // channels 16 i + 2 g (0, 1) and + 1 (2, 3) of columns 2 t and 2 t + 1
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
@@ -532,17 +567,18 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
               const int e = pr * R::PAIR + ee, h = k / 2, s = k % 2 * 2;
               const uint32_t w0 = kw[a][0][ee * 2 + h], w1 = kw[a][1][ee * 2 + h];
               if (k == 0) acc[ee][a][0] = acc[ee][a][1] = acc[ee][a][2] = acc[ee][a][3] = 0.f;
-              mma_16816(acc[ee][a], decode(__funnelshift_r(w0, w0, 4 * s), geo.k_magic),
-                        decode(__funnelshift_r(w1, w1, 4 * s), geo.k_magic),
-                        decode(__funnelshift_r(w0, w0, 4 * s + 4), geo.k_magic),
-                        decode(__funnelshift_r(w1, w1, 4 * s + 4), geo.k_magic), qb[e][h][s], qb[e][h][s + 1]);
+              mma_16816<false>(acc[ee][a], mask_or<CODE_MASK>(__funnelshift_r(w0, w0, 4 * s), geo.k_magic),
+                               mask_or<CODE_MASK>(__funnelshift_r(w1, w1, 4 * s), geo.k_magic),
+                               mask_or<CODE_MASK>(__funnelshift_r(w0, w0, 4 * s + 4), geo.k_magic),
+                               mask_or<CODE_MASK>(__funnelshift_r(w1, w1, 4 * s + 4), geo.k_magic), qb[e][h][s],
+                               qb[e][h][s + 1]);
             }
 #pragma unroll
         for (int ee = 0; ee < R::PAIR; ++ee) {
           const int e = pr * R::PAIR + ee;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float s = kp[j].scale(e), z = kp[j].zero(e, Z_EVEN);
+            const float s = kp[j].scale(e), z = kp[j].zero(e);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const float x = P == 2 && my_page ? acc[ee][P - 1][2 * j + c] : acc[ee][0][2 * j + c];
@@ -587,7 +623,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          if (P == 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));  // a head's two pages share the reference
+          if (P == 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));  // a head's two pages share it
           const float to = fmaxf(mc[c], mx * c2), f = ex2_approx(mc[c] - to);
           mc[c] = to;
           l[c] *= f;
@@ -604,37 +640,60 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
       }
       l[0] += pr[0] + pr[2];
       l[1] += pr[1] + pr[3];
-      // ---- O^T += V^T (p s)^T.  Two pages: columns 0 .. 3 of a page's product are its upper parts, 4 .. 7
-      // its lower ones, which the lanes of columns 4 .. 7 and 0 .. 3 swap.
+      const uint32_t largest = max(vp[0].largest(), vp[1].largest());
+      if (__any_sync(0xffffffffu, largest > v_most)) {
+        // a NaN scale says nothing about the others' range
+        uint32_t mine = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < NG; ++e) {
+            const uint32_t s = __float_as_uint(vp[j].scale(e)) >> 23;
+            if (s < 255) mine = max(mine, s);
+          }
+        const uint32_t to = __reduce_max_sync(0xffffffffu, mine);
+        if (v_unit == 0.f || to > v_exp) {
+          const float unit = __uint_as_float((254u - to) << 23), f = v_unit == 0.f ? 0.f : unit / v_unit;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int e = 0; e < NG; ++e) base[e][c] *= f;
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+              o[x][c] *= f;
+              o[x][2 + c] *= f;
+            }
+          }
+          v_unit = unit;
+          v_exp = to;
+          v_most = min((to + V_ROOM) << 7 | 127u, 0x7f7fu);
+        }
+      }
+      // ---- O^T += V^T (p s)^T
 #pragma unroll
       for (int e = 0; e < NG; ++e) {
-        uint32_t pb[2][2];  // [page, or upper and lower part][tokens 0 .. 7, 8 .. 15]
+        uint32_t pb[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float s = vp[j].scale(e), z = vp[j].zero(e, z_magic);
+          const float s = vp[j].scale(e) * v_unit, z = vp[j].zero(e) - 24.f;
           const float x0 = pr[2 * j] * s, x1 = pr[2 * j + 1] * s;
           base[e][0] = fmaf(x0, z, base[e][0]);
           base[e][1] = fmaf(x1, z, base[e][1]);
-          uint32_t hi = pack_bf16x2(x0, x1);
-          uint32_t lo_ = pack_bf16x2(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
-          if (P == 2) {
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, my_page ? hi : lo_, 2);
-            if (my_page) hi = got; else lo_ = got;
-          }
-          pb[0][j] = transpose_8x8(hi);
-          pb[1][j] = transpose_8x8(lo_);
+          pb[j] = transpose_8x8(pack_f16x2(x0, x1));
         }
 #pragma unroll
         for (int a = 0; a < P; ++a) {
+          const bool on = P == 1 || (g >> 2) == a;  // as an operand, this lane holds column g
+          const uint32_t b0 = on ? pb[0] : 0u, b1 = on ? pb[1] : 0u;
           const uint4 vw = *reinterpret_cast<const uint4*>(stage + a * R::BYTES + R::V_OFF + (e * 32 + lane) * 16);
           const uint32_t w4[4] = {vw.x, vw.y, vw.z, vw.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t w = w4[j];
-            const uint32_t a0 = decode(w << 3, geo.v_magic), a1 = decode(w >> 1, geo.v_magic);
-            const uint32_t a2 = decode(w >> 5, geo.v_magic), a3 = decode(w >> 9, geo.v_magic);
-            mma_16816(o[e * 4 + j], a0, a1, a2, a3, pb[a][0], pb[a][1]);
-            if (P == 1) mma_16816(o[e * 4 + j], a0, a1, a2, a3, pb[1][0], pb[1][1]);
+            const uint32_t w = w4[j], w8 = w >> 8;
+            mma_16816<true>(o[e * 4 + j], sub_f16x2(mask_or<V_MASK0>(w, geo.v_magic0), 0x64086408u),
+                            sub_f16x2(mask_or<V_MASK1>(w, geo.v_magic1), 0x54805480u),
+                            sub_f16x2(mask_or<V_MASK0>(w8, geo.v_magic0), 0x64086408u),
+                            sub_f16x2(mask_or<V_MASK1>(w8, geo.v_magic1), 0x54805480u), b0, b1);
           }
         }
       }
@@ -659,6 +718,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[x][j] += __shfl_xor_sync(0xffffffffu, o[x][j], 2);
     }
+    const float v_back = v_exp > 0 ? __uint_as_float(v_exp << 23) : 5.877471754111438e-39f;  // 2^(v_exp - 127)
     // the loading warp has merged the segment before this one
     if (seg > 0) {
       ok = __all_sync(0xffffffffu, mbar_wait(rec_free, free_phase)) && ok;
@@ -676,8 +736,10 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
 #pragma unroll
       for (int x = 0; x < D / 16; ++x) {
         float* at = my + 2 * ROWS + 2 * t * C::OROW + 16 * x + 2 * g;
-        *reinterpret_cast<float2*>(at) = make_float2(o[x][0] - base[x / 4][0], o[x][2] - base[x / 4][0]);
-        *reinterpret_cast<float2*>(at + C::OROW) = make_float2(o[x][1] - base[x / 4][1], o[x][3] - base[x / 4][1]);
+        *reinterpret_cast<float2*>(at) =
+            make_float2((o[x][0] - base[x / 4][0]) * v_back, (o[x][2] - base[x / 4][0]) * v_back);
+        *reinterpret_cast<float2*>(at + C::OROW) =
+            make_float2((o[x][1] - base[x / 4][1]) * v_back, (o[x][3] - base[x / 4][1]) * v_back);
       }
     }
     __syncwarp();
@@ -783,7 +845,8 @@ cudaError_t launch(const DecodeQ4Params& p, cudaStream_t stream) {
   geo.tiles = (p.Hq / p.Hkv + C::TILE - 1) / C::TILE;
   geo.units = p.Hkv * geo.tiles;
   geo.k_magic = K_MAGIC;
-  geo.v_magic = V_MAGIC;
+  geo.v_magic0 = V_MAGIC0;
+  geo.v_magic1 = V_MAGIC1;
   auto kern = decode_q4_kernel<D, P>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
   if (e != cudaSuccess) return e;
