@@ -10,8 +10,8 @@
 //   V, as fp16: a mask and an or each on 1024 or 64, whose mantissas take two nibbles without a shift,
 //     one shift, and a subtraction in the float pipe, which leaves c - 8.
 // p s enters that product as one fp16 number: 11 bits, off by 2^-12 at most, an eighth of the output's own
-// rounding (a bf16 one would double the output's error).  fp16's range is kept by a power of two common
-// to a warp's columns, moved when a scale grows past it, as the reference maximum is for p.
+// rounding (a bf16 one would double the output's error).  fp16's range is kept by a power of two for each
+// group of channels of a warp, moved when a scale grows past it, as the reference maximum is for p.
 //
 // Both products have the codes as the left operand, S^T = K Q^T and O^T = V^T P^T: their four registers
 // are the decoded words themselves, and 8 columns hold the query heads of a KV head.  With up to four
@@ -29,6 +29,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "cache_q4.cuh"
@@ -45,43 +46,29 @@ using q4::PAGE;
 using q4::Record;
 
 constexpr float LN2 = 0.693147180559945309f;
-#ifndef TSL
-#define TSL 50
-#endif
-#ifndef TSEG
-#define TSEG 10
-#endif
-constexpr int SEGMENT = TSEG;
-constexpr int COMBINE_THREADS = 512;
+constexpr int SEGMENT = 10;                   // steps that starting on a (sequence, unit) and leaving it cost
 constexpr int ROWS = 8;                       // score columns of a warp: query heads, or heads of two pages
 constexpr uint32_t CODE_MASK = 0x00780078u;   // a nibble on mantissa bits 3..6 of both halves
 constexpr uint32_t K_MAGIC = 0x41804180u;     // 16 + c in both halves
 constexpr uint32_t V_MASK0 = 0x000f000fu, V_MAGIC0 = 0x64006400u;  // fp16: 1024 + c
 constexpr uint32_t V_MASK1 = 0x00f000f0u, V_MAGIC1 = 0x54005400u;  // 64 + c
-constexpr uint32_t V_ROOM = 6;                // powers of two a scale may grow by before the common one moves
-constexpr float P_LIMIT = 256.f;              // a probability above it moves the reference maximum
+// p s is at most P_LIMIT * 2^(V_BITS + V_ROOM + 1) = 2^15 as fp16, whose largest number is 65504, and keeps its
+// 11 bits down to 2^-20 of the group's largest s (for p = 1)
+constexpr float P_LIMIT = 64.f;               // a probability above it moves the reference maximum
+constexpr uint32_t V_BITS = 6;                // where a group's unit puts the largest scale
+constexpr uint32_t V_ROOM = 2;                // powers of two a scale may grow by before the unit moves
 constexpr uint32_t Z_MASK = 0x00780000u, Z_MAGIC = 0x41800000u;  // a zero point on the same bits of a float: 16 + z
 
 // P: pages a warp takes at a step; ROWS / P query heads.
 template <int D, int P>
 struct Cfg {
-#ifndef TNW
-#define TNW 7
-#endif
-#ifndef TNW256
-#define TNW256 5
-#endif
-#ifndef TQ
-#define TQ 0
-#endif
-#ifndef TDEPTH
-#define TDEPTH 3
-#endif
-  static constexpr int NW = D == 256 ? (P == 2 ? 4 : TNW256) : D == 128 ? TNW : 7;  // warps that compute (one more loads)
+  // warps that compute; one more loads.  What shared memory holds with three steps in flight a warp
+  // (four warps for d = 256: 75 us at 8 sequences of 58000, 16/2 heads, against 77 with five)
+  static constexpr int NW = D == 256 ? 4 : 7;
   static constexpr int CTAS = 2;                   // CTAs an SM
   static constexpr int THREADS = (NW + 1) * 32;
   static constexpr int TILE = ROWS / P;            // query heads a tile
-  static constexpr int DEPTH = D == 256 ? (P == 2 ? 2 : 3) : D == 128 ? TDEPTH : 3;             // steps in flight a warp
+  static constexpr int DEPTH = D == 256 && P == 2 ? 2 : 3;  // steps in flight a warp (two: 73 us for 70, d = 128)
   static constexpr int SLOTS = NW * DEPTH;
   static constexpr int STAGE = (P * Record<D>::BYTES + 127) & ~127;
   static constexpr int OROW = D + 8;               // floats of a row in the merge buffer
@@ -101,7 +88,9 @@ __device__ __forceinline__ long long mul_div(long long a, long long b, long long
 }
 
 struct Q4Geometry {
-  int grid, tiles, units;  // CTAs, head tiles a KV head, (KV head, tile) pairs a sequence
+  int grid;          // CTAs
+  int tile;          // query heads a tile
+  int tiles, units;  // tiles a KV head, (KV head, tile) pairs a sequence
   // the magic numbers as arguments: a constant that the compiler knows would not stay in a register, and
   // decoding would take two instructions for the mask and the or
   uint32_t k_magic, v_magic0, v_magic1;
@@ -226,13 +215,6 @@ struct Params {
   __device__ __forceinline__ float zero(int e) const {
     return __uint_as_float(((e % 2 ? w[e / 2] << 3 : w[e / 2] << 19) & Z_MASK) | Z_MAGIC);
   }
-  // the largest word of a finite scale, compared as the scales are (the zero point below them)
-  __device__ __forceinline__ uint32_t largest() const {
-    uint32_t m = w[0];
-#pragma unroll
-    for (int i = 1; i < WORDS; ++i) m = __vmaxu2(m, w[i]);
-    return max(m >> 16, m & 0xffffu);
-  }
 };
 
 template <int D, int P>
@@ -240,6 +222,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
     decode_q4_kernel(const DecodeQ4Params p, const Q4Geometry geo) {
   using C = Cfg<D, P>;
   using R = Record<D>;
+  using VP = Params<R::NG>;
   constexpr int NW = C::NW, NG = R::NG, THREADS = C::THREADS, TILE = C::TILE, SLOTS = C::SLOTS;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_weight[NW + 1], s_steps[NW + 1], s_end[2], s_at;
@@ -300,8 +283,9 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
     steps += s_steps[i];
   }
   const long long W = weight * units;
-  // at least a step for each warp of a share
-  const long long most = steps * units / NW;
+  // Short lists make fewer shares than CTAs: of one step, they would only be more partials to merge (a
+  // sequence of 16 tokens: 10 us with two steps a share, 13 with four, 20 with seven)
+  const long long most = steps * units / 2;
   const long long shares = most >= geo.grid ? geo.grid : most < 1 ? 1 : most;
   const int b = blockIdx.x;
   const long long lo = b < shares ? mul_div(b, W, shares) : W, hi = b < shares ? mul_div(b + 1, W, shares) : W;
@@ -461,7 +445,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
       if (__any_sync(0xffffffffu, go) || merge_now) {
         since = global_timer_ns();
       } else {
-        __nanosleep(TSL);
+        __nanosleep(50);
         ok = __all_sync(0xffffffffu, global_timer_ns() - since < ATTN_WAIT_LIMIT_NS);
       }
     }
@@ -522,14 +506,15 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
     float mc[2] = {-1e38f, -1e38f};  // of columns 2 t, 2 t + 1: the reference maximum, in log2 units
     float l[2] = {0.f, 0.f};         // this lane's share of the sum of probabilities
     float base[NG][2];               // sum of p s (z - 8) over this lane's tokens
-    float v_unit = 0.f;              // s enters o and base times this power of two, 2^(127 - v_exp)
-    uint32_t v_exp = 0;
-    uint32_t v_most = 15;            // the largest parameter word that fits it (none at first)
+    float v_unit[NG];                // s enters o and base times this power of two; 0: no scale seen yet
+    uint32_t v_most[VP::WORDS];      // the largest parameter words that fit it, two groups a word
     float o[D / 16][4];              // channels 16 i + 2 g (0, 1) and + 1 (2, 3) of columns 2 t and 2 t + 1
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
 #pragma unroll
-    for (int e = 0; e < NG; ++e) base[e][0] = base[e][1] = 0.f;
+    for (int e = 0; e < NG; ++e) base[e][0] = base[e][1] = v_unit[e] = 0.f;
+#pragma unroll
+    for (int x = 0; x < VP::WORDS; ++x) v_most[x] = 0x000f000fu;  // a scale of 0 and any zero point
 
     // S^T of a step whose records are at `stage`: rows are tokens g (0, 1) and g + 8 (2, 3), columns 2 t and
     // 2 t + 1
@@ -640,33 +625,33 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
       }
       l[0] += pr[0] + pr[2];
       l[1] += pr[1] + pr[3];
-      const uint32_t largest = max(vp[0].largest(), vp[1].largest());
-      if (__any_sync(0xffffffffu, largest > v_most)) {
-        // a NaN scale says nothing about the others' range
-        uint32_t mine = 0;
+      bool grown = false;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+      for (int x = 0; x < VP::WORDS; ++x)
+        grown |= __vmaxu2(__vmaxu2(vp[0].w[x], vp[1].w[x]), v_most[x]) != v_most[x];
+      if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-          for (int e = 0; e < NG; ++e) {
-            const uint32_t s = __float_as_uint(vp[j].scale(e)) >> 23;
-            if (s < 255) mine = max(mine, s);
-          }
-        const uint32_t to = __reduce_max_sync(0xffffffffu, mine);
-        if (v_unit == 0.f || to > v_exp) {
-          const float unit = __uint_as_float((254u - to) << 23), f = v_unit == 0.f ? 0.f : unit / v_unit;
+        for (int e = 0; e < NG; ++e) {
+          // exponents; a NaN scale says nothing about the others' range
+          const uint32_t s0 = __float_as_uint(vp[0].scale(e)) >> 23, s1 = __float_as_uint(vp[1].scale(e)) >> 23;
+          uint32_t to = __reduce_max_sync(0xffffffffu, max(s0 < 255 ? s0 : 0u, s1 < 255 ? s1 : 0u));
+          if (to == 0 && v_unit[e] == 0.f) continue;
+          to = max(to, V_BITS + 1);
+          const float unit = __uint_as_float((254 + V_BITS - to) << 23);  // the largest scale: [2^V_BITS, 2 of it)
+          if (v_unit[e] != 0.f && unit >= v_unit[e]) continue;
+          const float f = v_unit[e] == 0.f ? 0.f : unit / v_unit[e];
+          v_unit[e] = unit;
+          const uint32_t most = min((to + V_ROOM) << 7 | 127u, 0x7f7fu);
+          v_most[e / 2] = e % 2 ? (v_most[e / 2] & 0xffffu) | most << 16 : (v_most[e / 2] & 0xffff0000u) | most;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
+            base[e][c] *= f;
 #pragma unroll
-            for (int e = 0; e < NG; ++e) base[e][c] *= f;
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
+            for (int x = 4 * e; x < 4 * e + 4; ++x) {
               o[x][c] *= f;
               o[x][2 + c] *= f;
             }
           }
-          v_unit = unit;
-          v_exp = to;
-          v_most = min((to + V_ROOM) << 7 | 127u, 0x7f7fu);
         }
       }
       // ---- O^T += V^T (p s)^T
@@ -675,11 +660,14 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
         uint32_t pb[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float s = vp[j].scale(e) * v_unit, z = vp[j].zero(e) - 24.f;
+          const float s = vp[j].scale(e) * v_unit[e], z = vp[j].zero(e) - 24.f;
           const float x0 = pr[2 * j] * s, x1 = pr[2 * j + 1] * s;
-          base[e][0] = fmaf(x0, z, base[e][0]);
-          base[e][1] = fmaf(x1, z, base[e][1]);
-          pb[j] = transpose_8x8(pack_f16x2(x0, x1));
+          // the rounded product in both sums, so that a code equal to its zero point stands for exactly 0
+          const uint32_t xh = pack_f16x2(x0, x1);
+          const float2 xf = __half22float2(*reinterpret_cast<const __half2*>(&xh));
+          base[e][0] = fmaf(xf.x, z, base[e][0]);
+          base[e][1] = fmaf(xf.y, z, base[e][1]);
+          pb[j] = transpose_8x8(xh);
         }
 #pragma unroll
         for (int a = 0; a < P; ++a) {
@@ -718,7 +706,9 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[x][j] += __shfl_xor_sync(0xffffffffu, o[x][j], 2);
     }
-    const float v_back = v_exp > 0 ? __uint_as_float(v_exp << 23) : 5.877471754111438e-39f;  // 2^(v_exp - 127)
+    float v_back[NG];  // 1 / v_unit
+#pragma unroll
+    for (int e = 0; e < NG; ++e) v_back[e] = __uint_as_float((254u << 23) - __float_as_uint(v_unit[e]));
     // the loading warp has merged the segment before this one
     if (seg > 0) {
       ok = __all_sync(0xffffffffu, mbar_wait(rec_free, free_phase)) && ok;
@@ -737,9 +727,9 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
       for (int x = 0; x < D / 16; ++x) {
         float* at = my + 2 * ROWS + 2 * t * C::OROW + 16 * x + 2 * g;
         *reinterpret_cast<float2*>(at) =
-            make_float2((o[x][0] - base[x / 4][0]) * v_back, (o[x][2] - base[x / 4][0]) * v_back);
+            make_float2((o[x][0] - base[x / 4][0]) * v_back[x / 4], (o[x][2] - base[x / 4][0]) * v_back[x / 4]);
         *reinterpret_cast<float2*>(at + C::OROW) =
-            make_float2((o[x][1] - base[x / 4][1]) * v_back, (o[x][3] - base[x / 4][1]) * v_back);
+            make_float2((o[x][1] - base[x / 4][1]) * v_back[x / 4], (o[x][3] - base[x / 4][1]) * v_back[x / 4]);
       }
     }
     __syncwarp();
@@ -750,79 +740,77 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
   if (!ok && lane == 0) set_error(&g_decode_q4_status, kDevWaitTimeout);
 }
 
-// One CTA a share: merges the partials of the cut sequence that starts there, if there is one.  Each
-// group of threads merges every RS-th partial, a running maximum with it, so that the loads of its
-// partials are in flight together; then the groups' sums are merged.
-template <int D, int P>
-__global__ void __launch_bounds__(COMBINE_THREADS) combine_q4_kernel(const DecodeQ4Params p, const Q4Geometry geo) {
+// Merges the partials of the cut sequence that starts in a share, if there is one: a CTA of T threads takes
+// HEADS query heads of share blockIdx.x.  Each of RS groups of threads takes every RS-th partial, U of
+// them in flight at a time, with a running maximum; then the groups' sums are merged.
+template <int D, int HEADS, int T>
+__global__ void __launch_bounds__(T) combine_q4_kernel(const DecodeQ4Params p, const Q4Geometry geo) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int TILE = ROWS / P;
-  constexpr int COLS = TILE * D / 4;  // threads that cover the outputs, 4 columns each
-  constexpr int RS = COMBINE_THREADS / COLS;
-  constexpr int U = 4;                // partials in flight a thread
+  constexpr int COLS = HEADS * D / 4;  // threads that cover the heads' outputs, 4 columns each
+  constexpr int RS = T / COLS;
+  constexpr int U = RS > 4 ? 4 : 8;
   __shared__ float4 s_o[RS][COLS];
-  __shared__ float s_m[RS][COLS], s_l[RS][COLS];
+  __shared__ float s_m[RS][HEADS], s_l[RS][HEADS];
   const Workspace ws = carve<D>(p.workspace, geo.grid);
-  const int4 d = ws.desc[blockIdx.x];
-  if (d.w == 0) return;
-  const int G = p.Hq / p.Hkv, kvh = d.y / geo.tiles, h0 = d.y % geo.tiles * TILE;
-  const int heads = G - h0 < TILE ? G - h0 : TILE;
   const int col = threadIdx.x % COLS, grp = threadIdx.x / COLS;
-  const int r = col / (D / 4), x = col % (D / 4) * 4;
-  const int first = blockIdx.x;
-  const int count = d.z - first + 1;
+  const int x = col % (D / 4) * 4, head = col / (D / 4);
+  const int first = blockIdx.x, r = blockIdx.y * HEADS + head;
+  const int4 d = ws.desc[first];
+  const int G = p.Hq / p.Hkv, kvh = d.y / geo.tiles, h = d.y % geo.tiles * geo.tile + r;
+  if (d.w == 0) return;
+  const int count = h < G ? d.z - first + 1 : 0;
   float M = -INFINITY, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float m, float l, const float4& y) {
-    const float to = fmaxf(M, m);
-    // a group without partials, M = m = -inf, has nothing to scale; a maximum of -inf otherwise comes of NaN
-    const float fo = M == -INFINITY ? 0.f : ex2_approx(M - to), fn = m == -INFINITY ? l : l * ex2_approx(m - to);
-    M = to;
-    L = fmaf(L, fo, fn);
-    O.x = fmaf(O.x, fo, y.x * fn); O.y = fmaf(O.y, fo, y.y * fn);
-    O.z = fmaf(O.z, fo, y.z * fn); O.w = fmaf(O.w, fo, y.w * fn);
-  };
-  if (r < heads) {
-    for (int j0 = grp; j0 < count; j0 += RS * U) {
-      float m[U], l[U];
-      float4 y[U];
+  for (int j0 = grp; j0 < count; j0 += RS * U) {
+    float m[U], l[U];
+    float4 y[U];
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int j = j0 + k * RS;
-        if (j >= count) break;
+    for (int k = 0; k < U; ++k) {
+      const int j = j0 + k * RS;
+      m[k] = -INFINITY;
+      if (j < count) {
         // partial j: the cut sequence's start, then the shares that continue it
         const int64_t s = static_cast<int64_t>(j == 0 ? 2 * first + 1 : 2 * (first + j)) * ROWS + r;
         m[k] = ws.m[s];
         l[k] = ws.l[s];
         y[k] = *reinterpret_cast<const float4*>(ws.o + s * D + x);
       }
+    }
+    float to = M;
 #pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (j0 + k * RS < count) add(m[k], l[k], y[k]);
+    for (int k = 0; k < U; ++k) to = fmaxf(to, m[k]);
+    const float f = ex2_approx(M - to);  // every partial has tokens, so `to` is a number
+    M = to;
+    L *= f;
+    O.x *= f; O.y *= f; O.z *= f; O.w *= f;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (j0 + k * RS >= count) break;
+      const float fn = l[k] * ex2_approx(m[k] - to);
+      L += fn;
+      O.x = fmaf(y[k].x, fn, O.x); O.y = fmaf(y[k].y, fn, O.y);
+      O.z = fmaf(y[k].z, fn, O.z); O.w = fmaf(y[k].w, fn, O.w);
     }
   }
-  if constexpr (RS > 1) {
-    s_m[grp][col] = M;
-    s_l[grp][col] = L;
-    // the groups' sums are not normalised: they enter with weight 1 at their maximum
-    s_o[grp][col] = O;
-    __syncthreads();
-    if (grp > 0) return;
-#pragma unroll
-    for (int k = 1; k < RS; ++k) {
-      if (k >= count) break;
-      const float m = s_m[k][col], to = fmaxf(M, m);
-      const float fo = ex2_approx(M - to), fn = ex2_approx(m - to);
-      const float4 y = s_o[k][col];
-      M = to;
-      L = L * fo + s_l[k][col] * fn;
-      O.x = O.x * fo + y.x * fn; O.y = O.y * fo + y.y * fn;
-      O.z = O.z * fo + y.z * fn; O.w = O.w * fo + y.w * fn;
-    }
+  s_o[grp][col] = O;
+  if (x == 0) {
+    s_m[grp][head] = M;
+    s_l[grp][head] = L;
   }
-  if (r >= heads) return;
+  __syncthreads();
+  if (grp > 0 || h >= G) return;
+#pragma unroll
+  for (int k = 1; k < RS; ++k) {
+    if (k >= count) break;  // the groups behind have no partials
+    const float to = fmaxf(M, s_m[k][head]), fo = ex2_approx(M - to), fn = ex2_approx(s_m[k][head] - to);
+    const float4 y = s_o[k][col];
+    M = to;
+    L = L * fo + s_l[k][head] * fn;
+    O.x = O.x * fo + y.x * fn; O.y = O.y * fo + y.y * fn;
+    O.z = O.z * fo + y.z * fn; O.w = O.w * fo + y.w * fn;
+  }
   const float inv = 1.f / L;
-  const int64_t row = static_cast<int64_t>(d.x) * p.Hq + kvh * G + h0 + r;
+  const int64_t row = static_cast<int64_t>(d.x) * p.Hq + kvh * G + h;
   *reinterpret_cast<uint2*>(p.o + row * D + x) =
       make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
   if (x == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(L)) * LN2;
@@ -842,6 +830,7 @@ cudaError_t launch(const DecodeQ4Params& p, cudaStream_t stream) {
   Q4Geometry geo;
   geo.grid = grid_of_device();
   if (geo.grid <= 0) return cudaErrorInvalidDevice;
+  geo.tile = C::TILE;
   geo.tiles = (p.Hq / p.Hkv + C::TILE - 1) / C::TILE;
   geo.units = p.Hkv * geo.tiles;
   geo.k_magic = K_MAGIC;
@@ -856,12 +845,21 @@ cudaError_t launch(const DecodeQ4Params& p, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(geo.grid);
-  cfg.blockDim = dim3(COMBINE_THREADS);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_q4_kernel<D, P>, p, geo);
+  // Few sequences and heads for many shares: many partials each, so every head gets a CTA (a sequence of
+  // 30000 tokens, 16/2 heads, d = 256, 152 partials a head: 21 us against 40).  Else a cut sequence has
+  // two or three, and the CTAs that find nothing to do cost more (64 sequences of 4352, 32/8 heads: 71 us
+  // against 68).
+  if (static_cast<int64_t>(p.N) * geo.units * 8 <= geo.grid) {
+    cfg.gridDim = dim3(geo.grid, std::min(C::TILE, p.Hq / p.Hkv));
+    cfg.blockDim = dim3(256);
+    return cudaLaunchKernelEx(&cfg, combine_q4_kernel<D, 1, 256>, p, geo);
+  }
+  cfg.gridDim = dim3(geo.grid);
+  cfg.blockDim = dim3(512);
+  return cudaLaunchKernelEx(&cfg, combine_q4_kernel<D, C::TILE, 512>, p, geo);
 }
 
 template <int D>

@@ -603,7 +603,9 @@ size_t attn_decode_q4_workspace_bytes(int d);
  * device, from the lengths: equal shares of all pages, one a CTA.
  * Arithmetic: products of the bf16 queries and the codes, which are exact;
  * float32 scores, sums and accumulators; each probability times its value's
- * scale enters the product with V as the sum of two bf16 numbers (16 bits).
+ * scale enters the product with V as one fp16 number: 11 bits down to 2^-20 of
+ * the largest scale that a sequence's values have in that group of channels,
+ * 2^-31 of that scale in absolute terms below it.
  * workspace: device buffer, 16-byte aligned, of at least
  * attn_decode_q4_workspace_bytes(d) bytes.  What a call reads from it the same
  * call has written; calls that overlap on the GPU (two streams, two graphs)

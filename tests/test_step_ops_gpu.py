@@ -7,11 +7,13 @@ most 2^-8 relative):
     the terms |a| + |b| of an output, taken as 2^-19; then one bf16 rounding.
   decode over the 4-bit cache: a group's product sums 64 terms |q| (16 + c) <= 31 |q| in float32, every
     addition allowed a whole ulp (2 u), so a score is off by at most B = scale * sum_g s_g * 31 * sum|q| *
-    70 * 2 u, and a probability relatively by B + 2^-16 (two bf16 parts, ex2, the merge).  A weighted mean
-    of terms t moves by at most 2 (B + 2^-16) max|t|.  The terms are not the values but what the kernel
-    sums, p s (16 + c) less p s (16 + z), the first with the two bf16 parts of p s, the second with p s
-    itself: a value of 0 (c = z) is a difference of two terms of up to 31 s.  So max|t| = 31 max s of the
-    group.  The LSE moves by at most B + 2^-20 (1 + |lse|).
+    70 * 2 u, and a probability relatively by B + 2^-16 (ex2, the merge).  A weighted mean of terms t moves
+    by at most 2 (B + 2^-16) max|t|.  The terms are what the kernel sums, x (c - 8) less x (z - 8) with x =
+    p s, a value of 0 (c = z) being a difference of two: max|t| is taken as 31 max s of the group.  x enters
+    both as the same fp16 number, off by half a step of 11 bits, 2^-12 relative: 2^-12 max|v| for the mean.
+    Below 2^-20 max s (at p = 1) it is off by 2^-31 max s instead: |c - z| <= 15 times L tokens of that are
+    under 2^-11 max s for L <= 2^16, less than half of 2^-16 * 31 max s.  The LSE moves by at most
+    B + 2^-20 (1 + |lse|).
   whole numbers, 4-bit codes and what they stand for: equal.
 """
 import math
@@ -351,7 +353,8 @@ def _check_decode(o, lse, q, lens, k, v, scale, what=""):
             step = 1.125 * 2 * np.abs(kk).reshape(length, -1, 64).max((0, 2)) / 15
             B = scale * (step * 31 * np.abs(q[n, h]).reshape(-1, 64).sum(-1)).sum() * 70 * 2.0 ** -23
             terms = 31 * 1.125 * 2 * np.repeat(np.abs(vv).reshape(length, -1, 64).max((0, 2)), 64) / 15
-            tol = 2.0 ** -8 * np.abs(want) + 2.01 * (B + 2.0 ** -16) * terms
+            most = np.repeat(np.abs(vv).reshape(length, -1, 64).max((0, 2)), 64)
+            tol = 2.0 ** -8 * np.abs(want) + 2.01 * (B + 2.0 ** -16) * terms + 2.0 ** -12 * most
             err = np.abs(o[n, h] - want)
             assert (err <= tol).all(), f"{what} n={n} h={h}: {(err / tol).max():.3g} of the tolerance"
             assert abs(lse[n, h] - want_l) <= B + 2.0 ** -20 * (1 + abs(want_l)), (what, n, h, lse[n, h], want_l)
@@ -391,6 +394,59 @@ def test_decode_q4_peaked_and_growing_scores(attn, gpu):
     q = _randn((1, 8, d), 22, gpu, 3.0)
     o, lse = attn.decode_paged_q4(q, cache, table, sl, scale=0.25)
     _check_decode(o, lse, q, [L], os_.stored(_np(k)), os_.stored(_np(v)), 0.25, "growing")
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (8, 1, 128), (8, 2, 128), (2, 2, 256), (5, 1, 256)])
+@pytest.mark.parametrize("which", ["growing", "shrinking", "zeros", "groups", "largest", "smallest", "one_sided"])
+def test_decode_q4_value_ranges(attn, gpu, which, Hq, Hkv, d):
+    """Scales of V that change along a sequence, that differ between the groups of a token, and at both ends of
+    the type's range.  Every group is held to its own scales."""
+    lens = [2500, 35]
+    cache, table, sl, k, v, slots = _cache_case(lens, Hkv, d, 61, gpu)
+    T = v.shape[0]
+    at = torch.arange(T, device=gpu, dtype=torch.float64) / T
+    e = {"growing": 80 * at - 40, "shrinking": 40 - 80 * at, "largest": 0 * at + 122, "smallest": 0 * at - 118}
+    if which in e:
+        v = (v.double() * torch.exp2(torch.floor(e[which]))[:, None, None]).to(torch.bfloat16)
+    elif which == "zeros":
+        v[(torch.arange(T, device=gpu) // 48) % 2 == 0] = 0
+    elif which == "groups":
+        v = (v.double() * torch.exp2(60.0 - 40 * (torch.arange(d, device=gpu) // 64).double())).to(torch.bfloat16)
+    else:
+        v = v.abs()
+    assert torch.isfinite(v).all()
+    attn.cache_append_q4(k, v, slots, cache)
+    q = _randn((2, Hq, d), 62, gpu)
+    o, lse = attn.decode_paged_q4(q, cache, table, sl)
+    _check_decode(o, lse, q, lens, os_.stored(_np(k)), os_.stored(_np(v)), 1 / math.sqrt(d), which)
+
+
+def test_decode_q4_huge_values_behind_other_values(attn, gpu):
+    """A NaN page, then ordinary ones: only the NaN's group of channels is lost, whatever comes after it."""
+    d, L = 256, 900
+    cache, table, sl, k, v, slots = _cache_case([L], 1, d, 63, gpu)
+    v[3, 0, 200] = float("inf")
+    attn.cache_append_q4(k, v, slots, cache)
+    q = _randn((1, 4, d), 64, gpu)
+    o, lse = attn.decode_paged_q4(q, cache, table, sl)
+    assert torch.isnan(o[..., 192:]).all() and torch.isfinite(lse).all()
+    v[3, 0, 200] = 0
+    clean = torch.zeros_like(cache)
+    attn.cache_append_q4(k, v, slots, clean)
+    want, _ = attn.decode_paged_q4(q, clean, table, sl)
+    assert torch.equal(o[..., :192], want[..., :192])
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_decode_q4_cut_anywhere(attn, gpu, seed):
+    """Many lengths from nothing to a few pages beside long ones: shares begin and end at every kind of place."""
+    rng = np.random.default_rng(seed)
+    lens = rng.integers(0, [40, 200, 40, 1000, 3, 5000][seed], [30, 90, 700, 25, 1100, 9][seed]).tolist()
+    Hq, Hkv, d = [(4, 2, 64), (16, 2, 128), (2, 2, 64), (8, 1, 256), (3, 1, 64), (18, 2, 128)][seed]
+    cache, table, sl, k, v = _filled(attn, lens, Hkv, d, 70 + seed, gpu)
+    q = _randn((len(lens), Hq, d), 80 + seed, gpu)
+    o, lse = attn.decode_paged_q4(q, cache, table, sl)
+    _check_decode(o, lse, q, lens, k, v, 1 / math.sqrt(d), str(seed))
 
 
 def test_decode_q4_agrees_with_the_bf16_cache(attn, gpu):
