@@ -62,10 +62,12 @@ constexpr uint32_t Z_MASK = 0x00780000u, Z_MAGIC = 0x41800000u;  // a zero point
 // P: pages a warp takes at a step; ROWS / P query heads.
 template <int D, int P>
 struct Cfg {
-  // warps that compute; one more loads.  What shared memory holds with three steps in flight a warp
-  // (four warps for d = 256: 75 us at 8 sequences of 58000, 16/2 heads, against 77 with five)
-  static constexpr int NW = D == 256 ? 4 : 7;
-  static constexpr int CTAS = 2;                   // CTAs an SM
+  // Warps that compute (one more loads), and CTAs an SM: what shared memory holds with three steps in flight
+  // a warp.  d = 256: 75 us with four warps, 77 with five (8 sequences of 58000, 16/2 heads).  d = 64: its
+  // copies are small, and one loading warp for seven others cannot issue them fast enough; 64 sequences
+  // of 8704, 32/8 heads: 93 us with 2 CTAs of seven warps, 83 with 3, 82 with 4 of five (64/8: 122, 103, 97).
+  static constexpr int NW = D == 256 ? 4 : D == 128 ? 7 : 5;
+  static constexpr int CTAS = D == 64 ? 4 : 2;
   static constexpr int THREADS = (NW + 1) * 32;
   static constexpr int TILE = ROWS / P;            // query heads a tile
   static constexpr int DEPTH = D == 256 && P == 2 ? 2 : 3;  // steps in flight a warp (two: 73 us for 70, d = 128)
@@ -89,6 +91,7 @@ __device__ __forceinline__ long long mul_div(long long a, long long b, long long
 
 struct Q4Geometry {
   int grid;          // CTAs
+  bool by_unit;      // few (sequence, unit) pairs: a descriptor for each; else one for each share
   int tile;          // query heads a tile
   int tiles, units;  // tiles a KV head, (KV head, tile) pairs a sequence
   // the magic numbers as arguments: a constant that the compiler knows would not stay in a register, and
@@ -98,7 +101,8 @@ struct Q4Geometry {
 
 // What the workspace holds: the shares' descriptors, then the partials' o, m and l.
 struct Workspace {
-  int4* desc;    // [grid]: (sequence, unit, last share, 1) of the cut sequence that starts in share b, or w = 0
+  int4* desc;    // [grid]: (sequence, unit, first share, last share) of a cut sequence, or z = -1; of the one
+                 // that starts in share b, or of pair sequence * units + unit
   float* o;      // [2 grid][ROWS][d]: index 2 b: continued from the share before, 2 b + 1: starts here
   float *m, *l;  // [2 grid][ROWS]
 };
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
   const Workspace ws = carve<D>(p.workspace, geo.grid);
   const int count = static_cast<int>(s_end[1] - s_end[0]);  // steps of this share
   if (count <= 0) {
-    if (threadIdx.x == 0) ws.desc[b] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0 && !geo.by_unit) ws.desc[b] = make_int4(0, 0, -1, 0);
     return;
   }
 
@@ -350,7 +354,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
     long long at = s_at;    // ... the weight before its (sequence, unit) ...
     int seg_i = 0;          // ... its first step's share index
     uint32_t seg_phase = 0;
-    int4 cut = make_int4(0, 0, 0, 0);
+    int4 cut = make_int4(0, 0, -1, 0);
     int i = lane;      // this lane's next step, with the pages' table entries
     int ids[P] = {};
     int stage_k = 0;
@@ -436,8 +440,10 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
         if (starts && !ends) {
           // the share that holds the last step: weight x lies in share ((x + 1) shares - 1) / W
           const long long past = at + SEGMENT + seg.ns;
-          cut = make_int4(seg.n, seg.u, static_cast<int>(mul_div(past * shares - 1, 1, W)), 1);
+          cut = make_int4(seg.n, seg.u, b, static_cast<int>(mul_div(past * shares - 1, 1, W)));
         }
+        if (geo.by_unit && starts && lane == 0)
+          ws.desc[seg.n * units + seg.u] = ends ? make_int4(0, 0, -1, 0) : cut;
         at += SEGMENT + seg.ns;
         seg_i += seg_steps;
         if (seg_i < count) seg.advance(seg_steps, p.seq_lens, N, units, p.max_blocks);
@@ -450,7 +456,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
       }
     }
     if (lane == 0) {
-      ws.desc[b] = cut;
+      if (!geo.by_unit) ws.desc[b] = cut;
       if (!ok) set_error(&g_decode_q4_status, kDevWaitTimeout);
     }
     // Copies in flight must land before the CTA's shared memory is given back: the newest of each slot.
@@ -740,9 +746,9 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
   if (!ok && lane == 0) set_error(&g_decode_q4_status, kDevWaitTimeout);
 }
 
-// Merges the partials of the cut sequence that starts in a share, if there is one: a CTA of T threads takes
-// HEADS query heads of share blockIdx.x.  Each of RS groups of threads takes every RS-th partial, U of
-// them in flight at a time, with a running maximum; then the groups' sums are merged.
+// Merges the partials of descriptor blockIdx.x's sequence, if it was cut: a CTA of T threads takes HEADS query
+// heads.  Each of RS groups of threads takes every RS-th partial, U of them in flight at a time, with a
+// running maximum; then the groups' sums are merged.
 template <int D, int HEADS, int T>
 __global__ void __launch_bounds__(T) combine_q4_kernel(const DecodeQ4Params p, const Q4Geometry geo) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -754,11 +760,14 @@ __global__ void __launch_bounds__(T) combine_q4_kernel(const DecodeQ4Params p, c
   const Workspace ws = carve<D>(p.workspace, geo.grid);
   const int col = threadIdx.x % COLS, grp = threadIdx.x / COLS;
   const int x = col % (D / 4) * 4, head = col / (D / 4);
-  const int first = blockIdx.x, r = blockIdx.y * HEADS + head;
-  const int4 d = ws.desc[first];
+  const int r = blockIdx.y * HEADS + head;
+  // an empty sequence has no steps that could have written its pairs' descriptors
+  if (geo.by_unit && clamped_len(p.seq_lens, blockIdx.x / geo.units, p.max_blocks) == 0) return;
+  const int4 d = ws.desc[blockIdx.x];
   const int G = p.Hq / p.Hkv, kvh = d.y / geo.tiles, h = d.y % geo.tiles * geo.tile + r;
-  if (d.w == 0) return;
-  const int count = h < G ? d.z - first + 1 : 0;
+  // after a wait that ran out (a recorded error) a descriptor may be missing: nothing of it is used
+  if (d.z < 0 || d.w >= geo.grid || d.x < 0 || d.x >= p.N || d.y < 0 || d.y >= geo.units) return;
+  const int first = d.z, count = h < G ? d.w - first + 1 : 0;
   float M = -INFINITY, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j0 = grp; j0 < count; j0 += RS * U) {
@@ -816,23 +825,26 @@ __global__ void __launch_bounds__(T) combine_q4_kernel(const DecodeQ4Params p, c
   if (x == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(L)) * LN2;
 }
 
-// CTAs of the grid: every SM filled (the same count for each variant)
+// CTAs of the grid: every SM filled
+template <int D>
 int grid_of_device() {
+  static_assert(Cfg<D, 1>::CTAS == Cfg<D, 2>::CTAS, "one size of workspace for a head dim");
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return sms * Cfg<128, 1>::CTAS;
+  return sms * Cfg<D, 1>::CTAS;
 }
 
 template <int D, int P>
 cudaError_t launch(const DecodeQ4Params& p, cudaStream_t stream) {
   using C = Cfg<D, P>;
   Q4Geometry geo;
-  geo.grid = grid_of_device();
+  geo.grid = grid_of_device<D>();
   if (geo.grid <= 0) return cudaErrorInvalidDevice;
   geo.tile = C::TILE;
   geo.tiles = (p.Hq / p.Hkv + C::TILE - 1) / C::TILE;
   geo.units = p.Hkv * geo.tiles;
+  geo.by_unit = static_cast<int64_t>(p.N) * geo.units * 8 <= geo.grid;
   geo.k_magic = K_MAGIC;
   geo.v_magic0 = V_MAGIC0;
   geo.v_magic1 = V_MAGIC1;
@@ -849,11 +861,11 @@ cudaError_t launch(const DecodeQ4Params& p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // Few sequences and heads for many shares: many partials each, so every head gets a CTA (a sequence of
-  // 30000 tokens, 16/2 heads, d = 256, 152 partials a head: 21 us against 40).  Else a cut sequence has
+  // 30000 tokens, 16/2 heads, d = 256, 152 partials a head: 18 us against 40).  Else a cut sequence has
   // two or three, and the CTAs that find nothing to do cost more (64 sequences of 4352, 32/8 heads: 71 us
   // against 68).
-  if (static_cast<int64_t>(p.N) * geo.units * 8 <= geo.grid) {
-    cfg.gridDim = dim3(geo.grid, std::min(C::TILE, p.Hq / p.Hkv));
+  if (geo.by_unit) {
+    cfg.gridDim = dim3(p.N * geo.units, std::min(C::TILE, p.Hq / p.Hkv));
     cfg.blockDim = dim3(256);
     return cudaLaunchKernelEx(&cfg, combine_q4_kernel<D, 1, 256>, p, geo);
   }
@@ -870,7 +882,10 @@ cudaError_t launch_for(const DecodeQ4Params& p, cudaStream_t stream) {
 }  // namespace
 
 size_t decode_q4_workspace_bytes(int d) {
-  const size_t grid = static_cast<size_t>(grid_of_device());
+  const size_t grid = d == 64    ? grid_of_device<64>()
+                      : d == 128 ? grid_of_device<128>()
+                      : d == 256 ? grid_of_device<256>()
+                                 : 0;
   return grid * 16 + 2 * grid * ROWS * (static_cast<size_t>(d) + 2) * sizeof(float);
 }
 
