@@ -9,7 +9,7 @@
 // byte by byte.  Quantising costs more than the memory allows for unless it is done in pairs: the range
 // by packed bf16 minima and maxima, the division as a product with the reciprocal and one correction
 // (which makes ties exact) on pairs of floats, the codes as 16-bit pairs.
-// Read-back: a warp a record; V words are exchanged between the four lanes that hold 8 neighbouring
+// Read-back: a warp at a record; V words are exchanged between the four lanes that hold 8 neighbouring
 // channels, so that each lane writes 16 bytes.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -33,6 +33,11 @@ constexpr int WARPS = 4;
 // 64 tokens 6.8 us against 8.8 us by pages, 2048 tokens 10.9 against 10.9, 8192 tokens 23.2 against 19.1
 // (cold L2).
 constexpr int64_t ROWWISE_VALUES = 1 << 21;
+
+// CTAs of a read-back, about: a block table may be far wider than its sequences are long.  One warp for each
+// of its records, 64 sequences of 1000 tokens, 8 heads, d = 128, take 138 us with 2048 pages a row and 53 us
+// with 63; with this limit 54 us both.  64 sequences of 8000: 405 us, without a limit 396.
+constexpr int64_t GATHER_CTAS = 152 * 64;
 
 constexpr float MAGIC = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, which the lower bits then hold
 
@@ -269,32 +274,14 @@ __device__ __forceinline__ uint4 values(uint32_t codes, uint32_t param) {
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// One warp a record
+// The first `valid` tokens of a record to page `at` of the output, by a warp
 template <int D>
-__global__ void __launch_bounds__(WARPS * 32) gather_q4_kernel(const GatherQ4Params p) {
+__device__ __forceinline__ void gather_record(const GatherQ4Params& p, const uint8_t* rec, int64_t at, int h, int valid,
+                                              int lane) {
   using R = Record<D>;
   constexpr int WPR = D / 8;     // code words a K row
   constexpr int RPI = 32 / WPR;  // K rows a load
   constexpr int NG = R::NG;
-  const int n = blockIdx.y, lane = threadIdx.x & 31;
-  const unsigned item = blockIdx.x * WARPS + (threadIdx.x >> 5);
-  const int page = item / p.Hkv, h = item - page * p.Hkv;
-  if (page >= p.max_blocks) return;
-  int len = p.seq_lens[n];
-  if (len < 0 || len > p.max_blocks * q4::PAGE) {
-    if (lane == 0 && item == 0) set_error(&g_cache_q4_status, kDevBadSeqlens);
-    len = len < 0 ? 0 : p.max_blocks * q4::PAGE;
-  }
-  const int64_t at = static_cast<int64_t>(n) * p.max_blocks + page;
-  if (p.out_table != nullptr && h == 0 && lane == 0) p.out_table[at] = static_cast<int32_t>(at);
-  const int valid = len - page * q4::PAGE;
-  if (valid <= 0) return;
-  int pid = p.block_table[at];
-  if (pid < 0 || pid >= p.num_blocks) {
-    if (lane == 0) set_error(&g_cache_q4_status, kDevBadPage);
-    pid = 0;
-  }
-  const uint8_t* rec = p.cache + (static_cast<int64_t>(pid) * p.Hkv + h) * R::BYTES;
   const int64_t row_stride = static_cast<int64_t>(p.Hkv) * D;
   const int64_t out0 = at * q4::PAGE * row_stride + static_cast<int64_t>(h) * D;
 
@@ -355,6 +342,30 @@ __global__ void __launch_bounds__(WARPS * 32) gather_q4_kernel(const GatherQ4Par
   }
 }
 
+// A warp takes every gridDim.x * WARPS-th record of sequence blockIdx.y
+template <int D>
+__global__ void __launch_bounds__(WARPS * 32) gather_q4_kernel(const GatherQ4Params p) {
+  const int n = blockIdx.y, lane = threadIdx.x & 31;
+  int len = p.seq_lens[n];
+  if (len < 0 || len > p.max_blocks * q4::PAGE) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) set_error(&g_cache_q4_status, kDevBadSeqlens);
+    len = len < 0 ? 0 : p.max_blocks * q4::PAGE;
+  }
+  const unsigned items = static_cast<unsigned>((len + q4::PAGE - 1) / q4::PAGE) * p.Hkv;
+  for (unsigned item = blockIdx.x * WARPS + (threadIdx.x >> 5); item < items; item += gridDim.x * WARPS) {
+    const int page = item / p.Hkv, h = item - page * p.Hkv;
+    const int64_t at = static_cast<int64_t>(n) * p.max_blocks + page;
+    if (p.out_table != nullptr && h == 0 && lane == 0) p.out_table[at] = static_cast<int32_t>(at);
+    int pid = p.block_table[at];
+    if (pid < 0 || pid >= p.num_blocks) {
+      if (lane == 0) set_error(&g_cache_q4_status, kDevBadPage);
+      pid = 0;
+    }
+    const uint8_t* rec = p.cache + (static_cast<int64_t>(pid) * p.Hkv + h) * Record<D>::BYTES;
+    gather_record<D>(p, rec, at, h, len - page * q4::PAGE, lane);
+  }
+}
+
 template <int D>
 cudaError_t append(const AppendQ4Params& p, cudaStream_t stream) {
   if (static_cast<int64_t>(p.T) * p.Hkv * D <= ROWWISE_VALUES) {
@@ -368,8 +379,10 @@ cudaError_t append(const AppendQ4Params& p, cudaStream_t stream) {
 
 template <int D>
 cudaError_t gather(const GatherQ4Params& p, cudaStream_t stream) {
-  const int64_t items = static_cast<int64_t>(p.max_blocks) * p.Hkv;
-  gather_q4_kernel<D><<<dim3(static_cast<unsigned>((items + WARPS - 1) / WARPS), p.N), WARPS * 32, 0, stream>>>(p);
+  const int64_t items = (static_cast<int64_t>(p.max_blocks) * p.Hkv + WARPS - 1) / WARPS;
+  const int64_t most = (GATHER_CTAS + p.N - 1) / p.N;
+  const unsigned grid = static_cast<unsigned>(items < most ? items : most);
+  gather_q4_kernel<D><<<dim3(grid, p.N), WARPS * 32, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

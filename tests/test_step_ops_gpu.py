@@ -260,6 +260,26 @@ def test_cache_append_and_gather(attn, gpu, lens, Hkv, d):
                         assert np.array_equal(got[which][tok], old[which][tok], equal_nan=True)
 
 
+def test_gather_from_a_wide_table(attn, gpu):
+    """Rows of the table far longer than the sequences, and more records than warps are started for."""
+    lens, Hkv, d, wide = [1, 0, 300, 16] + [40] * 700, 2, 64, 200
+    cache, table, sl, k, v, slots = _cache_case(lens, Hkv, d, 17, gpu)
+    attn.cache_append_q4(k, v, slots, cache)
+    spread = torch.full((len(lens), wide), -1, dtype=torch.int32, device=gpu)
+    spread[:, :table.shape[1]] = table
+    for n, length in enumerate(lens):
+        spread[n, _pages(length):] = -1
+    k0, v0 = attn.cache_gather_q4(cache, table, sl)
+    k1, v1 = attn.cache_gather_q4(cache, spread, sl)
+    assert attn.device_status(clear=True) == 0
+    at = 0
+    for n, length in enumerate(lens):
+        want_k, want_v = (os_.stored(_np(x[at:at + length])) for x in (k, v))
+        assert (_np(k1[n, :length]) == want_k).all() and (_np(v1[n, :length]) == want_v).all()
+        assert torch.equal(k0[n, :length], k1[n, :length]) and torch.equal(v0[n, :length], v1[n, :length])
+        at += length
+
+
 @pytest.mark.parametrize("order", ["shuffled", "reversed", "singles", "strided"])
 def test_cache_append_orders_agree(attn, gpu, order):
     """Whatever the order and grouping of the tokens, and the stride of their rows, the same bytes."""
