@@ -545,9 +545,10 @@ attn_status_t attn_qk_norm_rope(const void* q, long long q_stride, const void* k
  *       2^-129 below 2^-126),
  *   z = rint(-lo / s), code = clamp(rint(x / s) + z, 0, 15)
  * and the code stands for s * (code - z): within half a step s of x, and a
- * bf16 number exactly, so that reading a cache back loses nothing more.  A
- * group that holds an infinity or NaN, or whose hi - lo overflows float32,
- * reads back as NaN.  A record holds 16 tokens:
+ * bf16 number exactly, so that reading a cache back loses nothing more (a
+ * product past the type's largest number is an infinity).  A group that holds
+ * an infinity or NaN, or whose hi - lo overflows float32, reads back as NaN.
+ * A record holds 16 tokens:
  *   bytes [0, 8 d): K codes, d / 2 bytes a token; the 32-bit word that holds
  *     channels 64 e + 16 t + 8 h + (0 .. 7) of a token, channel j in nibble
  *     j, then rotated left by 3 bits, is word
