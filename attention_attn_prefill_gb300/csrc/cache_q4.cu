@@ -77,13 +77,15 @@ __device__ __forceinline__ uint32_t quantise(const uint4& raw, uint32_t& param) 
   // a NaN or infinity passes through
   __nv_bfloat162 hi2 = __hmax2_nan(__hmax2_nan(w[0], w[1]), __hmax2_nan(w[2], w[3]));
   __nv_bfloat162 lo2 = __hmin2_nan(__hmin2_nan(w[0], w[1]), __hmin2_nan(w[2], w[3]));
+  // the maximum and minus the minimum share a word for the rest of the way
+  const uint32_t h = reinterpret_cast<const uint32_t&>(hi2), l = reinterpret_cast<const uint32_t&>(lo2) ^ 0x80008000u;
+  const uint32_t lower = __byte_perm(h, l, 0x5410), upper = __byte_perm(h, l, 0x7632);
+  __nv_bfloat162 ext = __hmax2_nan(reinterpret_cast<const __nv_bfloat162&>(lower),
+                                   reinterpret_cast<const __nv_bfloat162&>(upper));
 #pragma unroll
-  for (int off = 1; off < 8; off <<= 1) {
-    hi2 = __hmax2_nan(hi2, __shfl_xor_sync(0xffffffffu, hi2, off));
-    lo2 = __hmin2_nan(lo2, __shfl_xor_sync(0xffffffffu, lo2, off));
-  }
-  const float2 hf = __bfloat1622float2(hi2), lf = __bfloat1622float2(lo2);
-  const float hi = max_nan(max_nan(hf.x, hf.y), 0.f), lo = fminf(fminf(lf.x, lf.y), 0.f);
+  for (int off = 1; off < 8; off <<= 1) ext = __hmax2_nan(ext, __shfl_xor_sync(0xffffffffu, ext, off));
+  const float2 ef = __bfloat1622float2(ext);
+  const float hi = max_nan(ef.x, 0.f), lo = fminf(-ef.y, 0.f);
   const float s = q4::make_scale(hi, lo);
   constexpr uint32_t LEAST = 0x1e3ce508u, MOST = 0x7e967699u;  // 1e-20, 1e38
   if (__float_as_uint(s) - LEAST >= MOST - LEAST) {  // NaN too: its bits are past all of these, with either sign
