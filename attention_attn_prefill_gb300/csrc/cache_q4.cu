@@ -29,11 +29,10 @@ namespace {
 using q4::Record;
 
 constexpr int WARPS = 4;
-// Up to this many values a call takes a row at a time: measured at 8 heads, d = 128, tokens that fill pages,
-// 64 tokens 6.8 us against 8.8 us by pages, 2048 tokens 10.9 against 10.9, 8192 tokens 23.2 against 19.1
-// (cold L2).
-constexpr int64_t ROWWISE_VALUES = 1 << 21;
-
+// Up to this many values a call takes a row at a time.  Measured at 8 heads, d = 128, by rows and by pages:
+// 512 tokens that fill pages 2.8 and 3.5 us, 1024 tokens 3.6 and 3.6, 2048 tokens 5.4 and 4.6, 8192 tokens
+// 16.1 and 11.7; tokens on a page each 3.1 and 4.8, 3.7 and 5.3, 5.4 and 6.8, 19.1 and 18.8.
+constexpr int64_t ROWWISE_VALUES = 1 << 20;
 // CTAs of a read-back, about: a block table may be far wider than its sequences are long.  One warp for each
 // of its records, 64 sequences of 1000 tokens, 8 heads, d = 128, take 138 us with 2048 pages a row and 53 us
 // with 63; with this limit 54 us both.  64 sequences of 8000: 405 us, without a limit 396.
@@ -161,8 +160,9 @@ __global__ void __launch_bounds__(128) append_rows_q4_kernel(const AppendQ4Param
 
 // K or V of a head, for 16 tokens from 16 blockIdx.x on.  A run of 16 tokens that fills a page belongs to
 // the warp of its first token, whatever tokens it reaches into; the others of a warp's tokens are
-// written row by row.  (K and V in one warp: 46 us instead of 40 us for 32002 tokens of 8 heads, d = 128,
-// for want of registers.)
+// written row by row, their loads in flight together too: the last, partly filled page of a prompt is what a
+// call of few pages waits for (2049 tokens of 8 heads, d = 128: 4.7 us; 8.1 us with two rows in flight).  K
+// and V in one warp take 46 us instead of 40 us for 32002 tokens, for want of registers (this form: 34 us).
 template <int D>
 __global__ void __launch_bounds__(WARPS * 32) append_q4_kernel(const AppendQ4Params p) {
   using R = Record<D>;
@@ -240,15 +240,21 @@ __global__ void __launch_bounds__(WARPS * 32) append_q4_kernel(const AppendQ4Par
     }
   }
   if (singles != 0) {
-#pragma unroll 2
+    uint4 raw[IT];
+#pragma unroll
     for (int it = 0; it < IT; ++it) {
+      const int k = it * RPI + k0;
+      raw[it] = make_uint4(0, 0, 0, 0);
+      if (singles >> k & 1) raw[it] = __ldcs(reinterpret_cast<const uint4*>(base + (chunk + k) * stride));
+    }
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      if ((singles >> (it * RPI) & ((1u << RPI) - 1)) == 0) continue;
       const int k = it * RPI + k0;
       const int slot = __shfl_sync(0xffffffffu, my_slot, 16 + k);
       const bool live = singles >> k & 1;
-      uint4 raw = make_uint4(0, 0, 0, 0);
-      if (live) raw = __ldcs(reinterpret_cast<const uint4*>(base + (chunk + k) * stride));
       uint32_t param;
-      const uint32_t codes = quantise(raw, param);
+      const uint32_t codes = quantise(raw[it], param);
       if (live) {
         uint8_t* rec = p.cache + (static_cast<int64_t>(slot / 16) * p.Hkv + h) * R::BYTES;
         if (is_v) store_row<D, true>(rec, slot % 16, sub, codes, param);
