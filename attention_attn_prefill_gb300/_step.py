@@ -332,7 +332,10 @@ def prefill_paged_q4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
                      out: torch.Tensor | None = None, lse: torch.Tensor | None = None, return_lse: bool = True,
                      workspace: torch.Tensor | None = None, stream=None):
     """Chunked prefill over the 4-bit cache: new tokens q [T,Hq,d] (their K/V already appended) against
-    all cached tokens of their sequences -> (o [T,Hq,d], lse [Hq,T])."""
+    all cached tokens of their sequences -> (o [T,Hq,d], lse [Hq,T]).
+
+    The workspace holds N * max_blocks pages as bf16: pass block_table[:, :pages].contiguous() where the
+    table is much wider than the longest sequence needs."""
     dev, N = q.get_device(), seq_lens.numel()
     T, Hq, d = q.shape
     num_blocks, Hkv, max_blocks = _check_paged(dev, d, cache, block_table, seq_lens, N)

@@ -10,7 +10,8 @@
 // consecutive tokens and scans the lengths itself (256 requests at a time, 8 bytes each, from L2)
 // until the requests of its own tokens are behind it, instead of waiting for a scan kernel's result;
 // it keeps the requests that own some of its tokens in shared memory, where each token finds its own
-// by binary search.  CTA 0 goes through all requests and writes the per-request outputs.
+// by binary search.  CTA 0 goes through all requests and writes the per-request outputs.  64 requests of
+// a token each take 2.7 us, an empty launch 2; 512 requests with 35,000 tokens 5.0 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>

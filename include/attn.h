@@ -620,7 +620,8 @@ attn_status_t attn_decode_paged_q4(const void* q, const void* cache, const int32
 /*
  * Bytes of workspace attn_prefill_paged_q4 needs: keys and values of num_seqs *
  * max_blocks_per_seq pages in bf16 and their block table, each rounded up to
- * 256.  0 for invalid arguments (also more than 2^30 token rows).
+ * 256.  0 for invalid arguments (also more than 2^30 token rows).  A block
+ * table cut to the columns that the longest sequence fills takes less.
  */
 size_t attn_prefill_q4_workspace_bytes(int num_seqs, int Hkv, int d, int max_blocks_per_seq);
 
