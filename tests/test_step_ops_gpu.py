@@ -300,6 +300,47 @@ def test_cache_append_orders_agree(attn, gpu, order):
     assert torch.equal(cache, want)
 
 
+@pytest.mark.parametrize("d,Hkv", [(64, 20), (128, 11), (256, 5)])
+@pytest.mark.parametrize("order", ["whole", "offset", "holes", "swapped", "shuffled", "tails"])
+def test_append_by_pages_agrees_with_rows(attn, gpu, order, d, Hkv):
+    """A call large enough to write whole pages at once gives the bytes of small calls, however the pages' tokens
+    lie in the batch."""
+    T, num_blocks = 997, 400
+    rng = np.random.default_rng(d)
+    pages = rng.permutation(num_blocks)
+    slots = np.concatenate([p * PAGE + np.arange(PAGE) for p in pages[:T // PAGE + 1]])
+    if order == "offset":                                     # a page starts 5 tokens into the batch
+        slots = np.concatenate([[pages[-1] * PAGE + i for i in (3, 7, 2, 9, 15)], slots])
+    elif order == "tails":                                    # short sequences between whole pages
+        cut = [slots[i * PAGE:i * PAGE + (PAGE if i % 3 else 1 + i % 15)] for i in range(T // PAGE + 1)]
+        slots = np.concatenate(cut + [pages[200 + i] * PAGE + np.arange(12) for i in range(60)])
+    slots = slots[:T]
+    if order == "holes":
+        slots = np.where(rng.random(T) < 0.05, -1, slots)
+    elif order == "swapped":                                  # two tokens of some pages in the other order
+        for i in range(0, T - PAGE, 3 * PAGE):
+            j = i + rng.integers(0, 15)
+            slots[j], slots[j + 1] = slots[j + 1], slots[j]
+    elif order == "shuffled":
+        slots = rng.permutation(slots)
+    slots = _i32(slots.tolist(), gpu)
+    T = slots.numel()
+    assert T * Hkv * d > 1 << 20 and 128 * Hkv * d <= 1 << 20   # by pages, and by rows
+    k, v = _randn((T, Hkv, d), 1, gpu), _randn((T, Hkv, d), 2, gpu)
+    cache = torch.randint(0, 256, (num_blocks, Hkv, 17 * d), dtype=torch.uint8,
+                          generator=torch.Generator().manual_seed(d)).to(gpu)
+    want = cache.clone()
+    attn.cache_append_q4(k, v, slots, cache)
+    for at in range(0, T, 128):
+        attn.cache_append_q4(k[at:at + 128], v[at:at + 128], slots[at:at + 128], want)
+    assert torch.equal(cache, want) and attn.device_status(clear=True) == 0
+    # slots past the end are reported and skipped, with the rest of the batch written
+    bad = slots.clone()
+    bad[500:520] = num_blocks * PAGE + torch.arange(20, dtype=torch.int32, device=gpu)
+    attn.cache_append_q4(k, v, bad, cache)
+    assert torch.equal(cache, want) and attn.device_status(clear=True) == 8
+
+
 def test_cache_values_at_the_edges(attn, gpu):
     """Zeros, one sign, ties, exact grids, tiny and large ranges; infinities and NaN spoil their group only."""
     d = 128
@@ -508,6 +549,33 @@ def test_decode_q4_reports(attn, gpu):
     assert attn.device_status(clear=True) == 3
     with pytest.raises(attn.AttnError):
         attn.decode_paged_q4(q, cache, table, sl, workspace=torch.empty(64, dtype=torch.uint8, device=gpu))
+
+
+def test_far_pages(attn, gpu):
+    """Pages past 2^32 bytes of a cache, and token rows past 2^32 bytes of their tensor."""
+    Hkv, d, num_blocks = 8, 256, 130000
+    cache = attn.cache_q4_empty(num_blocks, Hkv, d, device=gpu)
+    assert cache.numel() > 1 << 32
+    pages = [num_blocks - 1, 3, num_blocks - 2, num_blocks - 7]
+    L = 50
+    rows = torch.empty((L, 1 << 26), dtype=torch.bfloat16, device=gpu)   # 128 MB apart
+    k, v = (rows[:, at:at + Hkv * d].unflatten(1, (Hkv, d)) for at in (0, 1 << 25))
+    k.copy_(_randn((L, Hkv, d), 91, gpu))
+    v.copy_(_randn((L, Hkv, d), 92, gpu))
+    slots = _i32([pages[t // PAGE] * PAGE + t % PAGE for t in range(L)], gpu)
+    table, sl = _i32([pages], gpu), _i32([L], gpu)
+    attn.cache_append_q4(k, v, slots, cache)
+    want = [os_.stored(_np(x)) for x in (k, v)]
+    got = attn.cache_gather_q4(cache, table, sl)
+    assert all((_np(g[0, :L]) == w).all() for g, w in zip(got, want))
+    q = _randn((1, Hkv, d), 93, gpu)
+    o, lse = attn.decode_paged_q4(q, cache, table, sl)
+    _check_decode(o, lse, q, [L], *want, 1 / math.sqrt(d), "far")
+    kc, vc = (torch.zeros((20, PAGE, Hkv, d), dtype=torch.bfloat16, device=gpu) for _ in "kv")
+    _, kn = attn.qk_norm_rope(v, k, None, None, v=v, k_cache=kc, v_cache=vc, slots=_i32(list(range(L)), gpu),
+                              k_out=torch.empty_like(rows)[:, :Hkv * d].unflatten(1, (Hkv, d)))
+    assert torch.equal(kn, k) and torch.equal(kc.view(-1, Hkv, d)[:L], k) and torch.equal(vc.view(-1, Hkv, d)[:L], v)
+    assert attn.device_status(clear=True) == 0
 
 
 # ------------------------------------------------------------------------------------------ prefill
