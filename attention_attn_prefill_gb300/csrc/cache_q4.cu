@@ -9,7 +9,7 @@
 // byte by byte.  Quantising costs more than the memory allows for unless it is done in pairs: the range
 // by packed bf16 minima and maxima, the division as a product with the reciprocal and one correction
 // (which makes ties exact) on pairs of floats, the codes as 16-bit pairs.
-// 32002 tokens of 8 heads, d = 128, take 34 us, 24 at the rate of a copy; issue slots bound it (74% used).
+// 32002 tokens of 8 heads, d = 128, take 34 us, 24 at the rate of a copy; issue slots bound it (72% used).
 // Read-back: a warp at a record; V words are exchanged between the four lanes that hold 8 neighbouring
 // channels, so that each lane writes 16 bytes.  5.5 to 6.6 TB/s, HBM's rate.
 #include <cuda_bf16.h>
