@@ -4,6 +4,12 @@ Every computation happens in the library's CUDA kernels; these wrappers only
 check tensor shapes/dtypes, allocate outputs (and the decode workspace) with
 torch, and pass raw device pointers plus the current CUDA stream.  If the
 library is missing they raise -- there is no fallback path.
+
+With `stream` (a torch stream or a raw handle) a call runs there instead and is
+not ordered against the current stream: inputs, and outputs or a workspace that
+are passed in, have to be ready on it.  What the call allocates comes from that
+stream's own memory, so that it needs no such order; a result may be used on the
+current stream as soon as that waits for `stream`.
 """
 from __future__ import annotations
 
@@ -116,6 +122,41 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream or 0)
 
 
+def _other_stream(stream, dev: int):
+    """`stream` as a torch stream, or None where it is the current stream of device `dev` (or not given)."""
+    if stream is None:
+        return None
+    handle = _stream_handle(stream)
+    if handle == torch._C._cuda_getCurrentRawStream(dev):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+
+
+def _empty_on(shape, dtype, dev: int, stream, returned: bool = True) -> torch.Tensor:
+    """torch.empty in memory of the stream that the call runs on.  Memory of the current stream may still be in
+    use by work enqueued there before this call, which `stream` does not wait for.  `returned`: the caller gets
+    the tensor, and may use and free it on the current stream."""
+    on = _other_stream(stream, dev)
+    if on is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    current = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(on):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if returned:
+        t.record_stream(current)
+    return t
+
+
+def _empty(shape, dtype, device: torch.device, stream, returned: bool = True) -> torch.Tensor:
+    """_empty_on for a device as tensors name it."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _empty_on(shape, dtype, torch.cuda.current_device() if device.index is None else device.index, stream,
+                     returned)
+
+
 def _dev(t: torch.Tensor, dtype, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -137,9 +178,9 @@ def prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float | No
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device)
+        lse = _empty((B, Hq, S), torch.float32, q.device, stream)
     st = lib().attn_prefill(
         _dev(q, torch.bfloat16, "q"), _dev(k, torch.bfloat16, "k"), _dev(v, torch.bfloat16, "v"),
         _dev(out, torch.bfloat16, "out"), _dev(lse, torch.float32, "lse") if lse is not None else None,
@@ -161,9 +202,9 @@ def prefill_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+        lse = _empty((Hq, T), torch.float32, q.device, stream)
     st = lib().attn_prefill_varlen(
         _dev(q, torch.bfloat16, "q"), _dev(k, torch.bfloat16, "k"), _dev(v, torch.bfloat16, "v"),
         _dev(out, torch.bfloat16, "out"), _dev(lse, torch.float32, "lse") if lse is not None else None,
@@ -188,9 +229,9 @@ def prefill_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+        lse = _empty((Hq, T), torch.float32, q.device, stream)
     st = lib().attn_prefill_paged(
         _dev(q, torch.bfloat16, "q"), _dev(k_cache, torch.bfloat16, "k_cache"),
         _dev(v_cache, torch.bfloat16, "v_cache"), _dev(block_table, torch.int32, "block_table"),
@@ -236,8 +277,8 @@ def prefill_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float
         lse = torch.empty((Hq, S), dtype=torch.float32, pin_memory=pin)
     need = prefill_host_workspace_bytes(S, Hq, Hkv, d, chunks)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8,
-                                device=device if device is not None else torch.device("cuda", torch.cuda.current_device()))
+        workspace = _empty((max(need, 1),), torch.uint8,
+                           torch.device("cuda" if device is None else device), stream, returned=False)
     st = lib().attn_prefill_host(
         _host(q, torch.bfloat16, "q"), _host(k, torch.bfloat16, "k"), _host(v, torch.bfloat16, "v"),
         _host(out, torch.bfloat16, "out"), _host(lse, torch.float32, "lse") if lse is not None else None,
@@ -327,11 +368,11 @@ def decode_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
             raise AttnError(1, "attn_decode_num_slots")
         need = decode_workspace_bytes(N, Hq, d, slots)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty((need,), torch.uint8, q.device, stream, returned=False)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((N, Hq), torch.float32, q.device, stream)
     ws_ptr = workspace.data_ptr() if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = lib().attn_decode_paged(
@@ -355,9 +396,9 @@ def decode_paged_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((N, Hq), torch.float32, q.device, stream)
     st = lib().attn_decode_paged_noalloc(
         _dev(q, torch.bfloat16, "q"), _dev(k_cache, torch.bfloat16, "k_cache"),
         _dev(v_cache, torch.bfloat16, "v_cache"), _dev(block_table, torch.int32, "block_table"),
@@ -376,9 +417,9 @@ def combine(part_o: torch.Tensor, part_m: torch.Tensor, part_l: torch.Tensor, ou
     if part_m.shape != (rows, splits) or part_l.shape != (rows, splits):
         raise ValueError("part_m and part_l must be [rows, splits]")
     if out is None:
-        out = torch.empty((rows, d), dtype=torch.bfloat16, device=part_o.device)
+        out = _empty((rows, d), torch.bfloat16, part_o.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((rows,), dtype=torch.float32, device=part_o.device)
+        lse = _empty((rows,), torch.float32, part_o.device, stream)
     st = lib().attn_combine(
         _dev(part_o, torch.float32, "part_o"), _dev(part_m, torch.float32, "part_m"),
         _dev(part_l, torch.float32, "part_l"), rows, splits, d, _dev(out, torch.bfloat16, "out"),
@@ -435,11 +476,11 @@ def decode_paged_emulated(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
         raise AttnError(1, "attn_emulated_num_slots")
     need = int(lib().attn_emulated_workspace_bytes(N, Hq, d, slots))
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty((need,), torch.uint8, q.device, stream)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((N, Hq), torch.float32, q.device, stream)
     st = lib().attn_decode_paged_emulated(
         _dev(q, torch.bfloat16, "q"), _dev(k_cache, torch.bfloat16, "k_cache"),
         _dev(v_cache, torch.bfloat16, "v_cache"), _dev(block_table, torch.int32, "block_table"),
@@ -470,9 +511,9 @@ def merge_emulated(numerics: str, part_o: torch.Tensor, part_m: torch.Tensor, pa
     if part_m.shape != (rows, splits) or part_l.shape != (rows, splits):
         raise ValueError("part_m and part_l must be [rows, splits]")
     dev = part_o.device
-    o32 = torch.empty((rows, d), dtype=torch.float32, device=dev) if want_f32 else None
-    o = torch.empty((rows, d), dtype=torch.bfloat16, device=dev) if want_bf16 else None
-    lse = torch.empty((rows,), dtype=torch.float32, device=dev) if return_lse else None
+    o32 = _empty((rows, d), torch.float32, dev, stream) if want_f32 else None
+    o = _empty((rows, d), torch.bfloat16, dev, stream) if want_bf16 else None
+    lse = _empty((rows,), torch.float32, dev, stream) if return_lse else None
     st = lib().attn_merge_emulated(
         _numerics(numerics), _dev(part_o, torch.float32, "part_o"), _dev(part_m, torch.float32, "part_m"),
         _dev(part_l, torch.float32, "part_l"), rows, splits, d,

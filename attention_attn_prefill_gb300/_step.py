@@ -3,7 +3,8 @@ paged cache and attention over it.
 
 As in ``_lib``, these wrappers check shapes, types and devices, allocate what is not given and pass raw
 pointers.  A call runs on the device its tensors live on, on that device's current stream unless
-``stream`` is given; what it allocates for another stream is recorded there.
+``stream`` is given (what that asks of the caller, and where a call's own memory then comes from, is as
+in ``_lib``).
 """
 from __future__ import annotations
 
@@ -11,7 +12,7 @@ from typing import NamedTuple
 
 import torch
 
-from ._lib import PAGE_TOKENS, _check, lib
+from ._lib import PAGE_TOKENS, _check, _empty_on, _stream_handle, lib
 
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 
@@ -52,25 +53,17 @@ def _stride(t: torch.Tensor, name: str, dev: int) -> int:
     return token if T > 1 else H * d
 
 
-def _run(fn: str, dev: int, stream, made, *args) -> None:
+def _run(fn: str, dev: int, stream, *args) -> None:
     """Calls the C entry point with the stream appended, with device `dev` current."""
     if dev != _current_device():
         with torch.cuda.device(dev):
-            return _run(fn, dev, stream, made, *args)
+            return _run(fn, dev, stream, *args)
     call = _entry.get(fn)
     if call is None:
         call = _entry[fn] = getattr(lib(), fn)
-    if stream is None:
-        status = call(*args, _raw_stream(dev))
-        if status:
-            _check(status, fn)
-        return
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    _check(call(*args, handle), fn)
-    # memory allocated here belongs to the current stream: it may not be reused before `stream` is done
-    on = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=dev)
-    for t in made:
-        t.record_stream(on)
+    status = call(*args, _raw_stream(dev) if stream is None else _stream_handle(stream))
+    if status:
+        _check(status, fn)
 
 
 class StepTables(NamedTuple):
@@ -97,21 +90,20 @@ def step_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: t
         raise ValueError("cached_lens and new_lens must be [N], free_pages [num_free]")
     if block_table.dim() != 2 or block_table.shape[0] != N:
         raise ValueError("block_table must be [N, max_blocks]")
-    made = ()
     if out is None:
-        made = (torch.empty(2 * (num_tokens + N + 1), dtype=_I32, device=dev),)  # one allocation for all five
-        sl = made[0].data_ptr()
+        made = _empty_on(2 * (num_tokens + N + 1), _I32, dev, stream)  # one allocation for all five
+        sl = made.data_ptr()
         cu, pos = sl + 4 * N, sl + 4 * (2 * N + 1)
         slots = pos + 4 * num_tokens
         used = slots + 4 * num_tokens
-        out = StepTables(*torch.unsafe_split_with_sizes(made[0], (N, N + 1, num_tokens, num_tokens, 1)))
+        out = StepTables(*torch.unsafe_split_with_sizes(made, (N, N + 1, num_tokens, num_tokens, 1)))
     else:
         if [t.shape for t in out] != [(N,), (N + 1,), (num_tokens,), (num_tokens,), (1,)]:
             raise ValueError("out must have the shapes of StepTables for these lengths")
         if any(t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous() for t in out):
             _explain(dev, *((t, _I32, "out") for t in out))
         sl, cu, pos, slots, used = (t.data_ptr() for t in out)
-    _run("attn_step_tables", dev, stream, made, cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
+    _run("attn_step_tables", dev, stream, cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
          block_table.data_ptr(), sl, cu, pos, slots, used, N, num_tokens, free_pages.numel(), PAGE_TOKENS,
          block_table.shape[1], num_blocks)
     return out
@@ -122,8 +114,8 @@ def rope_table(max_positions: int, rot: int, theta: float = 10000.0, device=None
     device = torch.device("cuda") if device is None else torch.device(device)
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
-    table = torch.empty((max_positions, rot), dtype=_F32, device=device)
-    _run("attn_rope_table", device.index, stream, (table,), table.data_ptr(), max_positions, rot, float(theta))
+    table = _empty_on((max_positions, rot), _F32, device.index, stream)
+    _run("attn_rope_table", device.index, stream, table.data_ptr(), max_positions, rot, float(theta))
     return table
 
 
@@ -146,18 +138,15 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor | Non
     if dev < 0 or k.shape != (T, Hkv, d):
         raise ValueError("q must be a CUDA tensor [T, Hq, d] and k [T, Hkv, d]")
     paged = k_cache is not None or v_cache is not None
-    made = []
     if q_out is None:
-        q_out, qos = torch.empty((T, Hq, d), dtype=_BF16, device=dev), Hq * d
-        made.append(q_out)
+        q_out, qos = _empty_on((T, Hq, d), _BF16, dev, stream), Hq * d
     else:
         qos = _stride(q_out, "q_out", dev)
         if q_out.shape != q.shape:
             raise ValueError("q_out must have the shape of q")
     kop = kos = 0
     if k_out is None and not paged:
-        k_out, kos = torch.empty((T, Hkv, d), dtype=_BF16, device=dev), Hkv * d
-        made.append(k_out)
+        k_out, kos = _empty_on((T, Hkv, d), _BF16, dev, stream), Hkv * d
         kop = k_out.data_ptr()
     elif k_out is not None:
         kop, kos = k_out.data_ptr(), _stride(k_out, "k_out", dev)
@@ -201,7 +190,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor | Non
                 or not slots.is_contiguous() or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
             _explain(dev, (k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache"), (slots, _I32, "slots"))
         kcp, vcp, sp = k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr()
-    _run("attn_qk_norm_rope", dev, stream, made, q.data_ptr(), qs, k.data_ptr(), ks, vptr, vs, qwp, kwp, eps, pp, tp,
+    _run("attn_qk_norm_rope", dev, stream, q.data_ptr(), qs, k.data_ptr(), ks, vptr, vs, qwp, kwp, eps, pp, tp,
          max_positions, rot, 1 if interleaved else 0, q_out.data_ptr(), qos, kop, kos, kcp, vcp, sp, T, Hq, Hkv, d,
          page, num_blocks)
     return q_out, k_out
@@ -227,7 +216,7 @@ def cache_append_q4(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache
         raise ValueError("cache must be [num_blocks, Hkv, 17 d] matching k")
     if v.shape != k.shape or slots.shape != (T,):
         raise ValueError("k and v must be [T, Hkv, d] and slots [T]")
-    _run("attn_cache_append_q4", dev, stream, (), k.data_ptr(), _stride(k, "k", dev), v.data_ptr(),
+    _run("attn_cache_append_q4", dev, stream, k.data_ptr(), _stride(k, "k", dev), v.data_ptr(),
          _stride(v, "v", dev), slots.data_ptr(), cache.data_ptr(), T, Hkv, d, PAGE_TOKENS, cache.shape[0])
 
 
@@ -253,39 +242,33 @@ def cache_gather_q4(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: to
     d = cache.shape[-1] // 17
     num_blocks, Hkv, max_blocks = _check_paged(dev, d, cache, block_table, seq_lens, N)
     shape = (N, max_blocks * PAGE_TOKENS, Hkv, d)
-    made = []
     if k_out is None:
-        k_out = torch.empty(shape, dtype=_BF16, device=dev)
-        made.append(k_out)
+        k_out = _empty_on(shape, _BF16, dev, stream)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=_BF16, device=dev)
-        made.append(v_out)
+        v_out = _empty_on(shape, _BF16, dev, stream)
     if k_out.shape != shape or v_out.shape != shape:
         raise ValueError("k_out and v_out must be [N, max_blocks * 16, Hkv, d]")
     if (k_out.dtype is not _BF16 or v_out.dtype is not _BF16 or k_out.get_device() != dev
             or v_out.get_device() != dev or not k_out.is_contiguous() or not v_out.is_contiguous()):
         _explain(dev, (k_out, _BF16, "k_out"), (v_out, _BF16, "v_out"))
-    _run("attn_cache_gather_q4", dev, stream, made, cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+    _run("attn_cache_gather_q4", dev, stream, cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
          k_out.data_ptr(), v_out.data_ptr(), N, Hkv, d, PAGE_TOKENS, max_blocks, num_blocks)
     return k_out, v_out
 
 
-def _outputs(dev, q, out, lse, lse_shape, return_lse, workspace, need, made):
+def _outputs(dev, q, out, lse, lse_shape, return_lse, workspace, need, stream):
     """(out, lse, workspace), allocated where not given."""
     if out is None:
-        out = torch.empty(q.shape, dtype=_BF16, device=dev)
-        made.append(out)
+        out = _empty_on(q.shape, _BF16, dev, stream)
     elif out.shape != q.shape or out.dtype is not _BF16 or out.get_device() != dev or not out.is_contiguous():
         _explain(dev, (out, _BF16, "out (of q's shape)"))
     if lse is not None:
         if lse.shape != lse_shape or lse.dtype is not _F32 or lse.get_device() != dev or not lse.is_contiguous():
             _explain(dev, (lse, _F32, f"lse (of shape {list(lse_shape)})"))
     elif return_lse:
-        lse = torch.empty(lse_shape, dtype=_F32, device=dev)
-        made.append(lse)
+        lse = _empty_on(lse_shape, _F32, dev, stream)
     if workspace is None:
-        workspace = torch.empty(need, dtype=_U8, device=dev)
-        made.append(workspace)
+        workspace = _empty_on(need, _U8, dev, stream, returned=False)
     elif workspace.dtype is not _U8 or workspace.get_device() != dev or not workspace.is_contiguous():
         _explain(dev, (workspace, _U8, "workspace"))
     return out, lse, workspace
@@ -314,10 +297,9 @@ def decode_paged_q4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
     num_blocks, Hkv, max_blocks = _check_paged(dev, d, cache, block_table, seq_lens, N)
     if q.dtype is not _BF16 or not q.is_contiguous():
         _explain(dev, (q, _BF16, "q"))
-    made = []
     out, lse, workspace = _outputs(dev, q, out, lse, (N, Hq), return_lse, workspace,
-                                   _decode_ws.get((dev, d)) or decode_q4_workspace_bytes(d, dev), made)
-    _run("attn_decode_paged_q4", dev, stream, made, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
+                                   _decode_ws.get((dev, d)) or decode_q4_workspace_bytes(d, dev), stream)
+    _run("attn_decode_paged_q4", dev, stream, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
          seq_lens.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), N, Hq, Hkv, d, PAGE_TOKENS,
          max_blocks, num_blocks, d ** -0.5 if scale is None else scale, workspace.data_ptr(), workspace.numel())
     return out, lse
@@ -345,10 +327,9 @@ def prefill_paged_q4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
         _explain(dev, (cu_seqlens_q, _I32, "cu_seqlens_q"))
     if cu_seqlens_q.shape != (N + 1,):
         raise ValueError("cu_seqlens_q must be [N + 1]")
-    made = []
     out, lse, workspace = _outputs(dev, q, out, lse, (Hq, T), return_lse, workspace,
-                                   max(1, prefill_q4_workspace_bytes(N, Hkv, d, max_blocks)), made)
-    _run("attn_prefill_paged_q4", dev, stream, made, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
+                                   max(1, prefill_q4_workspace_bytes(N, Hkv, d, max_blocks)), stream)
+    _run("attn_prefill_paged_q4", dev, stream, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
          cu_seqlens_q.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), N,
          max_seqlen_q, T, Hq, Hkv, d, PAGE_TOKENS, max_blocks, num_blocks, d ** -0.5 if scale is None else scale,
          1 if causal else 0, workspace.data_ptr(), workspace.numel())
