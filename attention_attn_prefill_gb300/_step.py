@@ -78,7 +78,8 @@ def step_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: t
                 block_table: torch.Tensor, num_tokens: int, num_blocks: int, out: StepTables | None = None,
                 stream=None) -> StepTables:
     """Tables of one serving step from request lengths [N]; `block_table` [N, max_blocks] is extended in
-    place by pages from the front of `free_pages`.  All int32.  `num_tokens` >= sum(new_lens)."""
+    place by pages from the front of `free_pages`.  All int32.  `num_tokens` >= sum(new_lens).  `out` takes
+    the results in given tensors, none of which may overlap an input (seq_lens is not cached_lens)."""
     dev, N = cached_lens.get_device(), cached_lens.numel()
     if (dev < 0 or new_lens.get_device() != dev or free_pages.get_device() != dev or block_table.get_device() != dev
             or cached_lens.dtype is not _I32 or new_lens.dtype is not _I32 or free_pages.dtype is not _I32

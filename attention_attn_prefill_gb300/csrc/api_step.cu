@@ -41,6 +41,15 @@ bool records_fit(int max_blocks_per_seq, int Hkv) {
   return static_cast<int64_t>(max_blocks_per_seq) * Hkv <= (int64_t(1) << 31) - 1;
 }
 
+struct Ints {
+  const int32_t* at;
+  int64_t n;
+};
+bool overlap(const Ints& a, const Ints& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.n > 0 && b.n > 0 && x < y + 4 * b.n && y < x + 4 * a.n;
+}
+
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
@@ -63,6 +72,17 @@ attn_status_t attn_step_tables(const int32_t* cached_lens, const int32_t* new_le
       static_cast<int64_t>(max_blocks_per_seq) * kPage > kMaxTokens || num_tokens > kMaxTokens ||
       num_seqs > (1 << 24))
     return ATTN_ERR_INVALID_ARG;
+  // every CTA reads the lengths while the first writes its outputs: none may lie in another tensor of the call
+  const Ints outs[] = {{seq_lens, num_seqs},   {cu_seqlens, int64_t(num_seqs) + 1}, {positions, num_tokens},
+                       {slots, num_tokens},    {pages_used, 1},
+                       {block_table, static_cast<int64_t>(num_seqs) * max_blocks_per_seq}};
+  const Ints ins[] = {{cached_lens, num_seqs}, {new_lens, num_seqs}, {free_pages, num_free}};
+  for (const Ints& out : outs) {
+    for (const Ints& in : ins)
+      if (overlap(out, in)) return ATTN_ERR_INVALID_ARG;
+    for (const Ints& other : outs)
+      if (&other != &out && overlap(out, other)) return ATTN_ERR_INVALID_ARG;
+  }
   attn::StepTablesParams p;
   p.cached_lens = cached_lens;
   p.new_lens = new_lens;

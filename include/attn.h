@@ -480,6 +480,9 @@ attn_status_t attn_merge_emulated(int numerics, const float* part_o, const float
  *   positions   [num_tokens] (output): position of each new token in its sequence
  *   slots       [num_tokens] (output): block_table[n][position / 16] * 16 + position % 16
  *   pages_used  [1] (output): pages taken from the front of free_pages
+ * No output, block_table among them, may overlap another tensor of the call: a
+ * step's seq_lens are not its own cached_lens (a program that keeps its lengths
+ * in one place copies them over after the call).
  * num_tokens >= sum of new_lens; the tokens behind the last request (padding,
  * for example of a captured graph) get position 0 and slot -1.  num_tokens may
  * be 0.  Pages go to the requests in order, a request's in the order of its

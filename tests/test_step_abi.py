@@ -31,6 +31,23 @@ def test_step_tables_refusals(attn, over, want):
     assert _call(attn, "attn_step_tables", TABLES, over) == want
 
 
+def _apart():
+    """TABLES with a megabyte between the tensors."""
+    names = ["cached", "new", "free", "bt", "sl", "cu", "pos", "slots", "used"]
+    return dict(TABLES, **{n: FAKE + (i << 20) for i, n in enumerate(names)})
+
+
+@pytest.mark.parametrize("out,other,by", [
+    ("sl", "cached", 0), ("sl", "new", 0), ("cu", "cached", 0), ("cu", "cached", -8), ("sl", "cached", 4),
+    ("pos", "new", 4), ("slots", "free", 12), ("used", "free", 0), ("used", "cached", 4), ("pos", "slots", -28),
+    ("cu", "sl", 4), ("bt", "free", -28), ("bt", "cached", 0), ("used", "bt", 28), ("sl", "bt", -4), ("slots", "cu", 8),
+])
+def test_step_tables_refuses_outputs_in_other_tensors(attn, out, other, by):
+    """Whole or by one element, at either end: N = 2, T = 8, 4 free pages, a table of 2 x 4."""
+    a = _apart()
+    assert getattr(attn.lib(), "attn_step_tables")(*dict(a, **{out: a[other] + by}).values()) == 1
+
+
 @pytest.mark.parametrize("args,want", [
     ((None, 10, 32, 1e4, None), 1), ((FAKE + 4, 10, 32, 1e4, None), 1), ((FAKE, 0, 32, 1e4, None), 1),
     ((FAKE, 10, 0, 1e4, None), 1), ((FAKE, 10, 32, 0.0, None), 1), ((FAKE, 10, 32, float("inf"), None), 1),
