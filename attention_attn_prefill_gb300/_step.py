@@ -191,6 +191,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor | Non
                 or not slots.is_contiguous() or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
             _explain(dev, (k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache"), (slots, _I32, "slots"))
         kcp, vcp, sp = k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr()
+    if T == 0:  # a step without tokens
+        return q_out, k_out
     _run("attn_qk_norm_rope", dev, stream, q.data_ptr(), qs, k.data_ptr(), ks, vptr, vs, qwp, kwp, eps, pp, tp,
          max_positions, rot, 1 if interleaved else 0, q_out.data_ptr(), qos, kop, kos, kcp, vcp, sp, T, Hq, Hkv, d,
          page, num_blocks)
@@ -217,8 +219,11 @@ def cache_append_q4(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache
         raise ValueError("cache must be [num_blocks, Hkv, 17 d] matching k")
     if v.shape != k.shape or slots.shape != (T,):
         raise ValueError("k and v must be [T, Hkv, d] and slots [T]")
-    _run("attn_cache_append_q4", dev, stream, k.data_ptr(), _stride(k, "k", dev), v.data_ptr(),
-         _stride(v, "v", dev), slots.data_ptr(), cache.data_ptr(), T, Hkv, d, PAGE_TOKENS, cache.shape[0])
+    ks, vs = _stride(k, "k", dev), _stride(v, "v", dev)
+    if T == 0:  # a step without tokens
+        return
+    _run("attn_cache_append_q4", dev, stream, k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), cache.data_ptr(),
+         T, Hkv, d, PAGE_TOKENS, cache.shape[0])
 
 
 def _check_paged(dev, d, cache, block_table, seq_lens, N):
@@ -330,6 +335,8 @@ def prefill_paged_q4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
         raise ValueError("cu_seqlens_q must be [N + 1]")
     out, lse, workspace = _outputs(dev, q, out, lse, (Hq, T), return_lse, workspace,
                                    max(1, prefill_q4_workspace_bytes(N, Hkv, d, max_blocks)), stream)
+    if T == 0:  # a step without tokens
+        return out, lse
     _run("attn_prefill_paged_q4", dev, stream, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
          cu_seqlens_q.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), N,
          max_seqlen_q, T, Hq, Hkv, d, PAGE_TOKENS, max_blocks, num_blocks, d ** -0.5 if scale is None else scale,

@@ -463,7 +463,9 @@ attn_status_t attn_merge_emulated(int numerics, const float* part_o, const float
  * keys and writes K and V to the paged bf16 cache (or attn_cache_append_q4 to
  * a 4-bit one); then attn_decode_paged / attn_prefill_paged run on the bf16
  * cache, attn_decode_paged_q4 / attn_prefill_paged_q4 on the 4-bit one.  A
- * slot is page * 16 + row: the place of one token in a paged cache.
+ * slot is page * 16 + row: the place of one token in a paged cache.  A step may
+ * have no tokens for attn_step_tables; the others take at least one (the
+ * Python functions check their arguments and return without a launch for none).
  */
 
 /*

@@ -677,6 +677,36 @@ def test_a_serving_run(attn, gpu, four_bit):
         cached = tb.seq_lens.clone()
 
 
+@pytest.mark.parametrize("d", [64, 256])
+def test_a_step_without_tokens(attn, gpu, d):
+    """No request brings a token: every call of the step passes, and nothing changes.  Wrong arguments are
+    refused all the same."""
+    N, Hq, Hkv, num_blocks = 2, 4, 2, 6
+    cached, bt = _i32([20, 5], gpu), _i32([[3, 1, 0], [2, 0, 0]], gpu)
+    cache = torch.randint(0, 256, (num_blocks, Hkv, 17 * d), dtype=torch.uint8, device=gpu)
+    kc, vc = _randn((num_blocks, PAGE, Hkv, d), 1, gpu), _randn((num_blocks, PAGE, Hkv, d), 2, gpu)
+    before = [x.clone() for x in (bt, cache, kc, vc)]
+    tb = attn.step_tables(cached, _i32([0, 0], gpu), _i32([4, 5], gpu), bt, 0, num_blocks)
+    assert tb.seq_lens.tolist() == [20, 5] and tb.cu_seqlens.tolist() == [0, 0, 0] and int(tb.pages_used) == 0
+    q, k, v = (x.unflatten(1, (-1, d)) for x in
+               torch.empty((0, (Hq + 2 * Hkv) * d), dtype=torch.bfloat16, device=gpu).split([Hq * d, Hkv * d, Hkv * d], 1))
+    table, w = attn.rope_table(32, d, device=gpu), torch.ones(d, dtype=torch.bfloat16, device=gpu)
+    qr, kr = attn.qk_norm_rope(q, k, tb.positions, table, w, w)
+    assert qr.shape == (0, Hq, d) and kr.shape == (0, Hkv, d)
+    qr, none = attn.qk_norm_rope(q, k, tb.positions, table, w, w, v=v, k_cache=kc, v_cache=vc, slots=tb.slots)
+    assert qr.shape == (0, Hq, d) and none is None
+    attn.cache_append_q4(kr, v, tb.slots, cache)
+    o, lse = attn.prefill_paged_q4(qr, cache, bt, tb.cu_seqlens, tb.seq_lens, 0)
+    assert o.shape == (0, Hq, d) and lse.shape == (Hq, 0)
+    assert all(torch.equal(a, b) for a, b in zip((bt, cache, kc, vc), before))
+    with pytest.raises(ValueError):
+        attn.qk_norm_rope(q, k, tb.positions, table, w[:16], w)
+    with pytest.raises(ValueError):
+        attn.cache_append_q4(kr, v[:, :1], tb.slots, cache)
+    with pytest.raises(ValueError):
+        attn.prefill_paged_q4(qr, cache, bt, tb.cu_seqlens[:2], tb.seq_lens, 0)
+
+
 def test_captured_steps(attn, gpu):
     """Two captured decode steps (tables, norm + rotation, 4-bit write, attention) replayed over new lengths
     and inputs give what eager calls give; each has a workspace of its own."""
