@@ -63,6 +63,7 @@ constexpr uint32_t V_MASK1 = 0x00f000f0u, V_MAGIC1 = 0x54005400u;  // 64 + c
 constexpr float P_LIMIT = 64.f;               // a probability above it moves the reference maximum
 constexpr uint32_t V_BITS = 6;                // where a group's unit puts the largest scale
 constexpr uint32_t V_ROOM = 2;                // powers of two a scale may grow by before the unit moves
+constexpr uint32_t PAST_ALL = 0x7f800000u;    // a float's bits from which on it is no finite number
 constexpr uint32_t Z_MASK = 0x00780000u, Z_MAGIC = 0x41800000u;  // a zero point on the same bits of a float: 16 + z
 
 // P: pages a warp takes at a step; ROWS / P query heads.
@@ -644,11 +645,13 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
       if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
         for (int e = 0; e < NG; ++e) {
-          // exponents; a NaN scale says nothing about the others' range
-          const uint32_t s0 = __float_as_uint(vp[0].scale(e)) >> 23, s1 = __float_as_uint(vp[1].scale(e)) >> 23;
-          uint32_t to = __reduce_max_sync(0xffffffffu, max(s0 < 255 ? s0 : 0u, s1 < 255 ? s1 : 0u));
-          if (to == 0 && v_unit[e] == 0.f) continue;
-          to = max(to, V_BITS + 1);
+          // the largest scale's bits; a NaN scale says nothing about the others' range
+          const uint32_t s0 = __float_as_uint(vp[0].scale(e)), s1 = __float_as_uint(vp[1].scale(e));
+          const uint32_t top = __reduce_max_sync(0xffffffffu, max(s0 < PAST_ALL ? s0 : 0u, s1 < PAST_ALL ? s1 : 0u));
+          if (top == 0 && v_unit[e] == 0.f) continue;
+          // its exponent.  Below 2^(V_BITS - 126), scales without one (subnormal) among them, the unit stays
+          // 2^126, whose reciprocal is the smallest normal number.
+          const uint32_t to = max(top >> 23, V_BITS + 1);
           const float unit = __uint_as_float((254 + V_BITS - to) << 23);  // the largest scale: [2^V_BITS, 2 of it)
           if (v_unit[e] != 0.f && unit >= v_unit[e]) continue;
           const float f = v_unit[e] == 0.f ? 0.f : unit / v_unit[e];

@@ -611,7 +611,8 @@ size_t attn_decode_q4_workspace_bytes(int d);
  * float32 scores, sums and accumulators; each probability times its value's
  * scale enters the product with V as one fp16 number: 11 bits down to 2^-20 of
  * the largest scale that a sequence's values have in that group of channels,
- * 2^-31 of that scale in absolute terms below it.
+ * 2^-31 of that scale in absolute terms below it (2^-151 where the largest
+ * scale is below 2^-120).
  * workspace: device buffer, 16-byte aligned, of at least
  * attn_decode_q4_workspace_bytes(d) bytes.  What a call reads from it the same
  * call has written; calls that overlap on the GPU (two streams, two graphs)

@@ -482,6 +482,38 @@ def test_decode_q4_value_ranges(attn, gpu, which, Hq, Hkv, d):
     _check_decode(o, lse, q, lens, os_.stored(_np(k)), os_.stored(_np(v)), 1 / math.sqrt(d), which)
 
 
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (8, 1, 128), (8, 2, 128), (2, 2, 256), (5, 1, 256)])
+@pytest.mark.parametrize("later", [None, -110, 3])
+def test_decode_q4_subnormal_scales(attn, gpu, later, Hq, Hkv, d):
+    """V whose scales all lie below 2^-126, or do so at first.  With queries of zero every probability is 1, x = s
+    times a power of two is an fp16 number and a share's sums are of integers below 2^24, so that the output is off
+    by its own rounding (2^-8 relative, 2^-134 below 2^-126) and by the merge of up to 80 partials in 32 bits (under
+    2^-16).  Where larger scales follow, x of the small ones is off by 2^-31 of the largest: 15 of that at a token."""
+    lens = [2500, 35, 3]
+    cache, table, sl, k, v, slots = _cache_case(lens, Hkv, d, 65, gpu)
+    v = v.double().abs() * 2.0 ** -128
+    if later is not None:
+        v[700:2500] *= 2.0 ** (later + 128)
+    v = v.to(torch.bfloat16)
+    attn.cache_append_q4(k, v, slots, cache)
+    q = torch.zeros((3, Hq, d), dtype=torch.bfloat16, device=gpu)
+    o, lse = attn.decode_paged_q4(q, cache, table, sl)
+    stored, scales = os_.stored(_np(v)), os_.quantise(_np(v))[1]
+    at = 0
+    for n, length in enumerate(lens):
+        most = scales[at:at + length].max()
+        assert most > 0 and (later is not None and n == 0 or most < 2.0 ** -126)
+        want = stored[at:at + length].mean(0).repeat(Hq // Hkv, 0)
+        tol = 2.0 ** -134 + (2.0 ** -8 + 2.0 ** -16) * want + (15 * 2.0 ** -31 * most if most >= 2.0 ** -120 else 0)
+        assert (np.abs(_np(o[n]) - want) <= tol).all() and (want > 0).mean() > 0.9
+        at += length
+    assert np.abs(_np(lse) - np.log(lens)[:, None]).max() <= 2.0 ** -18
+    # and with ordinary queries
+    q = _randn((3, Hq, d), 66, gpu)
+    o, lse = attn.decode_paged_q4(q, cache, table, sl)
+    _check_decode(o, lse, q, lens, os_.stored(_np(k)), stored, 1 / math.sqrt(d), "subnormal")
+
+
 def test_decode_q4_huge_values_behind_other_values(attn, gpu):
     """A NaN page, then ordinary ones: only the NaN's group of channels is lost, whatever comes after it."""
     d, L = 256, 900
