@@ -46,6 +46,12 @@ namespace attn {
 
 __device__ uint32_t g_decode_q4_status;
 
+#ifdef ATTN_TEST_DROP_COPY
+// Test-only builds (never the product library), in the CTA that begins sequence 0: 1: the loading warp leaves out
+// its first copy; 2: it leaves at once.  The waits for what is then missing run out after ATTN_WAIT_LIMIT_NS.
+__device__ int g_test_drop_copy_q4;
+#endif
+
 namespace {
 
 using q4::PAGE;
@@ -375,6 +381,10 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
     const bool serves = lane < NW;
     if (serves && i < count) fetch();
     uint64_t since = global_timer_ns();
+#ifdef ATTN_TEST_DROP_COPY
+    const int drop = s_start.x == 0 && s_start.y == 0 && s_start.z == 0 ? g_test_drop_copy_q4 : 0;
+    ok = drop != 2;
+#endif
     while (ok && seg_i < count) {
       const int slot = lane + NW * stage_k;
       const bool go = serves && i < count && mbar_test_wait(&empty[slot], phase);
@@ -389,6 +399,9 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
             set_error(&g_decode_q4_status, kDevBadPage);
             id = 0;
           }
+#ifdef ATTN_TEST_DROP_COPY
+          if (drop == 1 && i == 0) continue;
+#endif
           bulk_load(smem + slot * C::STAGE + a * R::BYTES,
                     p.cache + (static_cast<int64_t>(id) * p.Hkv + cur.u / geo.tiles) * R::BYTES, R::BYTES, &full[slot]);
         }
@@ -703,6 +716,9 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[slot]);
     }
+    // A wait that ran out is this warp's last: waits of the others that need it run out once too, and not for
+    // every segment that is left.
+    if (!ok) break;
 
     // ---- this warp's state to shared memory, then the CTA's to global memory.  With two pages, a head's
     // sums are in columns c and c + 4, two lanes apart.
@@ -726,8 +742,9 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
     for (int e = 0; e < NG; ++e) v_back[e] = __uint_as_float((254u << 23) - __float_as_uint(v_unit[e]));
     // the loading warp has merged the segment before this one
     if (seg > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(rec_free, free_phase)) && ok;
+      ok = __all_sync(0xffffffffu, mbar_wait(rec_free, free_phase));
       free_phase ^= 1;
+      if (!ok) break;
     }
     float* my = merge + warp * C::MERGE;
     if (2 * t < TILE) {
@@ -889,6 +906,12 @@ cudaError_t launch_for(const DecodeQ4Params& p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+#ifdef ATTN_TEST_DROP_COPY
+extern "C" int attn_test_drop_copy_q4(int what) {
+  return static_cast<int>(cudaMemcpyToSymbol(g_test_drop_copy_q4, &what, sizeof(int)));
+}
+#endif
 
 size_t decode_q4_workspace_bytes(int d) {
   const size_t grid = d == 64    ? grid_of_device<64>()
