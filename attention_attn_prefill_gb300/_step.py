@@ -110,13 +110,21 @@ def step_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: t
     return out
 
 
+def _cuda_index(device) -> int:
+    """Index of a CUDA device given as an index, a name, a torch device or None (the current one)."""
+    if isinstance(device, int):
+        return device
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError(f"device must be a CUDA device, got {device}")
+    return torch.cuda.current_device() if device.index is None else device.index
+
+
 def rope_table(max_positions: int, rot: int, theta: float = 10000.0, device=None, stream=None) -> torch.Tensor:
     """Rotation table [max_positions, rot] f32 for qk_norm_rope (cosines, then sines; angles in double)."""
-    device = torch.device("cuda") if device is None else torch.device(device)
-    if device.index is None:
-        device = torch.device("cuda", torch.cuda.current_device())
-    table = _empty_on((max_positions, rot), _F32, device.index, stream)
-    _run("attn_rope_table", device.index, stream, table.data_ptr(), max_positions, rot, float(theta))
+    dev = _cuda_index(device)
+    table = _empty_on((max_positions, rot), _F32, dev, stream)
+    _run("attn_rope_table", dev, stream, table.data_ptr(), max_positions, rot, float(theta))
     return table
 
 
@@ -285,9 +293,7 @@ _decode_ws: dict[tuple[int, int], int] = {}
 
 def decode_q4_workspace_bytes(d: int, device=None) -> int:
     """Bytes of workspace decode_paged_q4 needs on a device (the current one if not given)."""
-    index = device if isinstance(device, int) else None if device is None else torch.device(device).index
-    if index is None:
-        index = torch.cuda.current_device()
+    index = _cuda_index(device)
     if (index, d) not in _decode_ws:
         with torch.cuda.device(index):
             _decode_ws[index, d] = int(lib().attn_decode_q4_workspace_bytes(d))

@@ -146,6 +146,14 @@ def test_wrappers_refuse_host_tensors(attn):
         attn.cache_q4_empty(4, 2, 96)
 
 
+@pytest.mark.parametrize("device", ["cpu", "cpu:0", torch.device("cpu")])
+def test_wrappers_refuse_other_devices_by_name(attn, device):
+    with pytest.raises(ValueError):
+        attn.rope_table(16, 16, device=device)
+    with pytest.raises(ValueError):
+        attn.decode_q4_workspace_bytes(64, device=device)
+
+
 def _bf16(x):
     return torch.from_numpy(np.asarray(x, np.float64)).to(torch.bfloat16).double().numpy()
 
