@@ -492,8 +492,9 @@ attn_status_t attn_merge_emulated(int numerics, const float* part_o, const float
  * A request whose lengths are negative or exceed the block table, for which
  * the free pages do not suffice, or whose tokens do not fit num_tokens, is
  * recorded as device status 6: it takes no page, its seq_len stays
- * cached_len, its tokens get position 0 and slot -1 (and so do those of the
- * requests after it that need pages, once the pages are used up).  A page id
+ * cached_len, its tokens get position 0 and slot -1.  Once a request has found
+ * too few free pages, so has every later one that needs any, though it may be
+ * fewer than are left; those that need none are served.  A page id
  * outside [0, num_blocks) is recorded as 2, the slots on it are -1 and the
  * table is not written.
  */

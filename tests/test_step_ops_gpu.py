@@ -117,6 +117,22 @@ def test_tables_report_what_does_not_fit(attn, gpu):
     assert code == 2 and out.slots.tolist() == [-1] * 16 + [80] and bt.tolist() == [[0, 5]]
 
 
+def test_tables_after_a_request_without_pages(attn, gpu):
+    """A request that finds too few pages ends the taking of pages, also for a later one that needs fewer than are
+    left; requests that need none are served."""
+    cached, new = [0, 0, 3, 0, 16, 5], [16, 80, 1, 0, 1, 11]
+    bt = torch.arange(36, dtype=torch.int32, device=gpu).view(6, 6)
+    before = bt.clone()
+    out = attn.step_tables(_i32(cached, gpu), _i32(new, gpu), _i32([50, 51, 52], gpu), bt, sum(new), 64)
+    assert attn.device_status(clear=True) == 6
+    assert out.seq_lens.tolist() == [16, 0, 4, 0, 16, 16] and int(out.pages_used) == 1
+    assert out.cu_seqlens.tolist() == np.concatenate([[0], np.cumsum(new)]).tolist()
+    assert out.slots.tolist() == (list(range(800, 816)) + [-1] * 80 + [12 * 16 + 3] + [-1]
+                                  + list(range(30 * 16 + 5, 30 * 16 + 16)))
+    before[0, 0] = 50
+    assert torch.equal(bt, before)
+
+
 # ------------------------------------------------------------------------------------------ norm + rotation
 def test_rope_table(attn, gpu):
     """Within half a float32 step of the cosine and sine, far positions too."""
