@@ -8,7 +8,7 @@
 // a page (any prompt), they are put together through shared memory and written as 16-byte words, else
 // byte by byte.  Quantising costs more than the memory allows for unless it is done in pairs: the range
 // by packed bf16 minima and maxima, the division as a product with the reciprocal and one correction
-// (which makes ties exact) on pairs of floats, the codes as 16-bit pairs.
+// by the exact remainder (P. Markstein, IBM J. Res. Dev. 34, 1990) on pairs of floats, the codes as 16-bit pairs.
 // 32002 tokens of 8 heads, d = 128, take 34 us, 24 at the rate of a copy; issue slots bound it (72% used).
 // Read-back: a warp at a record; V words are exchanged between the four lanes that hold 8 neighbouring
 // channels, so that each lane writes 16 bytes.  5.5 to 6.6 TB/s, HBM's rate.
@@ -93,8 +93,9 @@ __device__ __forceinline__ uint32_t quantise(const uint4& raw, uint32_t& param) 
     param = static_cast<uint32_t>(odd >> 32);
     return static_cast<uint32_t>(odd);
   }
-  // x / s rounded once: the product with the reciprocal, corrected by its remainder (exact), so that a
-  // tie is one exactly
+  // x / s by Markstein's correction: q = x inv is off by a few ulp, x - q s is exact as a fused product, and adding
+  // its quotient leaves an error of the last rounding alone.  That is all rint asks for: a tie, j + 1/2, is a float,
+  // so q lands on it; any other x / s keeps 1 / 960 from every tie, x having 8 significant bits and s 4.
   const float inv = rcp_approx(s);
   const float zq = -lo * inv;
   const float zt = fmaf(fmaf(-zq, s, -lo), inv, zq) + MAGIC;

@@ -381,6 +381,58 @@ def test_cache_values_at_the_edges(attn, gpu):
     assert np.array_equal(got, want, equal_nan=True)
 
 
+def _bf16_between(lo, hi):
+    """Every bf16 number x with lo <= x <= hi and |x| >= max(-lo, hi) / 120: all whose code is not the zero point's."""
+    x = np.arange(1 << 16, dtype=np.uint32) << 16
+    with np.errstate(invalid="ignore"):                       # NaN among them
+        x = x.view(np.float32).astype(np.float64)
+        return x[(x >= lo) & (x <= hi) & (np.abs(x) >= max(-lo, hi) / 120)]
+
+
+def _groups_of_every_quotient(exponent):
+    """Groups [n, 64] whose scale is m 2^(exponent - 3), m = 8 .. 15: for each zero point 0 .. 15 every bf16 number of
+    the range, and for each bf16 number as the minimum one group."""
+    rng = np.random.default_rng(exponent + 1000)
+    out = []
+    for m in range(8, 16):
+        s = m * 2.0 ** (exponent - 3)
+        for z in range(16):
+            x = _bf16_between(-z * s, (15 - z) * s)
+            x = np.concatenate([x, np.zeros(-len(x) % 62)]).reshape(-1, 62)
+            ends = np.broadcast_to([-z * s, (15 - z) * s], (len(x), 2))
+            out.append(np.concatenate([ends, x], 1))
+        every = _bf16_between(-15 * s, 15 * s)
+        for lo in every[(every < 0) & (every >= -15 * s)]:
+            ok = every[(every >= lo) & (every <= 15 * s + lo)]
+            if len(ok):
+                out.append(np.concatenate([[lo, ok.max()], rng.choice(ok, 62)])[None])
+    return np.concatenate(out)
+
+
+# the middle of the range, the ends of what the product with a reciprocal takes (s from 10^-20 on), and past them
+@pytest.mark.parametrize("exponent", [0, -66, -67, -70, -100, -120, 84, 119])
+def test_cache_quotients(attn, gpu, exponent):
+    """Every quotient of a bf16 number and a scale that does not round to 0, ties among them: the codes of the
+    definition.  By rows and by pages."""
+    x = _groups_of_every_quotient(exponent)
+    x = np.stack([x, x[::-1]], 1)                             # two heads
+    want = os_.stored(x)
+    t = torch.from_numpy(x).to(torch.bfloat16).to(gpu)
+    assert np.array_equal(_np(t), x)                          # bf16 numbers all
+    T = t.shape[0]
+    table = torch.arange(_pages(T), dtype=torch.int32, device=gpu).view(1, -1)
+    slots = torch.arange(T, dtype=torch.int32, device=gpu)
+    cache = attn.cache_q4_empty(_pages(T), 2, 64, device=gpu)
+    paged = cache.clone()
+    assert T > 1 << 13                                        # over 2^20 values go by pages
+    attn.cache_append_q4(t, t, slots, paged)
+    for at in range(0, T, 8192):
+        attn.cache_append_q4(t[at:at + 8192], t[at:at + 8192], slots[at:at + 8192], cache)
+    assert torch.equal(cache, paged)
+    for got in attn.cache_gather_q4(cache, table, _i32([T], gpu)):
+        assert np.array_equal(_np(got)[0, :T], want)
+
+
 def test_cache_reports(attn, gpu):
     cache, table, sl, k, v, slots = _cache_case([20], 1, 64, 3, gpu)
     want = cache.clone()
