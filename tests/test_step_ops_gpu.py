@@ -198,6 +198,23 @@ def test_norm_rope(attn, gpu, T, Hq, Hkv, d, rot, inter, norm):
     assert torch.equal(q3, qo) and torch.equal(k3, ko)
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("only", ["q", "k"])
+def test_norm_of_one_side(attn, gpu, only, inter):
+    """A weight for queries or for keys alone: the other side is turned without a norm."""
+    T, Hq, Hkv, d, rot = 21, 10, 3, 128, 96
+    q, k, v, pos, cos, sin = _rope_case(T, Hq, Hkv, d, rot, 5, gpu)
+    table = attn.rope_table(5000, rot, 10000.0, device=gpu)
+    w = (1 + 0.3 * torch.randn(d, generator=torch.Generator().manual_seed(6))).to(torch.bfloat16).to(gpu)
+    qw, kw = (w, None) if only == "q" else (None, w)
+    qo, ko = attn.qk_norm_rope(q, k, pos, table, qw, kw, eps=1e-5, interleaved=inter)
+    _check_rope(qo, q, qw, 1e-5, cos, sin, inter, "q")
+    _check_rope(ko, k, kw, 1e-5, cos, sin, inter, "k")
+    both, kboth = attn.qk_norm_rope(q, k, pos, table, w, w, eps=1e-5, interleaved=inter)
+    none, knone = attn.qk_norm_rope(q, k, pos, table, interleaved=inter)
+    assert torch.equal(qo, both if only == "q" else none) and torch.equal(ko, kboth if only == "k" else knone)
+
+
 def test_norm_of_small_large_and_zero_rows(attn, gpu):
     """eps keeps a row of zeros at zero; large rows stay finite."""
     d = 128
