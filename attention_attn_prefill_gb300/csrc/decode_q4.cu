@@ -27,10 +27,11 @@
 // does not depend on the batch.
 //
 // Measured: 64 sequences of 512 to 8192 tokens, 32/8 heads, d = 128: 70 us for 304 MB (45 at the rate of a
-// copy; the copies alone 58); 8 of up to 122,863, 16/2 heads, d = 256: 75 us for 281 MB.  What bounds it is the
-// decoding: of 600 instructions a step of two pages, 256 make operands and 32 are products, and 16 warps an
-// SM (10 at d = 256), all that the registers hold, use 56% of the issue slots.  A lone sequence of 1009 tokens
-// takes 9.4 us: two launches and six reads that wait for each other.
+// copy; the copies alone 58); 8 of up to 122,863, 16/2 heads, d = 256: 75 us for 281 MB.  No
+// resource is full: of 600 instructions a step of two pages, 256 make operands and 32 are products, they depend on
+// one another, and 16 warps an SM (10 at d = 256), all that the registers hold, use 56% of the issue slots.  With
+// two pages a step at d = 256, 42 bytes a thread spill (8/2 heads: 64 us for the 75 above).  A lone sequence of
+// 1009 tokens takes 9.5 us: two launches and six reads that wait for each other.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
