@@ -721,6 +721,31 @@ def test_prefill_q4(attn, gpu, ctx, new, Hq, Hkv, d, causal):
     assert np.abs(_np(lse) - want_l).max() <= 1e-3
 
 
+@pytest.mark.parametrize("fill", [0xFF, 0x7F, 0x00])
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,d", [([0, 40, 0, 129], [0, 3, 0, 129], 4, 2, 128), ([17, 0, 200], [1, 0, 70], 3, 1, 64)])
+def test_prefill_q4_takes_nothing_from_its_workspace(attn, gpu, ctx, new, Hq, Hkv, d, fill):
+    """What a workspace held before (NaN, page numbers out of range) reaches no result; sequences without tokens."""
+    cache, table, sl, k, v = _filled(attn, ctx, Hkv, d, 67, gpu)
+    wide = torch.full((len(ctx), table.shape[1] + 9), -1, dtype=torch.int32, device=gpu)
+    for n, length in enumerate(ctx):
+        wide[n, :_pages(length)] = table[n, :_pages(length)]
+    q = _randn((sum(new), Hq, d), 68, gpu)
+    cu = _i32(np.concatenate([[0], np.cumsum(new)]).tolist(), gpu)
+    need = attn.prefill_q4_workspace_bytes(len(ctx), Hkv, d, wide.shape[1])
+    ws = torch.full((need,), fill, dtype=torch.uint8, device=gpu)
+    o, lse = attn.prefill_paged_q4(q, cache, wide, cu, sl, max(new), workspace=ws)
+    at = kat = 0
+    for length, rows in zip(ctx, new):
+        if rows == 0:
+            kat += length
+            continue
+        want = _attend(_np(q[at:at + rows]), k[kat:kat + length], v[kat:kat + length], 1 / math.sqrt(d))
+        err = np.abs(_np(o[at:at + rows]) - want)
+        assert (err <= 2.0 ** -8 * np.abs(want) + 1.1 * 2.0 ** -8 * np.abs(v).max()).all()
+        at, kat = at + rows, kat + length
+    assert torch.isfinite(lse).all()
+
+
 # ------------------------------------------------------------------------------------------ together
 def _attend(q, k, v, scale):
     """q [R, Hq, d] at the last R positions of k, v [L, Hkv, d], causal."""

@@ -121,6 +121,27 @@ def test_a_call_on_a_side_stream_has_memory_of_its_own(attn, gpu, name, handle):
             assert torch.equal(a, b) or np.array_equal(a.cpu().float().numpy(), b.cpu().float().numpy(), equal_nan=True)
 
 
+def test_a_captured_call_on_a_forked_stream(attn, gpu):
+    """Inside a capture, on a stream forked from the capturing one, everything allocated there."""
+    calls = dict(_calls(attn, gpu))
+    names = ["decode_paged_q4", "prefill_paged_q4", "qk_norm_rope", "decode_paged"]
+    want = [[x.clone() for x in calls[n]()] for n in names]
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = [calls[n](stream=side) for n in names]
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for outs in got:
+            for x in outs:
+                x.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_default_stream_by_its_handle(attn, gpu):
     """Handle 0 is the default stream, from another current stream too."""
     x = _randn((64, 8, 128), 1, gpu)
