@@ -6,40 +6,13 @@
 #include <cmath>
 #include <cstdint>
 
+#include "api_checks.h"
 #include "attn.h"
 #include "step.h"
 
+using namespace attn::api;
+
 namespace {
-
-constexpr int kPage = 16;
-constexpr int64_t kMaxTokens = int64_t(1) << 30;
-
-bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
-bool given(const void* p, uintptr_t bytes) { return p != nullptr && aligned(p, bytes); }
-attn_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
-bool head_dim(int d) { return d == 64 || d == 128 || d == 256; }
-// tokens of heads x d values, `stride` elements apart: rows start on 16 bytes and do not overlap
-bool token_stride(int64_t stride, int heads, int d) {
-  return stride % 8 == 0 && stride >= static_cast<int64_t>(heads) * d && stride <= (int64_t(1) << 32);
-}
-
-// Arguments shared by the entry points that read the 4-bit cache through a block table.
-attn_status_t check_paged_q4(const void* cache, const int32_t* block_table, const int32_t* seq_lens, int num_seqs,
-                             int Hkv, int d, int page_size, int max_blocks_per_seq, int num_blocks) {
-  if (!given(cache, 16) || !given(block_table, 4) || !given(seq_lens, 4)) return ATTN_ERR_INVALID_ARG;
-  if (num_seqs < 1 || num_seqs > 65535 || Hkv < 1 || Hkv > 65535 || max_blocks_per_seq < 1 || num_blocks < 1)
-    return ATTN_ERR_INVALID_ARG;
-  if (page_size != kPage || !head_dim(d)) return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(num_blocks) * kPage > kMaxTokens ||
-      static_cast<int64_t>(max_blocks_per_seq) * kPage > kMaxTokens)
-    return ATTN_ERR_INVALID_ARG;
-  return ATTN_OK;
-}
-
-// the read-back numbers a sequence's records in 32 bits
-bool records_fit(int max_blocks_per_seq, int Hkv) {
-  return static_cast<int64_t>(max_blocks_per_seq) * Hkv <= (int64_t(1) << 31) - 1;
-}
 
 struct Ints {
   const int32_t* at;
@@ -49,8 +22,6 @@ bool overlap(const Ints& a, const Ints& b) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
   return a.n > 0 && b.n > 0 && x < y + 4 * b.n && y < x + 4 * a.n;
 }
-
-size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
@@ -199,7 +170,7 @@ attn_status_t attn_cache_gather_q4(const void* cache, const int32_t* block_table
                                    void* k_out, void* v_out, int num_seqs, int Hkv, int d, int page_size,
                                    int max_blocks_per_seq, int num_blocks, void* stream) {
   const attn_status_t chk =
-      check_paged_q4(cache, block_table, seq_lens, num_seqs, Hkv, d, page_size, max_blocks_per_seq, num_blocks);
+      check_paged(cache, block_table, seq_lens, num_seqs, Hkv, d, page_size, max_blocks_per_seq, num_blocks);
   if (chk != ATTN_OK) return chk;
   if (!given(k_out, 16) || !given(v_out, 16) || !records_fit(max_blocks_per_seq, Hkv)) return ATTN_ERR_INVALID_ARG;
   attn::GatherQ4Params p;
@@ -224,7 +195,7 @@ attn_status_t attn_decode_paged_q4(const void* q, const void* cache, const int32
                                    int page_size, int max_blocks_per_seq, int num_blocks, float scale,
                                    void* workspace, size_t workspace_bytes, void* stream) {
   const attn_status_t chk =
-      check_paged_q4(cache, block_table, seq_lens, num_seqs, Hkv, d, page_size, max_blocks_per_seq, num_blocks);
+      check_paged(cache, block_table, seq_lens, num_seqs, Hkv, d, page_size, max_blocks_per_seq, num_blocks);
   if (chk != ATTN_OK) return chk;
   if (!given(q, 16) || !given(o, 16) || !aligned(lse, 4)) return ATTN_ERR_INVALID_ARG;
   if (Hq < 1 || Hq > 65535 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
@@ -264,40 +235,16 @@ attn_status_t attn_prefill_paged_q4(const void* q, const void* cache, const int3
                                     int num_seqs, int max_seqlen_q, int total_q, int Hq, int Hkv, int d,
                                     int page_size, int max_blocks_per_seq, int num_blocks, float scale, int causal,
                                     void* workspace, size_t workspace_bytes, void* stream) {
-  const attn_status_t chk =
-      check_paged_q4(cache, block_table, seq_lens, num_seqs, Hkv, d, page_size, max_blocks_per_seq, num_blocks);
-  if (chk != ATTN_OK) return chk;
-  // what attn_prefill_paged would refuse, before anything is enqueued
-  if (!given(q, 16) || !given(o, 16) || !aligned(lse, 4) || !given(cu_seqlens_q, 4)) return ATTN_ERR_INVALID_ARG;
-  if (max_seqlen_q < 1 || total_q < 1 || total_q > kMaxTokens || Hq < 1 || Hq > 65535 || Hq % Hkv != 0 ||
-      static_cast<int64_t>(Hq) * d > (1 << 30))
-    return ATTN_ERR_INVALID_ARG;
-  const int64_t q_tiles = (static_cast<int64_t>(max_seqlen_q) + 127) / 128;
-  if (q_tiles > 65535 || q_tiles * num_seqs * Hq > (int64_t(1) << 30)) return ATTN_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
-  const size_t need = attn_prefill_q4_workspace_bytes(num_seqs, Hkv, d, max_blocks_per_seq);
-  if (need == 0) return ATTN_ERR_INVALID_ARG;
-  if (!given(workspace, 256) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
-  const size_t pages = static_cast<size_t>(num_seqs) * max_blocks_per_seq;
-  const size_t half = up256(pages * kPage * Hkv * d * 2);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
   attn::GatherQ4Params p;
-  p.cache = static_cast<const uint8_t*>(cache);
-  p.block_table = block_table;
-  p.seq_lens = seq_lens;
-  p.k_out = reinterpret_cast<__nv_bfloat16*>(ws);
-  p.v_out = reinterpret_cast<__nv_bfloat16*>(ws + half);
-  p.out_table = reinterpret_cast<int32_t*>(ws + 2 * half);
-  p.N = num_seqs;
-  p.Hkv = Hkv;
-  p.d = d;
-  p.max_blocks = max_blocks_per_seq;
-  p.num_blocks = num_blocks;
+  const attn_status_t chk = check_prefill_readback(q, cache, block_table, cu_seqlens_q, seq_lens, o, lse, num_seqs,
+                                                   max_seqlen_q, total_q, Hq, Hkv, d, page_size, max_blocks_per_seq,
+                                                   num_blocks, scale, workspace, workspace_bytes, p);
+  if (chk != ATTN_OK) return chk;
   const cudaError_t e = attn::gather_q4_launch(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return ATTN_ERR_CUDA;
   return attn_prefill_paged(q, p.k_out, p.v_out, p.out_table, cu_seqlens_q, seq_lens, o, lse, num_seqs, max_seqlen_q,
-                            total_q, Hq, Hkv, d, page_size, max_blocks_per_seq, static_cast<int>(pages), scale, causal,
-                            stream);
+                            total_q, Hq, Hkv, d, page_size, max_blocks_per_seq, num_seqs * max_blocks_per_seq, scale,
+                            causal, stream);
 }
 
 }  // extern "C"
