@@ -78,6 +78,17 @@ _SIGNATURES = {
     "attn_decode_paged_q4": (c_int, [c_void_p] * 6 + [c_int] * 7 + [c_float, c_void_p, c_size_t, c_void_p]),
     "attn_prefill_q4_workspace_bytes": (c_size_t, [c_int] * 4),
     "attn_prefill_paged_q4": (c_int, [c_void_p] * 7 + [c_int] * 9 + [c_float, c_int, c_void_p, c_size_t, c_void_p]),
+    "attn_cache_f8_record_bytes": (c_size_t, [c_int]),
+    "attn_cache_append_f8": (c_int, [c_void_p, c_ll] * 2 + [c_void_p] * 3 + [c_int] * 5 + [c_void_p]),
+    "attn_cache_gather_f8": (c_int, [c_void_p] * 5 + [c_int] * 6 + [c_void_p]),
+    "attn_decode_f8_workspace_bytes": (c_size_t, [c_int]),
+    "attn_decode_paged_f8": (c_int, [c_void_p] * 6 + [c_int] * 7 + [c_float, c_void_p, c_size_t, c_void_p]),
+    "attn_decode_blocks_f8": (c_int, [c_void_p] * 6 + [c_int] + [c_void_p] * 2 + [c_int] * 8
+                              + [c_float, c_void_p, c_size_t, c_void_p]),
+    "attn_prefill_f8_workspace_bytes": (c_size_t, [c_int] * 4),
+    "attn_prefill_paged_f8": (c_int, [c_void_p] * 7 + [c_int] * 9 + [c_float, c_int, c_void_p, c_size_t, c_void_p]),
+    "attn_select_blocks_workspace_bytes": (c_size_t, [c_int] * 4),
+    "attn_select_blocks": (c_int, [c_void_p] * 6 + [c_int] * 12 + [c_void_p, c_size_t, c_void_p]),
 }
 
 # Decode numerics of other backends (attn_numerics_t).

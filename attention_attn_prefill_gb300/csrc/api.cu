@@ -603,7 +603,8 @@ attn_status_t attn_device_status(uint32_t* code, int clear) {
   if (cudaDeviceSynchronize() != cudaSuccess) return ATTN_ERR_CUDA;
   uint32_t first = 0;
   for (auto status : {attn::prefill_status, attn::decode_status, attn::step_tables_status, attn::qk_rope_status,
-                      attn::cache_q4_status, attn::decode_q4_status}) {
+                      attn::cache_q4_status, attn::decode_q4_status, attn::cache_f8_status,
+                      attn::decode_f8_status, attn::select_blocks_status}) {
     uint32_t word = 0;
     if (status(&word, clear != 0) != cudaSuccess) return ATTN_ERR_CUDA;
     if (first == 0) first = word;

@@ -1,5 +1,5 @@
 // Internal interface between the C-ABI layer and the serving-step kernels: tables from request
-// lengths, query/key norm with rotation, and the 4-bit paged cache.
+// lengths, query/key norm with rotation, the 4-bit and the 8-bit paged cache, and block selection.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -73,10 +73,62 @@ struct DecodeQ4Params {
 size_t decode_q4_workspace_bytes(int d);  // on the current device; 0 on error
 cudaError_t decode_q4_launch(int d, const DecodeQ4Params& p, cudaStream_t stream);
 
+struct AppendF8Params {
+  const __nv_bfloat16 *k, *v;
+  const int32_t* slots;
+  uint8_t* cache;
+  __nv_bfloat16* bounds;  // [num_blocks][Hkv][2][d] or null
+  int64_t k_stride, v_stride, num_slots;
+  int T, Hkv, d;
+};
+cudaError_t append_f8_launch(const AppendF8Params& p, cudaStream_t stream);
+
+struct GatherF8Params {
+  const uint8_t* cache;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  __nv_bfloat16 *k_out, *v_out;  // [N][max_blocks * 16][Hkv][d]
+  int32_t* out_table;            // [N][max_blocks] or null: the page of k_out that holds each page
+  int N, Hkv, d, max_blocks, num_blocks;
+};
+cudaError_t gather_f8_launch(const GatherF8Params& p, cudaStream_t stream);
+
+struct DecodeF8Params {
+  const __nv_bfloat16* q;  // [T][Hq][d]
+  const uint8_t* cache;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* cu;      // [N + 1] or null: one query a sequence
+  const int32_t* blocks;  // [T][Hkv][K] or null: all blocks
+  __nv_bfloat16* o;       // [T][Hq][d]
+  float* lse;             // [T][Hq] or null
+  void* workspace;
+  int T, N, Hq, Hkv, K, max_blocks, num_blocks;
+  float scale_log2;
+};
+size_t decode_f8_workspace_bytes(int d);  // on the current device; 0 on error
+cudaError_t decode_f8_launch(int d, const DecodeF8Params& p, cudaStream_t stream);
+
+struct SelectBlocksParams {
+  const __nv_bfloat16* q;       // [T][Hq][d]
+  const __nv_bfloat16* bounds;  // [num_blocks][Hkv][2][d]
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* cu;  // [N + 1] or null: one query a sequence
+  int32_t* blocks;    // [T][Hkv][K]
+  void* workspace;
+  int T, N, max_q, Hq, Hkv, d, K, first, last, max_blocks, num_blocks;
+};
+size_t select_blocks_workspace_bytes(int64_t T, int64_t N, int64_t Hkv, int64_t max_blocks);
+cudaError_t select_blocks_launch(const SelectBlocksParams& p, cudaStream_t stream);
+
 cudaError_t step_tables_status(uint32_t* out, bool clear);
 cudaError_t qk_rope_status(uint32_t* out, bool clear);
 cudaError_t cache_q4_status(uint32_t* out, bool clear);
 cudaError_t decode_q4_status(uint32_t* out, bool clear);
+cudaError_t cache_f8_status(uint32_t* out, bool clear);
+cudaError_t decode_f8_status(uint32_t* out, bool clear);
+cudaError_t select_blocks_status(uint32_t* out, bool clear);
 
 // Reads (and optionally clears) a kernel file's device status word.
 template <class Symbol>

@@ -461,8 +461,9 @@ attn_status_t attn_merge_emulated(int numerics, const float* part_o, const float
  * A step of a serving program: attn_step_tables turns request lengths into
  * block tables, positions and slots; attn_qk_norm_rope prepares queries and
  * keys and writes K and V to the paged bf16 cache (or attn_cache_append_q4 to
- * a 4-bit one); then attn_decode_paged / attn_prefill_paged run on the bf16
- * cache, attn_decode_paged_q4 / attn_prefill_paged_q4 on the 4-bit one.  A
+ * a 4-bit one, attn_cache_append_f8 to an 8-bit one); then attn_decode_paged /
+ * attn_prefill_paged run on the bf16 cache, attn_decode_paged_q4 /
+ * attn_prefill_paged_q4 on the 4-bit one, and their _f8 forms.  A
  * slot is page * 16 + row: the place of one token in a paged cache.  A step may
  * have no tokens for attn_step_tables; the others take at least one (the
  * Python functions check their arguments and return without a launch for none).
@@ -643,6 +644,162 @@ attn_status_t attn_prefill_paged_q4(const void* q, const void* cache, const int3
                                     int num_seqs, int max_seqlen_q, int total_q, int Hq, int Hkv, int d,
                                     int page_size, int max_blocks_per_seq, int num_blocks, float scale, int causal,
                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---- The 8-bit paged cache, and attention over blocks that a query selects.
+ *
+ * attn_cache_append_f8 writes a step's keys and values in place of
+ * attn_cache_append_q4; attn_decode_paged_f8 / attn_prefill_paged_f8 attend to
+ * all of a cache.  For long contexts attn_select_blocks picks the pages that
+ * each query is to read, by key bounds that the write keeps, and
+ * attn_decode_blocks_f8 attends to those alone.
+ *
+ * The cache: [num_blocks, Hkv, 32 d + 16] bytes, one record for each page and
+ * KV head (attn_cache_f8_record_bytes(d) for d in {64, 128, 256}, else 0): one
+ * byte a value.
+ * Format: the keys of a page's 16 tokens share a scale, and so do its values:
+ * 2^e with the smallest e >= -124 for which no finite value exceeds 448 2^e.  A
+ * value's code is x 2^-e rounded to the nearest e4m3 number (sign, 4 exponent
+ * and 3 mantissa bits, largest number 448; ties to even) and stands for the code
+ * times 2^e: within 2^-4 of x relatively, or 2^(e - 10) absolutely where the
+ * code is below 2^-6, and a bf16 number exactly (a product past the type's
+ * largest number is an infinity).  An infinity or NaN is kept as NaN.
+ * A record holds 16 tokens:
+ *   bytes [0, 16 d): K codes; channel c of token k is byte
+ *     ((k / 8 * (d / 64) + c / 64) * 32 + 4 (k % 8) + c % 64 / 16) * 16 + c % 16;
+ *   bytes [16 d, 32 d): V codes; with B = min(16, d / 8), channel c of token k is byte
+ *     (((k / 8 * 2 + k % 2) * (d / (8 B)) + c / (8 B)) * 32 + c % (8 B) / B * 4 + k % 8 / 2) * B + c % B;
+ *   bytes [32 d, 32 d + 16): f32 scale of the keys, f32 scale of the values, 8
+ *     bytes unused.
+ * A cache of zeros reads back as zeros.
+ */
+size_t attn_cache_f8_record_bytes(int d);
+
+/*
+ * Writes new tokens into the 8-bit cache.
+ *   k, v   [num_tokens, Hkv, d] bf16, tokens k_stride / v_stride elements apart
+ *          (multiples of 8), the heads of a token dense
+ *   slots  [num_tokens] int32; a token with a negative slot is not written
+ *   cache  [num_blocks, Hkv, 32 d + 16] (in and out)
+ *   bounds [num_blocks, Hkv, 2, d] bf16 (in and out) or NULL: the smallest and
+ *          the largest key, as given, of a page's tokens in each channel; for
+ *          attn_select_blocks
+ * A page's scale belongs to all its tokens.  So the tokens of a call that go to
+ * one page stand next to each other with consecutive slots, in order, as
+ * attn_step_tables gives them, and the non-negative slots of a call are
+ * distinct.  Such a run at rows r .. of a page leaves the rows below r: where its
+ * tokens need a larger scale, the codes of those rows are moved to it (code
+ * times 2^(old - new), rounded again), and the bounds grow.  The rows above the
+ * run no longer hold tokens: a run at row 0 begins the page anew, scale and
+ * bounds included.  A slot past the last page is recorded as device status 8
+ * and its run skipped.
+ */
+attn_status_t attn_cache_append_f8(const void* k, long long k_stride, const void* v, long long v_stride,
+                                   const int32_t* slots, void* cache, void* bounds, int num_tokens, int Hkv, int d,
+                                   int page_size, int num_blocks, void* stream);
+
+/* Reads sequences of the 8-bit cache back; arguments and errors as for attn_cache_gather_q4. */
+attn_status_t attn_cache_gather_f8(const void* cache, const int32_t* block_table, const int32_t* seq_lens,
+                                   void* k_out, void* v_out, int num_seqs, int Hkv, int d, int page_size,
+                                   int max_blocks_per_seq, int num_blocks, void* stream);
+
+/*
+ * Bytes of workspace attn_decode_paged_f8 and attn_decode_blocks_f8 need on the
+ * current device, whatever the batch: two partials of 8 query heads for each
+ * CTA of a grid that fills the device.  0 for a head dim other than 64, 128, 256
+ * or when no CUDA device can be queried.
+ */
+size_t attn_decode_f8_workspace_bytes(int d);
+
+/*
+ * attn_decode_paged over the 8-bit cache: arguments, conventions, errors and
+ * workspace as for attn_decode_paged_q4, with attn_decode_f8_workspace_bytes(d)
+ * bytes.
+ * Arithmetic: products of the codes, exact as fp16, with the queries as fp16
+ * numbers times a power of two a head: their 8 bits are kept down to 2^-28 of
+ * the head's largest channel, and 2^-39 of it in absolute terms below.  float32
+ * scores, sums and accumulators.  Each probability times its values' scale enters
+ * the product with V as one fp16 number: 11 bits down to 2^-22 of the largest
+ * such number that a warp has met in the sequence, 2^-33 of it in absolute terms
+ * below.
+ */
+attn_status_t attn_decode_paged_f8(const void* q, const void* cache, const int32_t* block_table,
+                                   const int32_t* seq_lens, void* o, float* lse, int num_seqs, int Hq, int Hkv, int d,
+                                   int page_size, int max_blocks_per_seq, int num_blocks, float scale,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of single tokens over listed blocks of the 8-bit cache.  A block is
+ * a page: the 16 tokens whose positions divided by 16 give its number.
+ *   q, o         [num_tokens, Hq, d] bf16 (o is output), lse [num_tokens, Hq] f32
+ *                (output, may be NULL)
+ *   cu_seqlens_q [num_seqs + 1] int32 or NULL: q rows cu_seqlens_q[n] ..
+ *                cu_seqlens_q[n+1]-1 are the last tokens of sequence n; NULL: one
+ *                row a sequence (num_tokens == num_seqs)
+ *   seq_lens     [num_seqs] int32: cached tokens, the rows' own included
+ *   blocks       [num_tokens, Hkv, num_selected] int32: numbers of blocks in the
+ *                sequence, in any order, for each row and KV head
+ * A row attends to those tokens of its blocks that it sees: its own position and
+ * what lies before.  Negative entries, and blocks past a row's position, are
+ * passed over; a block that is named twice counts twice.  A row that sees nothing
+ * (also one of more rows than its sequence has tokens) gives o = 0, lse = -inf.
+ * Rows of q that belong to no sequence are left as they were.
+ * Errors on the device: 2 for a page of a named block out of range (page 0 is
+ * read instead), 3 for a seq_len the block table cannot cover (clamped), 5 for
+ * cu_seqlens_q entries that decrease or pass num_tokens.  Arithmetic and
+ * workspace as for attn_decode_paged_f8.
+ */
+attn_status_t attn_decode_blocks_f8(const void* q, const void* cache, const int32_t* block_table,
+                                    const int32_t* cu_seqlens_q, const int32_t* seq_lens, const int32_t* blocks,
+                                    int num_selected, void* o, float* lse, int num_tokens, int num_seqs, int Hq, int Hkv,
+                                    int d, int page_size, int max_blocks_per_seq, int num_blocks, float scale,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace attn_prefill_paged_f8 needs; as attn_prefill_q4_workspace_bytes. */
+size_t attn_prefill_f8_workspace_bytes(int num_seqs, int Hkv, int d, int max_blocks_per_seq);
+
+/* attn_prefill_paged over the 8-bit cache, read back into the workspace; as attn_prefill_paged_q4. */
+attn_status_t attn_prefill_paged_f8(const void* q, const void* cache, const int32_t* block_table,
+                                    const int32_t* cu_seqlens_q, const int32_t* seq_lens, void* o, float* lse,
+                                    int num_seqs, int max_seqlen_q, int total_q, int Hq, int Hkv, int d,
+                                    int page_size, int max_blocks_per_seq, int num_blocks, float scale, int causal,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace attn_select_blocks needs: a score for each row, KV head and
+ * column of the block table, and their error bounds.  0 for invalid arguments.
+ */
+size_t attn_select_blocks_workspace_bytes(int num_tokens, int num_seqs, int Hkv, int max_blocks_per_seq);
+
+/*
+ * Selects the blocks that each query token and KV head attends to.
+ *   q            [num_tokens, Hq, d] bf16
+ *   bounds       [num_blocks, Hkv, 2, d] bf16, as attn_cache_append_f8 keeps them
+ *   block_table  [num_seqs, max_blocks_per_seq] (at most 2^18 columns), and
+ *   cu_seqlens_q, seq_lens as for attn_decode_blocks_f8
+ *   max_seqlen_q upper bound of the rows of a sequence (1 without cu_seqlens_q)
+ *   blocks       [num_tokens, Hkv, num_selected] int32 (output), ascending
+ * Of the blocks that a row sees (its own, and those before): all, if they are at
+ * most num_selected, with -1 behind; else the first `first`, the last `last` and
+ * of the others those with the highest scores, the lower number where scores
+ * are equal.  first >= 0, last >= 1, first + last <= num_selected.  The score of
+ * a block is
+ *   sum_c (neg_c lo_c + pos_c hi_c),  neg_c = sum_g min(q_gc, 0), pos_c = sum_g max(q_gc, 0)
+ * over the channels c and the query heads g of the KV head: the largest sum of
+ * q . k that a key within the bounds could have for each head.  Scores are
+ * compared as 64-bit arithmetic has them; one that is not a number (a NaN or
+ * infinity among its terms) counts as the highest.
+ * Rows of q that belong to no sequence are left as they were in `blocks`.  Errors
+ * on the device: 2 for a page out of range (page 0 is taken), 5 for cu_seqlens_q
+ * or seq_lens that do not fit (a sequence whose rows do not fit num_tokens or
+ * max_seqlen_q is skipped, a length is clamped).
+ * workspace: 256-byte aligned; calls that overlap on the GPU need one each.
+ */
+attn_status_t attn_select_blocks(const void* q, const void* bounds, const int32_t* block_table,
+                                 const int32_t* cu_seqlens_q, const int32_t* seq_lens, int32_t* blocks, int num_selected,
+                                 int first, int last, int num_tokens, int num_seqs, int max_seqlen_q, int Hq, int Hkv,
+                                 int d, int page_size, int max_blocks_per_seq, int num_blocks, void* workspace,
+                                 size_t workspace_bytes, void* stream);
 
 /*
  * Device-side status: waits for all work on the current device, then stores
