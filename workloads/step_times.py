@@ -1,7 +1,7 @@
-"""Times of the serving-step operators on this GPU: `python -m workloads.step_times [name ...]`.
+"""Times of the serving-step operators on this GPU: `python -m workloads.step_times [4-bit|8-bit] [name ...]`.
 
-For each case of perf/operators.py, and for head counts that it does not list, the time of a call among 20 in a
-captured graph, over two sets of inputs in turn (those of the large cases exceed L2, those of the small ones stay in
+For each case of perf/operators.py (4-bit) and of perf/more_operators.py (8-bit), and for head counts that they do not
+list, the time of a call among 20 in a captured graph, over two sets of inputs in turn (those of the large cases exceed L2, those of the small ones stay in
 it), median of nine replays after two.  The decode cases are timed on a bf16 cache of the same lengths too, by the
 same method, with the group size that decode_auto_split_tokens picks.
 """
@@ -13,6 +13,7 @@ import sys
 import torch
 
 import attention_attn_prefill_gb300 as attn
+import perf.more_operators as more_ops
 import perf.operators as ops
 
 CALLS = 20
@@ -56,18 +57,24 @@ def _bf16(state):
 
 
 def main(names) -> None:
-    for case in ops.listed() + FORMS:
-        if names and case["name"] not in names:
-            continue
-        ops.own = False
-        states = [ops.prepare(case, seed) for seed in (1, 2)]
-        ops.own = True
-        us, work = graph_us([lambda s=s: ops.run(s) for s in states]), ops.work(case)
-        line = f"{case['name']:26s} {us:8.2f} us {work['bytes'] / us / 1e3:8.1f} GB/s {work['flops'] / us / 1e6:8.1f} TFLOP/s"
-        if case["op"] == "decode" and case["d"] > 64:  # decode_paged takes head dims of 128 and 256
-            line += f"   bf16 cache {graph_us([_bf16(s) for s in states]):8.2f} us"
-        print(line, flush=True)
-        del states
+    kinds = {"4-bit": ops, "8-bit": more_ops}
+    wanted = [x for x in names if x in kinds] or list(kinds)
+    names = [x for x in names if x not in kinds]
+    for kind in wanted:
+        mod = kinds[kind]
+        for case in mod.listed() + FORMS:
+            if names and case["name"] not in names:
+                continue
+            mod.own = False
+            states = [mod.prepare(case, seed) for seed in (1, 2)]
+            mod.own = True
+            us, work = graph_us([lambda s=s: mod.run(s) for s in states]), mod.work(case)
+            line = (f"{kind} {case['name']:26s} {us:8.2f} us {work['bytes'] / us / 1e3:8.1f} GB/s"
+                    f" {work['flops'] / us / 1e6:8.1f} TFLOP/s")
+            if mod is ops and case["op"] == "decode" and case["d"] > 64:  # decode_paged takes head dims of 128 and 256
+                line += f"   bf16 cache {graph_us([_bf16(s) for s in states]):8.2f} us"
+            print(line, flush=True)
+            del states
 
 
 if __name__ == "__main__":
