@@ -50,7 +50,9 @@ attn_status_t decode_f8(attn::DecodeF8Params& p, const void* q, const void* cach
 bool select_fits(int num_tokens, int num_seqs, int Hkv, int max_blocks_per_seq) {
   return num_tokens >= 1 && num_tokens <= kMaxTokens && num_seqs >= 1 && num_seqs <= 65535 && Hkv >= 1 && Hkv <= 65535 &&
          max_blocks_per_seq >= 1 && max_blocks_per_seq <= kMostBlocks &&
-         static_cast<int64_t>(num_tokens) * Hkv <= (int64_t(1) << 31) - 1;
+         static_cast<int64_t>(num_tokens) * Hkv <= (int64_t(1) << 31) - 1 &&
+         // the kernel numbers tiles of 16 blocks in 32 bits
+         static_cast<int64_t>(num_seqs) * Hkv <= ((int64_t(1) << 31) - 1) / ((max_blocks_per_seq + 15) / 16);
 }
 
 }  // namespace

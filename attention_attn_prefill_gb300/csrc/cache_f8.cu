@@ -233,38 +233,33 @@ __device__ __forceinline__ uint2 values(uint32_t w, float scale) {
   return make_uint2(pack_bf16x2(x.x * scale, x.y * scale), pack_bf16x2(y.x * scale, y.y * scale));
 }
 
-// The first `valid` tokens of a record's keys or values to rows row_stride apart, by a warp
+// The first `valid` tokens of a record's keys or values to rows row_stride apart, by a warp.  A lane takes 8 bytes at a
+// time: neighbouring lanes then write neighbouring 16 bytes, whole sectors at once.
 template <int D, bool IS_V>
 __device__ __forceinline__ void gather_half(const uint8_t* rec, float scale, __nv_bfloat16* out, int64_t row_stride,
                                             int valid, int lane) {
   using R = Record<D>;
-  constexpr int CB = IS_V ? R::VB : 16, CPT = IS_V ? R::VH : R::KJ, TOK = IS_V ? 4 : 2, W = CB / 4;
-  const int g = lane >> 2, t = lane & 3;
-  const uint8_t* codes = rec + (IS_V ? R::V_OFF : R::K_OFF) + lane * CB;
-  uint32_t raw[TOK * CPT][W];
+  constexpr int LOADS = D / 16;
+  const uint8_t* codes = rec + (IS_V ? R::V_OFF : R::K_OFF) + lane * 8;
+  uint2 raw[LOADS];
 #pragma unroll
-  for (int i = 0; i < TOK * CPT; ++i) {
-    if constexpr (CB == 16) {
-      const uint4 x = __ldcs(reinterpret_cast<const uint4*>(codes + i * 32 * CB));
-      raw[i][0] = x.x; raw[i][1] = x.y; raw[i][2] = x.z; raw[i][3] = x.w;
+  for (int i = 0; i < LOADS; ++i) raw[i] = __ldcs(reinterpret_cast<const uint2*>(codes + i * 256));
+#pragma unroll
+  for (int i = 0; i < LOADS; ++i) {
+    constexpr int ROW = IS_V ? 32 * R::VB : 512;  // bytes of a row of the record
+    const int row = i * 256 / ROW, at = i * 256 % ROW + lane * 8;
+    int token, channel;
+    if (IS_V) {
+      const int k = row / R::VH, g = at / (4 * R::VB), t = at / R::VB % 4;
+      token = 8 * (k >> 1) + 2 * t + (k & 1);
+      channel = 8 * R::VB * (row % R::VH) + R::VB * g + at % R::VB;
     } else {
-      const uint2 x = __ldcs(reinterpret_cast<const uint2*>(codes + i * 32 * CB));
-      raw[i][0] = x.x; raw[i][1] = x.y;
+      token = 8 * (row / R::KJ) + at / 64;
+      channel = 64 * (row % R::KJ) + at % 64;
     }
-  }
-#pragma unroll
-  for (int i = 0; i < TOK; ++i) {
-    const int row = IS_V ? 8 * (i >> 1) + 2 * t + (i & 1) : 8 * i + g;
-    if (row >= valid) continue;
-#pragma unroll
-    for (int c = 0; c < CPT; ++c) {
-      const int channel = IS_V ? 8 * CB * c + CB * g : 64 * c + 16 * t;
-#pragma unroll
-      for (int w = 0; w < W; w += 2) {
-        const uint2 a = values(raw[i * CPT + c][w], scale), b = values(raw[i * CPT + c][w + 1], scale);
-        *reinterpret_cast<uint4*>(out + row * row_stride + channel + 4 * w) = make_uint4(a.x, a.y, b.x, b.y);
-      }
-    }
+    if (token >= valid) continue;
+    const uint2 a = values(raw[i].x, scale), b = values(raw[i].y, scale);
+    *reinterpret_cast<uint4*>(out + token * row_stride + channel) = make_uint4(a.x, a.y, b.x, b.y);
   }
 }
 
