@@ -69,8 +69,14 @@ struct Cfg {
   static constexpr int MERGE_OFF = SLOTS * STAGE;
   static constexpr int BAR_OFF = MERGE_OFF + NW * MERGE * 4;
   static constexpr int ALLOC = BAR_OFF + (2 * SLOTS + 2) * 8;
-  static_assert(CTAS * (ALLOC + 1024 + 512) <= 228 * 1024, "shared memory budget");
+  static_assert(CTAS * (ALLOC + 1024 + 24 * THREADS) <= 228 * 1024, "shared memory budget");
 };
+
+// 64-bit division costs over a hundred instructions, and the lists of all but the largest batches are counted in 32 bits
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if ((a | b) >> 32 == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 
 // Sequence of query row r (-1: none) and the tokens that it sees.
 struct RowInfo {
@@ -131,6 +137,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
   constexpr int NW = C::NW, THREADS = C::THREADS, TILE = C::TILE, SLOTS = C::SLOTS;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_weight[NW + 1], s_steps[NW + 1], s_end[2], s_at;
+  __shared__ longlong2 s_before[LISTED ? 1 : THREADS];  // weight and steps of the warp's sequences before a thread's
   __shared__ int3 s_start;
   __shared__ int s_valid[SLOTS][P];  // listed blocks: tokens of each page of a slot that the query sees
   float* merge = reinterpret_cast<float*>(smem + C::MERGE_OFF);
@@ -152,22 +159,27 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
     fence_mbar_init();
   }
   // The list is cut by weight: a (row, unit) weighs its steps and SEGMENT more, what starting on it and
-  // leaving its result cost.
+  // leaving its result cost.  Short lists make fewer shares than CTAs: of one step, they would only be more partials to
+  // merge.  Share b is the weight from b * per on.
   const int b = blockIdx.x;
-  long long W, shares;
+  long long W, per;
+  auto cut_list = [&](long long steps) {
+    const long long most = steps / 2, shares = most >= geo.grid ? geo.grid : most < 1 ? 1 : most;
+    per = quotient(W + shares - 1, shares);
+  };
   if constexpr (LISTED) {
     const int S = (p.K + P - 1) / P;
-    const long long pairs = static_cast<long long>(rows) * units, steps = pairs * S;
+    const long long pairs = static_cast<long long>(rows) * units;
     W = pairs * (S + SEGMENT);
-    const long long most = steps / 2;
-    shares = most >= geo.grid ? geo.grid : most < 1 ? 1 : most;
+    cut_list(pairs * S);
     if (threadIdx.x < 2) {
-      const long long x = b + static_cast<int>(threadIdx.x) < shares ? mul_div(b + threadIdx.x, W, shares) : W;
-      const long long pair = x / (S + SEGMENT);
+      const long long x = per * (b + threadIdx.x) < W ? per * (b + threadIdx.x) : W;
+      const long long pair = quotient(x, S + SEGMENT);
       const int in = static_cast<int>(x - pair * (S + SEGMENT)), step = in > SEGMENT ? in - SEGMENT : 0;
       s_end[threadIdx.x] = pair * S + step;  // steps before x
       if (threadIdx.x == 0) {
-        s_start = make_int3(static_cast<int>(pair / units), static_cast<int>(pair % units), step);
+        const int row = static_cast<int>(quotient(pair, units));
+        s_start = make_int3(row, static_cast<int>(pair - static_cast<long long>(row) * units), step);
         s_at = pair * (S + SEGMENT);
       }
     }
@@ -184,7 +196,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
   } else {
     // ---- total steps, and the sequence that holds this share's first one
     const int N = p.N;
-    const int chunk = (N + THREADS - 1) / THREADS;
+    const int chunk = (N + THREADS - 1) / THREADS;  // sequences a thread counts
     const int n_lo = static_cast<int>(threadIdx.x) * chunk < N ? threadIdx.x * chunk : N;
     const int n_hi = n_lo + chunk < N ? n_lo + chunk : N;
     long long my_weight = 0, my_steps = 0;
@@ -204,6 +216,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
         to_steps += c;
       }
     }
+    s_before[threadIdx.x] = make_longlong2(to_weight - my_weight, to_steps - my_steps);
     if (lane == 31) {
       s_weight[warp] = to_weight;
       s_steps[warp] = to_steps;
@@ -212,41 +225,53 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
     long long weight = 0, steps = 0;
 #pragma unroll
     for (int i = 0; i < NW + 1; ++i) {
-      if (i < warp) {
-        to_weight += s_weight[i];
-        to_steps += s_steps[i];
-      }
       weight += s_weight[i];
       steps += s_steps[i];
     }
     W = weight * units;
-    // Short lists make fewer shares than CTAs: of one step, they would only be more partials to merge
-    const long long most = steps * units / 2;
-    shares = most >= geo.grid ? geo.grid : most < 1 ? 1 : most;
-    const long long lo = b < shares ? mul_div(b, W, shares) : W, hi = b < shares ? mul_div(b + 1, W, shares) : W;
-    if (threadIdx.x == 0) s_end[0] = s_end[1] = steps * units;  // where the share's end is the list's
-    __syncthreads();
-    // the sequences in which the share begins and ends
+    cut_list(steps * units);
+    if (warp < 2) {  // where the share begins (warp 0) and ends
+      const long long x = per * (b + warp);
+      if (x >= W) {
+        if (lane == 0) s_end[warp] = steps * units;
+      } else {
+        // the last warp, and of it the last thread, whose sequences begin at or before x
+        long long at = 0, before = 0;
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const long long x = side ? hi : lo;
-      if (x < (to_weight - my_weight) * units || x >= to_weight * units) continue;
-      long long at = (to_weight - my_weight) * units, before = (to_steps - my_steps) * units;
-      int n = n_lo, ns = 0;
-      for (;; ++n) {
-        ns = steps_of<P>(p.seq_lens, n, p.max_blocks);
-        const long long w = ns > 0 ? static_cast<long long>(ns + SEGMENT) * units : 0;
-        if (x < at + w) break;
-        at += w;
-        before += static_cast<long long>(ns) * units;
-      }
-      const int u = static_cast<int>(mul_div(x - at, 1, ns + SEGMENT));
-      const int in = static_cast<int>(x - at - static_cast<long long>(u) * (ns + SEGMENT));
-      const int step = in > SEGMENT ? in - SEGMENT : 0;
-      s_end[side] = before + static_cast<long long>(u) * ns + step;  // steps before x
-      if (side == 0) {
-        s_start = make_int3(n, u, step);
-        s_at = at + static_cast<long long>(u) * (ns + SEGMENT);
+        for (int i = 0; i < NW; ++i) {
+          if ((at + s_weight[i]) * units > x) break;
+          at += s_weight[i];
+          before += s_steps[i];
+        }
+        int v = 0;
+        long long upto = 0;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+          upto += s_weight[i];
+          v += upto * units <= x ? 1 : 0;
+        }
+        const longlong2 mine = s_before[v * 32 + lane];
+        const int u = 31 - __clz(__ballot_sync(FULL, (at + mine.x) * units <= x));
+        at = (at + __shfl_sync(FULL, mine.x, u)) * units;
+        before = (before + __shfl_sync(FULL, mine.y, u)) * units;
+        int n = (v * 32 + u) * chunk, ns = 0;
+        for (;; ++n) {
+          ns = steps_of<P>(p.seq_lens, n, p.max_blocks);
+          const long long w = ns > 0 ? static_cast<long long>(ns + SEGMENT) * units : 0;
+          if (x < at + w) break;
+          at += w;
+          before += static_cast<long long>(ns) * units;
+        }
+        const int unit = static_cast<int>(quotient(x - at, ns + SEGMENT));
+        const int in = static_cast<int>(x - at - static_cast<long long>(unit) * (ns + SEGMENT));
+        const int step = in > SEGMENT ? in - SEGMENT : 0;
+        if (lane == 0) {
+          s_end[warp] = before + static_cast<long long>(unit) * ns + step;  // steps before x
+          if (warp == 0) {
+            s_start = make_int3(n, unit, step);
+            s_at = at + static_cast<long long>(unit) * (ns + SEGMENT);
+          }
+        }
       }
     }
     // empty sequences: this CTA's part of them
@@ -286,24 +311,35 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
     int4 cut = make_int4(0, 0, -1, 0);
     int i = lane;  // this lane's next step, with the pages' table entries and the tokens that are seen of them
     int ids[P] = {}, seen[P] = {};
+    int listed[P] = {};           // listed blocks: the entries of the step behind, read a step ahead of their pages
+    At<P, LISTED> behind = cur;
     int stage_k = 0;
     uint32_t phase = 1;  // a slot's first use waits for nothing
     int info_row = -1;
     RowInfo info{-1, 0};
-    auto fetch = [&]() {
+    auto read_list = [&]() {  // entries of step `behind`
+      const int32_t* list = p.blocks + (static_cast<int64_t>(behind.n) * p.Hkv + behind.u / geo.tiles) * p.K + behind.step * P;
+#pragma unroll
+      for (int a = 0; a < P; ++a) listed[a] = behind.step * P + a < p.K ? list[a] : -1;
+    };
+    // step `cur`: its pages and what is seen of them; `more`: another step of this lane follows
+    auto fetch = [&](bool more) {
       if constexpr (LISTED) {
         if (info_row != cur.n) {
           info = row_info(p, cur.n);
           info_row = cur.n;
         }
-        const int32_t* list = p.blocks + (static_cast<int64_t>(cur.n) * p.Hkv + cur.u / geo.tiles) * p.K + cur.step * P;
 #pragma unroll
         for (int a = 0; a < P; ++a) {
           seen[a] = 0;
-          const int blk = info.n >= 0 && cur.step * P + a < p.K ? list[a] : -1;
+          const int blk = info.n >= 0 ? listed[a] : -1;
           if (blk < 0 || blk >= p.max_blocks || blk * PAGE >= info.seen) continue;
           seen[a] = info.seen - blk * PAGE < PAGE ? info.seen - blk * PAGE : PAGE;
           ids[a] = p.block_table[static_cast<int64_t>(info.n) * p.max_blocks + blk];
+        }
+        if (more) {
+          behind.go(NW, p, units);
+          read_list();
         }
       } else {
         const int32_t* row = p.block_table + static_cast<int64_t>(cur.n) * p.max_blocks + cur.step * P;
@@ -318,7 +354,11 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
     const bool serves = lane < NW;
     if (serves && i < count) {
       if (lane > 0) cur.go(lane, p, units);
-      fetch();
+      if constexpr (LISTED) {
+        behind = cur;
+        read_list();
+      }
+      fetch(i + NW < count);
     }
     uint64_t since = global_timer_ns();
 #ifdef ATTN_TEST_DROP_COPY
@@ -358,7 +398,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
         i += NW;
         if (i < count) {
           cur.go(NW, p, units);
-          fetch();
+          fetch(i + NW < count);
         }
       }
       const bool merge_now = __all_sync(FULL, mbar_test_wait(rec_full, seg_phase));
@@ -371,46 +411,56 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
         const int64_t part = 2 * b + (starts ? 1 : 0);
         // a row of no sequence has no result
         const bool lives = !LISTED || p.cu == nullptr || row_info(p, seg.n).n >= 0;
-        for (int w = lane; w < heads * (D / 4); w += 32) {
-          const int r = w / (D / 4), x = w % (D / 4) * 4;
-          float M = -INFINITY;
+        // four at a time: one alone would wait for its loads (d = 256, 8 heads: 9700 cycles one by one)
+        constexpr int AT_ONCE = 4;
+        for (int w0 = lane; w0 < heads * (D / 4); w0 += 32 * AT_ONCE) {
+          float M[AT_ONCE], L[AT_ONCE];
+          float4 O[AT_ONCE];
 #pragma unroll
-          for (int v = 0; v < NW; ++v) M = fmaxf(M, merge[v * C::MERGE + r]);
-          float L = 0.f;
-          float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 0; k < AT_ONCE; ++k) {
+            const int w = w0 + 32 * k, r = w < heads * (D / 4) ? w / (D / 4) : 0, x = w % (D / 4) * 4;
+            M[k] = -INFINITY;
 #pragma unroll
-          for (int v = 0; v < NW; ++v) {
-            const float* src = merge + v * C::MERGE;
-            float wl = src[ROWS + r];
-            if (wl == 0.f) continue;  // a warp without tokens
-            wl *= ex2_approx(src[r] - M);
-            const float4 y = *reinterpret_cast<const float4*>(src + 2 * ROWS + r * C::OROW + x);
-            L += wl;
-            O.x = fmaf(y.x, wl, O.x); O.y = fmaf(y.y, wl, O.y);
-            O.z = fmaf(y.z, wl, O.z); O.w = fmaf(y.w, wl, O.w);
-          }
-          const float inv = L == 0.f ? 0.f : 1.f / L;
-          O.x *= inv; O.y *= inv; O.z *= inv; O.w *= inv;
-          if (starts && ends) {
-            if (lives) {
-              const int64_t row = static_cast<int64_t>(seg.n) * p.Hq + kvh * G + h0 + r;
-              *reinterpret_cast<uint2*>(p.o + row * D + x) = make_uint2(pack_bf16x2(O.x, O.y), pack_bf16x2(O.z, O.w));
-              if (x == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(L)) * LN2;
+            for (int v = 0; v < NW; ++v) M[k] = fmaxf(M[k], merge[v * C::MERGE + r]);
+            L[k] = 0.f;
+            O[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int v = 0; v < NW; ++v) {
+              const float* src = merge + v * C::MERGE;
+              const float l = src[ROWS + r];
+              const float wl = l == 0.f ? 0.f : l * ex2_approx(src[r] - M[k]);  // 0: a warp without tokens
+              const float4 y = *reinterpret_cast<const float4*>(src + 2 * ROWS + r * C::OROW + x);
+              L[k] += wl;
+              O[k].x = fmaf(y.x, wl, O[k].x); O[k].y = fmaf(y.y, wl, O[k].y);
+              O[k].z = fmaf(y.z, wl, O[k].z); O[k].w = fmaf(y.w, wl, O[k].w);
             }
-          } else {
-            *reinterpret_cast<float4*>(ws.o + (part * ROWS + r) * D + x) = O;
-            if (x == 0) {
-              ws.m[part * ROWS + r] = M;
-              ws.l[part * ROWS + r] = L;
+            const float inv = L[k] == 0.f ? 0.f : 1.f / L[k];
+            O[k].x *= inv; O[k].y *= inv; O[k].z *= inv; O[k].w *= inv;
+          }
+#pragma unroll
+          for (int k = 0; k < AT_ONCE; ++k) {
+            const int w = w0 + 32 * k, r = w / (D / 4), x = w % (D / 4) * 4;
+            if (w >= heads * (D / 4)) break;
+            if (starts && ends) {
+              if (lives) {
+                const int64_t row = static_cast<int64_t>(seg.n) * p.Hq + kvh * G + h0 + r;
+                *reinterpret_cast<uint2*>(p.o + row * D + x) = make_uint2(pack_bf16x2(O[k].x, O[k].y), pack_bf16x2(O[k].z, O[k].w));
+                if (x == 0 && p.lse != nullptr) p.lse[row] = (M[k] + log2f(L[k])) * LN2;
+              }
+            } else {
+              *reinterpret_cast<float4*>(ws.o + (part * ROWS + r) * D + x) = O[k];
+              if (x == 0) {
+                ws.m[part * ROWS + r] = M[k];
+                ws.l[part * ROWS + r] = L[k];
+              }
             }
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(rec_free);
         if (starts && !ends && lives) {
-          // the share that holds the last step: weight x lies in share ((x + 1) shares - 1) / W
-          const long long past = at + SEGMENT + seg.ns;
-          cut = make_int4(seg.n, seg.u, b, static_cast<int>(mul_div(past * shares - 1, 1, W)));
+          // the share that holds the last step
+          cut = make_int4(seg.n, seg.u, b, static_cast<int>(quotient(at + SEGMENT + seg.ns - 1, per)));
         }
         if (geo.by_unit && starts && lane == 0)
           ws.desc[static_cast<int64_t>(seg.n) * units + seg.u] = ends || !lives ? make_int4(0, 0, -1, 0) : cut;
