@@ -202,8 +202,9 @@ def prefill_paged_f8(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
     return out, lse
 
 
-def select_blocks_workspace_bytes(num_tokens: int, num_seqs: int, Hkv: int, max_blocks: int) -> int:
-    return int(lib().attn_select_blocks_workspace_bytes(num_tokens, num_seqs, Hkv, max_blocks))
+def select_blocks_workspace_bytes(num_tokens: int, num_seqs: int, max_seqlen_q: int, Hkv: int, d: int,
+                                  max_blocks: int) -> int:
+    return int(lib().attn_select_blocks_workspace_bytes(num_tokens, num_seqs, max_seqlen_q, Hkv, d, max_blocks))
 
 
 def select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -230,7 +231,7 @@ def select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tens
           or not out.is_contiguous()):
         _explain(dev, (out, _I32, "out (of shape [T, Hkv, num_selected])"))
     if workspace is None:
-        workspace = _empty_on(max(1, select_blocks_workspace_bytes(T, N, Hkv, block_table.shape[1])), _U8, dev, stream,
+        workspace = _empty_on(max(1, select_blocks_workspace_bytes(T, N, max_seqlen_q, Hkv, d, block_table.shape[1])), _U8, dev, stream,
                               returned=False)
     elif workspace.dtype is not _U8 or workspace.get_device() != dev or not workspace.is_contiguous():
         _explain(dev, (workspace, _U8, "workspace"))

@@ -87,7 +87,7 @@ _SIGNATURES = {
                               + [c_float, c_void_p, c_size_t, c_void_p]),
     "attn_prefill_f8_workspace_bytes": (c_size_t, [c_int] * 4),
     "attn_prefill_paged_f8": (c_int, [c_void_p] * 7 + [c_int] * 9 + [c_float, c_int, c_void_p, c_size_t, c_void_p]),
-    "attn_select_blocks_workspace_bytes": (c_size_t, [c_int] * 4),
+    "attn_select_blocks_workspace_bytes": (c_size_t, [c_int] * 6),
     "attn_select_blocks": (c_int, [c_void_p] * 6 + [c_int] * 12 + [c_void_p, c_size_t, c_void_p]),
 }
 

@@ -160,9 +160,10 @@ attn_status_t attn_prefill_paged_f8(const void* q, const void* cache, const int3
                             causal, stream);
 }
 
-size_t attn_select_blocks_workspace_bytes(int num_tokens, int num_seqs, int Hkv, int max_blocks_per_seq) {
-  if (!select_fits(num_tokens, num_seqs, Hkv, max_blocks_per_seq)) return 0;
-  return attn::select_blocks_workspace_bytes(num_tokens, num_seqs, Hkv, max_blocks_per_seq);
+size_t attn_select_blocks_workspace_bytes(int num_tokens, int num_seqs, int max_seqlen_q, int Hkv, int d,
+                                          int max_blocks_per_seq) {
+  if (!head_dim(d) || max_seqlen_q < 1 || !select_fits(num_tokens, num_seqs, Hkv, max_blocks_per_seq)) return 0;
+  return attn::select_blocks_workspace_bytes(num_tokens, num_seqs, max_seqlen_q, Hkv, d, max_blocks_per_seq);
 }
 
 attn_status_t attn_select_blocks(const void* q, const void* bounds, const int32_t* block_table,
@@ -187,7 +188,8 @@ attn_status_t attn_select_blocks(const void* q, const void* bounds, const int32_
   const int64_t row_tiles = (static_cast<int64_t>(max_q) + 3) / 4;
   if (row_tiles * num_seqs * Hkv > (int64_t(1) << 30)) return ATTN_ERR_INVALID_ARG;
   if (!given(workspace, 256) ||
-      workspace_bytes < attn::select_blocks_workspace_bytes(num_tokens, num_seqs, Hkv, max_blocks_per_seq))
+      workspace_bytes <
+          attn::select_blocks_workspace_bytes(num_tokens, num_seqs, max_seqlen_q, Hkv, d, max_blocks_per_seq))
     return ATTN_ERR_WORKSPACE;
   attn::SelectBlocksParams p;
   p.q = static_cast<const __nv_bfloat16*>(q);

@@ -9,8 +9,9 @@
 // order of summation: scores come from the tensor cores with an error bound, and those blocks that lie within the
 // bound of the border are scored again in 64 bits.
 //
-// Score kernel: a warp holds the bounds of 16 blocks as the left operand, from HBM straight to registers, and
-// multiplies them with up to 32 query rows; Q+- enter as two bf16 numbers each (16 bits), in two columns.
+// Scores: bounds are the left operand, Q+- enter as two bf16 numbers each (16 bits).  Up to FEW rows a sequence (a decode
+// step) are bound by reading the bounds: score_few_kernel.  More (a prompt's chunk) by the products: score_many_kernel,
+// 128 blocks by 64 rows a tcgen05 tile.  Either way
 //   |score - exact| <= eps ||Q|| ||b||,  b = (lo, hi) of a block, by Cauchy and Schwarz on the sum of |terms|.
 // Select kernel: a CTA puts the scores of its row and head into bins over their range, gathers the few in and about the
 // bin that holds the border, and a warp settles the border among them.
@@ -33,8 +34,7 @@ using shares::mma_16816;
 
 constexpr uint32_t FULL = 0xffffffffu;
 constexpr int PAGE = 16;
-constexpr int SCORE_WARPS = 8;
-constexpr int TILE_ROWS = 32;      // query rows a CTA scores
+constexpr int FEW = 4;             // rows a sequence up to which score_few_kernel takes them
 constexpr int BINS = 512;          // of a window of scores
 constexpr int CACHED = 12288;      // scores of a row that shared memory holds
 constexpr int NARROW = 1024;       // columns of a block table, and ...
@@ -47,6 +47,7 @@ struct Scratch {
   float* scores;  // [T][Hkv][stride]
   float* q_norm;  // [T][Hkv]
   float* b_norm;  // [N][Hkv][tiles]: a bound of the largest norm among 16 blocks
+  uint8_t* images;  // [row tiles][Hkv]: the queries' sums, where a sequence has more than FEW rows
   int64_t stride;
   int tiles;
   float eps;
@@ -96,6 +97,23 @@ __device__ __forceinline__ uint32_t add_squares(uint32_t w, uint32_t sum) {
   uint32_t d;
   asm("fma.rn.bf16x2 %0, %1, %1, %2;" : "=r"(d) : "r"(w), "r"(sum));
   return d;
+}
+
+// Adds a pair to its negative and positive sums; a NaN stays one in both
+__device__ __forceinline__ void add_parts(uint32_t w, float* neg, float* pos) {
+  const float2 y = pair_of(w);
+  neg[0] += y.x > 0.f ? 0.f : y.x;
+  pos[0] += y.x < 0.f ? 0.f : y.x;
+  neg[1] += y.y > 0.f ? 0.f : y.y;
+  pos[1] += y.y < 0.f ? 0.f : y.y;
+}
+// A row's norm, from the lanes' sums of squares and whether any of its numbers is not 0
+__device__ __forceinline__ void write_norm(float* to, float squares, uint32_t any, int lane) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) squares += __shfl_xor_sync(FULL, squares, off);
+  any = __reduce_or_sync(FULL, any);
+  // (a NaN passes the comparison)
+  if (lane == 0) *to = any == 0 ? 0.f : squares < LEAST_NORM * LEAST_NORM ? LEAST_NORM : sqrtf(squares);
 }
 
 // A piece of 16 bytes of row r of a tile in shared memory: rows are whole multiples of 128 bytes apart, and a quarter
@@ -283,14 +301,7 @@ __global__ void __launch_bounds__(FewCfg<D>::MOST_WARPS * 32, 1) score_few_kerne
 #pragma unroll
           for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int x = 0; x < D / 64; ++x) {
-              const float2 y = pair_of(heads[e][x]);
-              // a NaN stays one in both sums
-              neg[2 * x] += y.x > 0.f ? 0.f : y.x;
-              pos[2 * x] += y.x < 0.f ? 0.f : y.x;
-              neg[2 * x + 1] += y.y > 0.f ? 0.f : y.y;
-              pos[2 * x + 1] += y.y < 0.f ? 0.f : y.y;
-            }
+            for (int x = 0; x < D / 64; ++x) add_parts(heads[e][x], neg + 2 * x, pos + 2 * x);
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half)
@@ -306,13 +317,7 @@ __global__ void __launch_bounds__(FewCfg<D>::MOST_WARPS * 32, 1) score_few_kerne
             squares = fmaf(a, a, fmaf(b, b, squares));
             any |= hi & 0x7fff7fffu;
           }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) squares += __shfl_xor_sync(FULL, squares, off);
-        any = __reduce_or_sync(FULL, any);
-        // (a NaN passes the comparison)
-        if (at.tile == 0 && lane == 0)
-          ws.q_norm[static_cast<int64_t>(r0 + row) * Hkv + at.h] =
-              any == 0 ? 0.f : squares < LEAST_NORM * LEAST_NORM ? LEAST_NORM : sqrtf(squares);
+        if (at.tile == 0) write_norm(ws.q_norm + static_cast<int64_t>(r0 + row) * Hkv + at.h, squares, any, lane);
       }
     }
     asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -375,176 +380,252 @@ __global__ void __launch_bounds__(FewCfg<D>::MOST_WARPS * 32, 1) score_few_kerne
   }
 }
 
-// CG: groups of four query rows that a CTA takes
-template <int D, int CG>
-__global__ void __launch_bounds__(SCORE_WARPS * 32, D == 256 ? 1 : 2)
-    score_kernel(const SelectBlocksParams p, const Scratch ws, int row_tiles, int chunks) {
-  constexpr int KK = 2 * D / 32;            // 32 of the 2 d terms at a time
-  constexpr int PART = KK < 8 ? KK : 8;     // as many as registers hold
-  constexpr int PARTS = KK / PART;
-  extern __shared__ __align__(16) uint32_t s_q[];  // [CG][KK][8 columns][16 words]
-  const int chunk = blockIdx.x % chunks;
-  const int rest = blockIdx.x / chunks, rt = rest % row_tiles, nh = rest / row_tiles;
-  const int n = nh / p.Hkv, h = nh % p.Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const Span s = span_of(p, n, chunk == 0 && rt == 0 && h == 0 && threadIdx.x == 0);
-  const int r0 = s.first + rt * (4 * CG);
-  const int rows = s.end - r0 < 4 * CG ? s.end - r0 : 4 * CG;
-  if (rows <= 0) return;
-  const int nb = blocks_seen(s, r0 + rows - 1);
-  if (nb <= p.K || chunk * SCORE_WARPS * 16 >= nb) return;  // every block is chosen, or none is this CTA's
-  const bool last_rows = r0 + rows == s.end;  // they see all that the others do: the blocks' norms are theirs to write
+// ---- more rows: the tensor cores take 128 blocks by RT rows at a time
+template <int D>
+struct ManyCfg {
+  static constexpr int RT = D == 256 ? 32 : 64;     // rows of a tile
+  static constexpr int STAGES = D == 256 ? 1 : 2;   // row tiles in flight
+  static constexpr int PANELS = 2 * D / 64;         // 128-byte columns of the 2 d terms
+  static constexpr int A_PANEL = 128 * 128, B_PANEL = RT * 128;
+  static constexpr int A_BYTES = PANELS * A_PANEL;
+  static constexpr int B_BYTES = 2 * PANELS * B_PANEL;  // a row tile: Q- and Q+, first and second bf16 parts
+  static constexpr int B_OFF = A_BYTES;
+  static constexpr int SMEM = A_BYTES + STAGES * B_BYTES;
+  static constexpr uint32_t TMEM_COLS = 2 * RT;     // two accumulators
+  static constexpr int EPILOGUE = 4, LOADER = 4, ISSUER = 5, WARPS = 6;
+};
+constexpr int SUM_ROWS = 16;  // rows a CTA of the kernel that sums the heads takes
 
-  // page of block 16 tile + lane % 16
-  auto page_of = [&](int tile) {
-    const int blk = tile * 16 + (lane & 15);
-    int id = blk < nb ? p.block_table[static_cast<int64_t>(n) * p.max_blocks + blk] : 0;
-    if (id < 0 || id >= p.num_blocks) {
-      set_error(&g_select_blocks_status, kDevBadPage);
-      id = 0;
-    }
-    return id;
-  };
-  // terms 32 PART part .. of this lane's share of blocks 16 tile + g and + 8: 16 bytes of each 64
-  uint32_t a[PART][2][4];
-  auto load = [&](int tile, int id, int part) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int64_t page = __shfl_sync(FULL, id, g + 8 * e);
-      const bool there = tile * 16 + g + 8 * e < nb;
-      const __nv_bfloat16* from = p.bounds + (page * p.Hkv + h) * 2 * D + 32 * PART * part + 8 * t;
-#pragma unroll
-      for (int k = 0; k < PART; ++k) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (there) x = *reinterpret_cast<const uint4*>(from + 32 * k);
-        a[k][e][0] = x.x; a[k][e][1] = x.y; a[k][e][2] = x.z; a[k][e][3] = x.w;
-      }
-    }
-  };
-  int tile = chunk * SCORE_WARPS + warp;
-  int id = 0;
-  if (tile * 16 < nb) id = page_of(tile);
+// Place of row tile i of a sequence whose first row is `first`, among all tiles' images: no two share one
+__host__ __device__ constexpr int64_t tile_place(int64_t first, int64_t n, int64_t i, int RT) { return first / RT + n + i; }
 
-  // ---- Q-, Q+ of the rows, each as two bf16 numbers in neighbouring columns
-  const int G = p.Hq / p.Hkv;
-  for (int i = threadIdx.x; i < CG * 4 * (D / 2); i += SCORE_WARPS * 32) {
-    const int row = i / (D / 2), c = i % (D / 2);  // channels 2 c, 2 c + 1
-    float neg[2] = {0.f, 0.f}, pos[2] = {0.f, 0.f};
-    if (row < rows) {
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q + (static_cast<int64_t>(r0 + row) * p.Hq + h * G) * D) + c;
-      for (int e0 = 0; e0 < G; e0 += 4) {  // four heads' loads in flight
-        uint32_t w[4];
+// Q-, Q+ of a row and KV head, each as two bf16 numbers, into the image of its row tile: [part][panel][row][128 bytes],
+// as the tensor core reads it from shared memory (16-byte pieces exchanged within 128 bytes, by the row)
+template <int D>
+__global__ void __launch_bounds__(SUM_ROWS / 2 * 32) sum_heads_kernel(const SelectBlocksParams p, const Scratch ws, int row_tiles) {
+  using C = ManyCfg<D>;
+  const int rt = blockIdx.x % row_tiles, nh = blockIdx.x / row_tiles, n = nh / p.Hkv, h = nh % p.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.Hq / p.Hkv;
+  const Span s = span_of(p, n, rt == 0 && h == 0 && threadIdx.x == 0);
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {
+    const int at = rt * SUM_ROWS + 2 * warp + e, row = s.first + at;  // at: within the sequence
+    if (row >= s.end) return;
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(p.q + (static_cast<int64_t>(row) * p.Hq + h * G) * D) + lane;
+    float neg[D / 32] = {}, pos[D / 32] = {};  // of channels 2 lane + 64 x and the next
+    for (int e0 = 0; e0 < G; e0 += 4) {        // four heads' loads in flight
+      uint32_t w[4][D / 64];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = e0 + e < G ? q[(e0 + e) * (D / 2)] : 0u;
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 x = pair_of(w[e]);
-          // a NaN stays one in both sums
-          neg[0] += x.x > 0.f ? 0.f : x.x; pos[0] += x.x < 0.f ? 0.f : x.x;
-          neg[1] += x.y > 0.f ? 0.f : x.y; pos[1] += x.y < 0.f ? 0.f : x.y;
-        }
+        for (int x = 0; x < D / 64; ++x) w[k][x] = e0 + k < G ? from[(e0 + k) * (D / 2) + 32 * x] : 0u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) add_parts(w[k][x], neg + 2 * x, pos + 2 * x);
+    }
+    uint8_t* image = ws.images + (tile_place(s.first, n, at / C::RT, C::RT) * p.Hkv + h) * C::B_BYTES;
+    float squares = 0.f;
+    uint32_t any = 0;
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x) {
+        const float a = half ? pos[2 * x] : neg[2 * x], b = half ? pos[2 * x + 1] : neg[2 * x + 1];
+        const uint32_t hi = pack_bf16x2(a, b);
+        const float2 z = pair_of(hi);
+        const int word = half * (D / 2) + 32 * x + lane, r = at % C::RT;
+        uint8_t* to = image + word / 32 * C::B_PANEL + r * 128 + ((word % 32 / 4) ^ (r & 7)) * 16 + word % 4 * 4;
+        *reinterpret_cast<uint32_t*>(to) = hi;
+        *reinterpret_cast<uint32_t*>(to + C::PANELS * C::B_PANEL) = pack_bf16x2(a - z.x, b - z.y);
+        squares = fmaf(a, a, fmaf(b, b, squares));
+        any |= hi & 0x7fff7fffu;
       }
-    }
-    uint32_t* at = s_q + ((row / 4) * KK + c / 16) * 128 + row % 4 * 32 + c % 16;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const float* x = half ? pos : neg;
-      const uint32_t hi = pack_bf16x2(x[0], x[1]);
-      const float2 y = pair_of(hi);
-      at[half * (KK / 2) * 128] = hi;
-      at[half * (KK / 2) * 128 + 16] = pack_bf16x2(x[0] - y.x, x[1] - y.y);
-    }
+    write_norm(ws.q_norm + static_cast<int64_t>(row) * p.Hkv + h, squares, any, lane);
   }
-  __syncthreads();
-  if (chunk == 0)
-    for (int row = warp; row < rows; row += SCORE_WARPS) {
-      float sum = 0.f;
-      uint32_t any = 0;
-      for (int i = lane; i < KK * 16; i += 32) {
-        const uint32_t* at = s_q + ((row / 4) * KK + i / 16) * 128 + row % 4 * 32 + i % 16;
-        any |= at[0] & 0x7fff7fffu;
-        const float2 hi = pair_of(at[0]), lo = pair_of(at[16]);
-        sum = fmaf(hi.x + lo.x, hi.x + lo.x, fmaf(hi.y + lo.y, hi.y + lo.y, sum));
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(FULL, sum, off);
-      any = __reduce_or_sync(FULL, any);
-      // (a NaN passes the comparison)
-      if (lane == 0)
-        ws.q_norm[static_cast<int64_t>(r0 + row) * p.Hkv + h] = any == 0 ? 0.f : sum < LEAST_NORM * LEAST_NORM ? LEAST_NORM : sqrtf(sum);
-    }
+}
 
-  if (tile * 16 < nb) load(tile, id, 0);
-  while (tile * 16 < nb) {
-    const int next = tile + chunks * SCORE_WARPS;
-    int next_id = 0;
-    if (next * 16 < nb) next_id = page_of(next);
-    float* out = ws.scores + (static_cast<int64_t>(r0 + t) * p.Hkv + h) * ws.stride + tile * 16 + g;
-    const int64_t four_rows = 4 * p.Hkv * ws.stride;
-    auto write = [&](int c, const float (&acc)[4]) {  // columns 2 t, 2 t + 1 are row 4 c + t's
-      if (4 * c + t >= rows) return;
-      if (tile * 16 + g < nb) out[c * four_rows] = acc[0] + acc[1];
-      if (tile * 16 + g + 8 < nb) out[c * four_rows + 8] = acc[2] + acc[3];
-    };
-    float acc[PARTS > 1 ? CG : 1][4];
-#pragma unroll
-    for (int c = 0; c < (PARTS > 1 ? CG : 1); ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
-    float norm[2] = {0.f, 0.f};
-#pragma unroll
-    for (int part = 0; part < PARTS; ++part) {
-      if (part > 0) load(tile, id, part);
-      if (last_rows) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t sum[2] = {0u, 0u};
-#pragma unroll
-          for (int k = 0; k < PART; ++k)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) sum[w & 1] = add_squares(a[k][e][w], sum[w & 1]);
-          const float2 x = pair_of(sum[0]), y = pair_of(sum[1]);
-          norm[e] += (x.x + x.y) + (y.x + y.y);
-        }
-      }
-      auto multiply = [&](int c, float (&sum)[4]) {
-#pragma unroll
-        for (int k = 0; k < PART; ++k) {
-          const uint4 b = *reinterpret_cast<const uint4*>(s_q + (c * KK + part * PART + k) * 128 + g * 16 + t * 4);
-          mma_16816<false>(sum, a[k][0][0], a[k][1][0], a[k][0][1], a[k][1][1], b.x, b.y);
-          mma_16816<false>(sum, a[k][0][2], a[k][1][2], a[k][0][3], a[k][1][3], b.z, b.w);
-        }
-      };
-      if constexpr (PARTS > 1) {
-#pragma unroll
-        for (int c = 0; c < CG; ++c)
-          if (4 * c < rows) multiply(c, acc[c]);
-      } else {
-#pragma unroll 2
-        for (int c = 0; c < CG; ++c) {
-          if (4 * c >= rows) break;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          multiply(c, sum);
-          write(c, sum);
-        }
-      }
+// A CTA takes every `chunks`-th tile of 128 blocks of a sequence and KV head: its bounds are gathered through the block
+// table once and multiplied with one row tile after another, which arrive in bulk copies.
+template <int D>
+__global__ void __launch_bounds__(ManyCfg<D>::WARPS * 32, 1)
+    score_many_kernel(const SelectBlocksParams p, const Scratch ws, int chunks) {
+  using C = ManyCfg<D>;
+  constexpr int RT = C::RT, STAGES = C::STAGES, THREADS = C::WARPS * 32;
+  extern __shared__ __align__(1024) uint8_t tiles[];
+  __shared__ uint64_t bars[2 * STAGES + 2 * 2 + 1];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_page[128];
+  uint64_t* b_full = bars;              // [STAGES]
+  uint64_t* b_empty = b_full + STAGES;  // [STAGES]
+  uint64_t* d_full = b_empty + STAGES;  // [2]: a row tile's products are done
+  uint64_t* d_empty = d_full + 2;       // [2]: its scores have been read
+  uint64_t* all_done = d_empty + 2;
+  const int warp = __shfl_sync(FULL, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int chunk = blockIdx.x % chunks, nh = blockIdx.x / chunks, n = nh / p.Hkv, h = nh % p.Hkv;
+  const Span s = span_of(p, n, false);
+  const int rows = s.end - s.first;
+  if (rows <= 0) return;
+  const int nb = blocks_seen(s, s.end - 1);
+  if (nb <= p.K || chunk * 128 >= nb) return;  // every block is chosen, or none is this CTA's
+  if ((smem_u32(tiles) & 1023u) != 0) {         // swizzled tiles need 1 KB alignment
+    if (threadIdx.x == 0) set_error(&g_select_blocks_status, kDevMisaligned);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&b_full[i], 1);
+      mbar_init(&b_empty[i], 1);
     }
-    if constexpr (PARTS > 1) {
-#pragma unroll
-      for (int c = 0; c < CG; ++c) write(c, acc[c]);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], C::EPILOGUE);
     }
-    if (last_rows) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        norm[e] += __shfl_xor_sync(FULL, norm[e], 1);
-        norm[e] += __shfl_xor_sync(FULL, norm[e], 2);
-        if (!(norm[e] < INFINITY)) norm[e] = INFINITY;  // NaN too
+    mbar_init(all_done, 1);
+    fence_mbar_init();
+  }
+  if (warp == C::ISSUER) {
+    tmem_alloc(&s_tmem, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(FULL, s_tmem, 0);
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(FULL, mbar_wait(bar, parity)) != 0; };
+
+  const int row_tiles = (rows + RT - 1) / RT;
+  bool ok = true;
+  int done = 0;    // row tiles so far, over all tiles of blocks
+  int issued = 0;  // of them, those that the loading warp has asked for
+  for (int tile = chunk; tile * 128 < nb; tile += chunks) {
+    // ---- the bounds of 128 blocks, of page 0 where there is none
+    if (threadIdx.x < 128) {
+      const int blk = tile * 128 + threadIdx.x;
+      int id = blk < nb ? p.block_table[static_cast<int64_t>(n) * p.max_blocks + blk] : 0;
+      if (id < 0 || id >= p.num_blocks) {
+        set_error(&g_select_blocks_status, kDevBadPage);
+        id = 0;
       }
-      const float most = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(fmaxf(norm[0], norm[1]))));
+      s_page[threadIdx.x] = id;
+    }
+    __syncthreads();
+#pragma unroll 8
+    for (int i = threadIdx.x; i < 128 * (D / 4); i += THREADS) {
+      const int r = i / (D / 4), piece = i % (D / 4);
+      const __nv_bfloat16* from = p.bounds + (static_cast<int64_t>(s_page[r]) * p.Hkv + h) * 2 * D + piece * 8;
+      const uint32_t to = smem_u32(tiles) + piece / 8 * C::A_PANEL + r * 128 + ((piece % 8) ^ (r & 7)) * 16;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    __syncthreads();
+    // rows see more blocks the later they are: the first row tile with something to score here
+    const int least = tile * 128 > p.K ? tile * 128 : p.K;
+    int first = 0;
+    while (blocks_seen(s, min(s.first + (first + 1) * RT, s.end) - 1) <= least) ++first;
+    const int count = row_tiles - first;
+
+    if (warp == C::LOADER) {
+      for (int i = 0; i < count && ok; ++i) {
+        const int stage = (done + i) % STAGES;
+        ok = wait(&b_empty[stage], ((done + i) / STAGES & 1) ^ 1);
+        if (!ok) break;
+        const int rt = first + i, left = rows - rt * RT;
+        // eight rows at a time, as the exchange of pieces goes; what lies behind the last row is not looked at
+        const uint32_t bytes = (left < RT ? (left + 7) / 8 * 8 : RT) * 128;
+        if (lane == 0) mbar_arrive_expect_tx(&b_full[stage], 2 * C::PANELS * bytes);
+        __syncwarp();
+        const uint8_t* image = ws.images + (tile_place(s.first, n, rt, RT) * p.Hkv + h) * C::B_BYTES;
+        if (lane < 2 * C::PANELS)
+          bulk_load(tiles + C::B_OFF + stage * C::B_BYTES + lane * C::B_PANEL, image + lane * C::B_PANEL, bytes, &b_full[stage]);
+        __syncwarp();
+        issued = done + i + 1;
+      }
+    } else if (warp == C::ISSUER) {
+      constexpr uint32_t IDESC = idesc_bf16_f32(128, RT, 0);  // bounds (K-major) x queries (K-major)
+      for (int i = 0; i < count && ok; ++i) {
+        const int stage = (done + i) % STAGES, buf = (done + i) & 1;
+        ok = wait(&b_full[stage], (done + i) / STAGES & 1) && wait(&d_empty[buf], ((done + i) / 2 & 1) ^ 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a = smem_u32(tiles), b = smem_u32(tiles + C::B_OFF + stage * C::B_BYTES);
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int k = 0; k < 2 * D / 16; ++k)
+            umma_ss_warp(tmem + buf * RT, smem_desc_sw128(a + (k >> 2) * C::A_PANEL + (k & 3) * 32, 16, 1024),
+                         smem_desc_sw128(b + (part * C::PANELS + (k >> 2)) * C::B_PANEL + (k & 3) * 32, 16, 1024), IDESC,
+                         part + k > 0 ? 1u : 0u);
+        umma_commit_warp(&d_full[buf]);
+        umma_commit_warp(&b_empty[stage]);
+      }
+    } else {
+      // ---- norms of the blocks, a thread a block, then its scores of one row after another
+      const int r = threadIdx.x, blk = tile * 128 + r;
+      float norm = 0.f;
+#pragma unroll 1
+      for (int panel = 0; panel < C::PANELS; ++panel) {
+        uint32_t sum[2] = {0u, 0u};
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(tiles + panel * C::A_PANEL + r * 128 + (c ^ (r & 7)) * 16);
+          sum[0] = add_squares(x.x, sum[0]); sum[1] = add_squares(x.y, sum[1]);
+          sum[0] = add_squares(x.z, sum[0]); sum[1] = add_squares(x.w, sum[1]);
+        }
+        const float2 y = pair_of(sum[0]), z = pair_of(sum[1]);
+        norm += (y.x + y.y) + (z.x + z.y);
+      }
+      if (!(norm < INFINITY)) norm = INFINITY;  // NaN too
+      uint32_t most = blk < nb ? __float_as_uint(norm) : 0u;
+      for (int off = 8; off > 0; off >>= 1) most = max(most, __shfl_xor_sync(FULL, most, off));
       // the sum of squares may have been an eighth too small
-      if (lane == 0) ws.b_norm[static_cast<int64_t>(nh) * ws.tiles + tile] = fmaxf(1.1f * sqrtf(most), LEAST_NORM);
+      if (lane % 16 == 0 && blk < nb)
+        ws.b_norm[static_cast<int64_t>(nh) * ws.tiles + blk / 16] = fmaxf(1.1f * sqrtf(__uint_as_float(most)), LEAST_NORM);
+      for (int i = 0; i < count && ok; ++i) {
+        const int buf = (done + i) & 1, row0 = (first + i) * RT;
+        ok = wait(&d_full[buf], (done + i) / 2 & 1);
+        if (!ok) break;
+        tc_fence_after();
+        float* out = ws.scores + (static_cast<int64_t>(s.first + row0) * p.Hkv + h) * ws.stride + blk;
+        const int64_t next = static_cast<int64_t>(p.Hkv) * ws.stride;
+        const int left = rows - row0 < RT ? rows - row0 : RT;
+#pragma unroll
+        for (int c = 0; c < RT; c += 32) {
+          uint32_t x[32];
+          tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + buf * RT + c, x);
+          tmem_ld_wait();
+          if (c + 32 == RT) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&d_empty[buf]);
+          }
+          if (blk < nb) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (c + k < left) out[(c + k) * next] = __uint_as_float(x[k]);
+          }
+        }
+      }
     }
-    tile = next;
-    id = next_id;
-    if (tile * 16 < nb) load(tile, id, 0);
+    done += count;
+    // the products that read these bounds are done where their scores have been read
+    ok = __syncthreads_and(ok);
+    if (!ok) break;
+  }
+  // nothing is on its way to this CTA's memory when it leaves, also after a wait that ran out
+  if (warp == C::ISSUER) {
+    umma_commit_warp(all_done);
+    ok = wait(all_done, 0) && ok;
+  }
+  if (warp == C::LOADER)
+    for (int k = issued > STAGES ? issued - STAGES : 0; k < issued; ++k) ok = wait(&b_full[k % STAGES], k / STAGES & 1) && ok;
+  if (!ok && lane == 0) set_error(&g_select_blocks_status, kDevWaitTimeout);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::ISSUER) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
@@ -943,16 +1024,18 @@ cudaError_t score_few(const SelectBlocksParams& p, const Scratch& ws, cudaStream
   return cudaGetLastError();
 }
 
-template <int D, int CG>
-cudaError_t score_rows(const SelectBlocksParams& p, const Scratch& ws, cudaStream_t stream) {
-  const int row_tiles = (p.max_q + 4 * CG - 1) / (4 * CG);
-  const int64_t pairs = static_cast<int64_t>(p.N) * p.Hkv * row_tiles;
-  const int64_t all = (p.max_blocks + SCORE_WARPS * 16 - 1) / (SCORE_WARPS * 16), most = (SCORE_CTAS + pairs - 1) / pairs;
-  const int chunks = static_cast<int>(all < most ? all : most);
-  const int smem = CG * (2 * D / 32) * 512;
-  const cudaError_t e = cudaFuncSetAttribute(score_kernel<D, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <int D>
+cudaError_t score_many(const SelectBlocksParams& p, const Scratch& ws, cudaStream_t stream) {
+  using C = ManyCfg<D>;
+  const int row_tiles = (p.max_q + SUM_ROWS - 1) / SUM_ROWS;
+  const int64_t pairs = static_cast<int64_t>(p.N) * p.Hkv;
+  sum_heads_kernel<D><<<static_cast<unsigned>(pairs * row_tiles), SUM_ROWS / 2 * 32, 0, stream>>>(p, ws, row_tiles);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(score_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  score_kernel<D, CG><<<static_cast<unsigned>(pairs * chunks), SCORE_WARPS * 32, smem, stream>>>(p, ws, row_tiles, chunks);
+  const int64_t all = (p.max_blocks + 127) / 128, most = (SCORE_CTAS + pairs - 1) / pairs;
+  const int chunks = static_cast<int>(all < most ? all : most);
+  score_many_kernel<D><<<static_cast<unsigned>(pairs * chunks), C::WARPS * 32, C::SMEM, stream>>>(p, ws, chunks);
   return cudaGetLastError();
 }
 
@@ -960,7 +1043,7 @@ template <int D>
 cudaError_t launch(const SelectBlocksParams& p, Scratch& ws, cudaStream_t stream) {
   // the two roundings of Q+-, the sums over heads, and 2 d / 16 products of 16 terms with their final addition
   ws.eps = 1.f / (1 << 18) + static_cast<float>(p.Hq / p.Hkv) / (1 << 24) + static_cast<float>(D / 8 + 2) / (1 << 22);
-  const cudaError_t e = p.max_q <= 4 ? score_few<D>(p, ws, stream) : score_rows<D, TILE_ROWS / 4>(p, ws, stream);
+  const cudaError_t e = p.max_q <= FEW ? score_few<D>(p, ws, stream) : score_many<D>(p, ws, stream);
   if (e != cudaSuccess) return e;
   // few rows leave the latency of one to be shortened; many, the CTAs an SM holds
   const bool many = static_cast<int64_t>(p.T) * p.Hkv >= FEW_ROWS;
@@ -969,8 +1052,11 @@ cudaError_t launch(const SelectBlocksParams& p, Scratch& ws, cudaStream_t stream
 
 }  // namespace
 
-size_t select_blocks_workspace_bytes(int64_t T, int64_t N, int64_t Hkv, int64_t max_blocks) {
-  return up256(T * Hkv * score_stride(max_blocks) * 4) + up256(T * Hkv * 4) + up256(N * Hkv * ((max_blocks + 15) / 16) * 4);
+size_t select_blocks_workspace_bytes(int64_t T, int64_t N, int64_t max_q, int64_t Hkv, int d, int64_t max_blocks) {
+  const int RT = d == 256 ? ManyCfg<256>::RT : ManyCfg<128>::RT;
+  const int64_t images = max_q <= FEW ? 0 : tile_place(T, N, 1, RT);
+  return up256(T * Hkv * score_stride(max_blocks) * 4) + up256(T * Hkv * 4) + up256(N * Hkv * ((max_blocks + 15) / 16) * 4) +
+         images * Hkv * RT * 8 * d;
 }
 
 cudaError_t select_blocks_launch(const SelectBlocksParams& p, cudaStream_t stream) {
@@ -984,6 +1070,8 @@ cudaError_t select_blocks_launch(const SelectBlocksParams& p, cudaStream_t strea
   ws.q_norm = reinterpret_cast<float*>(at);
   at += up256(rows * 4);
   ws.b_norm = reinterpret_cast<float*>(at);
+  at += up256(static_cast<size_t>(p.N) * p.Hkv * ws.tiles * 4);
+  ws.images = at;
   if (p.d == 64) return launch<64>(p, ws, stream);
   if (p.d == 128) return launch<128>(p, ws, stream);
   if (p.d == 256) return launch<256>(p, ws, stream);

@@ -119,7 +119,7 @@ struct SelectBlocksParams {
   void* workspace;
   int T, N, max_q, Hq, Hkv, d, K, first, last, max_blocks, num_blocks;
 };
-size_t select_blocks_workspace_bytes(int64_t T, int64_t N, int64_t Hkv, int64_t max_blocks);
+size_t select_blocks_workspace_bytes(int64_t T, int64_t N, int64_t max_q, int64_t Hkv, int d, int64_t max_blocks);
 cudaError_t select_blocks_launch(const SelectBlocksParams& p, cudaStream_t stream);
 
 cudaError_t step_tables_status(uint32_t* out, bool clear);

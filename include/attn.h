@@ -767,9 +767,12 @@ attn_status_t attn_prefill_paged_f8(const void* q, const void* cache, const int3
 
 /*
  * Bytes of workspace attn_select_blocks needs: a score for each row, KV head and
- * column of the block table, and their error bounds.  0 for invalid arguments.
+ * column of the block table, and their error bounds; with more than 4 rows a
+ * sequence also the queries' sums over the heads of a KV head.  0 for invalid
+ * arguments (also 2^31 tiles of 16 blocks over all sequences and KV heads).
  */
-size_t attn_select_blocks_workspace_bytes(int num_tokens, int num_seqs, int Hkv, int max_blocks_per_seq);
+size_t attn_select_blocks_workspace_bytes(int num_tokens, int num_seqs, int max_seqlen_q, int Hkv, int d,
+                                          int max_blocks_per_seq);
 
 /*
  * Selects the blocks that each query token and KV head attends to.

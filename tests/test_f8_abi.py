@@ -91,9 +91,15 @@ def test_sizes(attn):
     assert L.attn_prefill_f8_workspace_bytes(3, 2, 64, 5) == 2 * up(15 * 16 * 2 * 64 * 2) + up(60)
     assert L.attn_prefill_f8_workspace_bytes(3, 2, 96, 5) == 0
     assert L.attn_decode_f8_workspace_bytes(96) == 0
-    assert L.attn_select_blocks_workspace_bytes(5, 3, 2, 100) == up(10 * 104 * 4) + up(40) + up(6 * 7 * 4)
-    assert L.attn_select_blocks_workspace_bytes(5, 3, 2, (1 << 18) + 1) == 0
-    assert L.attn_select_blocks_workspace_bytes(0, 3, 2, 100) == 0
+    few = up(10 * 104 * 4) + up(40) + up(6 * 7 * 4)
+    assert L.attn_select_blocks_workspace_bytes(5, 3, 1, 2, 128, 100) == few
+    assert L.attn_select_blocks_workspace_bytes(5, 3, 4, 2, 128, 100) == few
+    # a row tile of 64 rows (32 at d = 256) for each sequence, and one for each 64 rows
+    assert L.attn_select_blocks_workspace_bytes(5, 3, 5, 2, 128, 100) == few + 4 * 2 * 64 * 8 * 128
+    assert L.attn_select_blocks_workspace_bytes(5, 3, 5, 2, 256, 100) == few + 4 * 2 * 32 * 8 * 256
+    for bad in ((0, 3, 1, 2, 128, 100), (5, 3, 0, 2, 128, 100), (5, 3, 1, 2, 96, 100), (5, 3, 1, 2, 128, (1 << 18) + 1),
+                (65535, 65535, 1, 1024, 128, 1000)):
+        assert L.attn_select_blocks_workspace_bytes(*bad) == 0
 
 
 def test_wrappers_refuse(attn):
