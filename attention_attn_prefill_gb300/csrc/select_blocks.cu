@@ -390,7 +390,8 @@ struct ManyCfg {
   static constexpr int A_BYTES = PANELS * A_PANEL;
   static constexpr int B_BYTES = 2 * PANELS * B_PANEL;  // a row tile: Q- and Q+, first and second bf16 parts
   static constexpr int B_OFF = A_BYTES;
-  static constexpr int SMEM = A_BYTES + STAGES * B_BYTES;
+  static constexpr int OUT_OFF = B_OFF + STAGES * B_BYTES;  // a tile's scores, [RT][128]
+  static constexpr int SMEM = OUT_OFF + RT * 128 * 4;
   static constexpr uint32_t TMEM_COLS = 2 * RT;     // two accumulators
   static constexpr int EPILOGUE = 4, LOADER = 4, ISSUER = 5, WARPS = 6;
 };
@@ -582,30 +583,33 @@ __global__ void __launch_bounds__(ManyCfg<D>::WARPS * 32, 1)
       // the sum of squares may have been an eighth too small
       if (lane % 16 == 0 && blk < nb)
         ws.b_norm[static_cast<int64_t>(nh) * ws.tiles + blk / 16] = fmaxf(1.1f * sqrtf(__uint_as_float(most)), LEAST_NORM);
-      for (int i = 0; i < count && ok; ++i) {
-        const int buf = (done + i) & 1, row0 = (first + i) * RT;
-        ok = wait(&d_full[buf], (done + i) / 2 & 1);
-        if (!ok) break;
+      // A thread has a block's scores in TMEM, a row of scores lies in one piece: through shared memory, and on in bulk
+      // copies (stored by the threads themselves they took 5500 cycles a tile, three times the products).
+      float* staging = reinterpret_cast<float*>(tiles + C::OUT_OFF);
+      const int held = ws.stride - tile * 128 < 128 ? static_cast<int>(ws.stride) - tile * 128 : 128;  // a multiple of 8
+      for (int i = 0; i < count; ++i) {
+        const int buf = (done + i) & 1, row = (first + i) * RT + r;  // whose scores this thread sends off
+        if (ok) ok = wait(&d_full[buf], (done + i) / 2 & 1);         // after a wait that ran out: none, all the same steps
         tc_fence_after();
-        float* out = ws.scores + (static_cast<int64_t>(s.first + row0) * p.Hkv + h) * ws.stride + blk;
-        const int64_t next = static_cast<int64_t>(p.Hkv) * ws.stride;
-        const int left = rows - row0 < RT ? rows - row0 : RT;
+        tma_store_wait_read0();
+        named_barrier_sync(1, C::EPILOGUE * 32);
 #pragma unroll
         for (int c = 0; c < RT; c += 32) {
           uint32_t x[32];
           tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + buf * RT + c, x);
           tmem_ld_wait();
-          if (c + 32 == RT) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&d_empty[buf]);
-          }
-          if (blk < nb) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (c + k < left) out[(c + k) * next] = __uint_as_float(x[k]);
-          }
+          for (int k = 0; k < 32; ++k) staging[(c + k) * 128 + r] = __uint_as_float(x[k]);
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&d_empty[buf]);
+        fence_proxy_async_smem();
+        named_barrier_sync(1, C::EPILOGUE * 32);
+        if (r < RT && row < rows)
+          bulk_store(ws.scores + (static_cast<int64_t>(s.first + row) * p.Hkv + h) * ws.stride + tile * 128,
+                     staging + r * 128, held * 4);
+        tma_store_commit();
       }
     }
     done += count;
@@ -621,6 +625,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::WARPS * 32, 1)
   if (warp == C::LOADER)
     for (int k = issued > STAGES ? issued - STAGES : 0; k < issued; ++k) ok = wait(&b_full[k % STAGES], k / STAGES & 1) && ok;
   if (!ok && lane == 0) set_error(&g_select_blocks_status, kDevWaitTimeout);
+  tma_store_wait0();
   tc_fence_before();
   __syncthreads();
   if (warp == C::ISSUER) {
@@ -679,7 +684,9 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectBlocksParams p, c
   {
     const float* norms = ws.b_norm + (static_cast<int64_t>(n) * p.Hkv + h) * ws.tiles;
     const float q_norm = ws.q_norm[blockIdx.x];
-    uint32_t most = 0, least = ~0u, top = 0;  // norms by their bits, scores by their order
+    uint32_t most = 0;  // norms by their bits
+    low = INFINITY;
+    high = -INFINITY;
     for (int i = threadIdx.x; i < (nb + 15) / 16; i += T) most = max(most, __float_as_uint(norms[i]));
     float* to = reinterpret_cast<float*>(s_bits + 2 * ((p.max_blocks + 31) / 32));
     const bool keep = nb <= cached;
@@ -688,10 +695,11 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectBlocksParams p, c
       const float x = sc[i];
       if (keep) to[i] = x;
       if (i >= c0) {
-        least = min(least, order_of(x));
-        top = max(top, order_of(x));
+        low = fminf(low, x);
+        high = fmaxf(high, x);
       }
     }
+    uint32_t least = order_of(low), top = order_of(high);
     if (keep) sc = to;
     most = __reduce_max_sync(FULL, most);
     least = __reduce_min_sync(FULL, least);
