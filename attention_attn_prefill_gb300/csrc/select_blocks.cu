@@ -36,9 +36,9 @@ constexpr uint32_t FULL = 0xffffffffu;
 constexpr int PAGE = 16;
 constexpr int FEW = 4;             // rows a sequence up to which score_few_kernel takes them
 constexpr int BINS = 512;          // of a window of scores
-constexpr int CACHED = 12288;      // scores of a row that shared memory holds
-constexpr int NARROW = 1024;       // columns of a block table, and ...
-constexpr int64_t FEW_ROWS = 1024;  // ... rows times heads from which on a row has 128 threads
+constexpr int CACHED_BLOCKS = 12288;  // scores of a row that shared memory holds
+constexpr int NARROW = 1024;       // columns of a block table up to which 128 threads take a row
+constexpr int64_t MANY_ROWS = 1024;  // rows times heads from which on they do so for any table
 // Norms below this count as this: squares of smaller numbers may vanish, and a bound that is too large does no harm
 constexpr float LEAST_NORM = 1e-14f;
 constexpr int64_t SCORE_CTAS = 152 * 4;  // of the grid, about: a block table may be far wider than its sequences
@@ -648,12 +648,17 @@ __device__ __forceinline__ unsigned long long order_of(double x) {
   return u >> 63 ? ~u : u | 1ull << 63;
 }
 
-template <int D, int T>
-__global__ void __launch_bounds__(T) select_kernel(const SelectBlocksParams p, const Scratch ws, int cached) {
+// Words of shared memory before the scores: two bits a block, in whole 16 bytes
+__host__ __device__ constexpr int cache_at(int max_blocks) { return (2 * ((max_blocks + 31) / 32) + 3) / 4 * 4; }
+
+// T threads a row and KV head.  CACHED: shared memory holds its scores, else they are read again and again.
+template <int T, bool CACHED>
+__global__ void __launch_bounds__(T) select_kernel(const SelectBlocksParams p, const Scratch ws) {
   constexpr int NW = T / 32;
-  extern __shared__ __align__(16) uint32_t s_bits[];  // [words] chosen blocks, [words] ties; then [cached] scores
+  extern __shared__ __align__(16) uint32_t s_bits[];  // [words] chosen blocks, [words] ties; then the scores
   __shared__ __align__(16) int s_hist[2][BINS];
-  __shared__ double s_q[2 * D];
+  __shared__ double s_q[2 * 256];
+  const int D = p.d;
   __shared__ float s_score[32];
   __shared__ int s_at[32], s_open[2], s_over[2], s_digit, s_above;
   __shared__ unsigned s_among;
@@ -663,7 +668,7 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectBlocksParams p, c
   const int r = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
   const int n = p.cu == nullptr ? r : sequence_of(p, r);
   const Span s = span_of(p, n, false);
-  for (int i = threadIdx.x; i < 2 * BINS; i += T) s_hist[0][i] = 0;
+  for (int i = threadIdx.x; i < BINS / 4; i += T) reinterpret_cast<int4*>(s_hist[0])[i] = make_int4(0, 0, 0, 0);
   if (threadIdx.x < 2) s_open[threadIdx.x] = s_over[threadIdx.x] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores are there
   if (r < s.first || r >= s.end) return;  // of no sequence: left as it was
@@ -680,27 +685,43 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectBlocksParams p, c
 
   // ---- how far a score may be off, and the scores' range
   const float* sc = ws.scores + static_cast<int64_t>(blockIdx.x) * ws.stride;
-  float low, high, off;
+  float* cache = reinterpret_cast<float*>(s_bits + cache_at(p.max_blocks));
+  const float none = __uint_as_float(0x7fffffffu);  // a NaN: neither above, below nor within a window
+  auto competes = [&](int i) { return i >= c0 && i < c1; };
+  auto score = [&](int i) {  // of a block that competes, else none
+    if constexpr (CACHED) return cache[i];
+    else return competes(i) ? sc[i] : none;
+  };
+  // four scores at a time, of blocks 4 v ..: rows are whole multiples of eight floats apart
+  auto edge = [&](int v) { return 4 * v < c0 || 4 * v + 4 > c1; };
+  auto read_four = [&](int v) {
+    float4 x = *reinterpret_cast<const float4*>(sc + 4 * v);
+    if (edge(v)) {
+      x.x = competes(4 * v) ? x.x : none;
+      x.y = competes(4 * v + 1) ? x.y : none;
+      x.z = competes(4 * v + 2) ? x.z : none;
+      x.w = competes(4 * v + 3) ? x.w : none;
+    }
+    return x;
+  };
+  auto four = [&](int v) {
+    if constexpr (CACHED) return *reinterpret_cast<const float4*>(cache + 4 * v);
+    else return read_four(v);
+  };
+  float low = INFINITY, high = -INFINITY, off;
   {
     const float* norms = ws.b_norm + (static_cast<int64_t>(n) * p.Hkv + h) * ws.tiles;
     const float q_norm = ws.q_norm[blockIdx.x];
     uint32_t most = 0;  // norms by their bits
-    low = INFINITY;
-    high = -INFINITY;
     for (int i = threadIdx.x; i < (nb + 15) / 16; i += T) most = max(most, __float_as_uint(norms[i]));
-    float* to = reinterpret_cast<float*>(s_bits + 2 * ((p.max_blocks + 31) / 32));
-    const bool keep = nb <= cached;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < c1; i += T) {
-      const float x = sc[i];
-      if (keep) to[i] = x;
-      if (i >= c0) {
-        low = fminf(low, x);
-        high = fmaxf(high, x);
-      }
+#pragma unroll 2
+    for (int v = threadIdx.x; 4 * v < nb; v += T) {
+      const float4 x = read_four(v);
+      if constexpr (CACHED) *reinterpret_cast<float4*>(cache + 4 * v) = x;
+      low = fminf(fminf(low, fminf(x.x, x.y)), fminf(x.z, x.w));
+      high = fmaxf(fmaxf(high, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
     }
     uint32_t least = order_of(low), top = order_of(high);
-    if (keep) sc = to;
     most = __reduce_max_sync(FULL, most);
     least = __reduce_min_sync(FULL, least);
     top = __reduce_max_sync(FULL, top);
@@ -762,13 +783,18 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectBlocksParams p, c
     int* hist = s_hist[round & 1];
     const float range = high - low, per_bin = BINS / range;
     if (!(range < INFINITY && per_bin < INFINITY)) break;  // all alike, or past float32
-#pragma unroll 2
-    for (int i = threadIdx.x; i < c1; i += T) {
-      const float x = sc[i];
-      if (i >= c0 && x >= low && x <= high) {
+    auto count = [&](float x) {
+      if (x >= low && x <= high) {
         const int bin = static_cast<int>((x - low) * per_bin);
         atomicAdd(&hist[bin < BINS ? bin : BINS - 1], 1);
       }
+    };
+    for (int v = threadIdx.x; 4 * v < nb; v += T) {
+      const float4 x = four(v);
+      count(x.x);
+      count(x.y);
+      count(x.z);
+      count(x.w);
     }
     __syncthreads();
     // every warp finds the bin of the border: lane 0 holds the highest
@@ -798,30 +824,41 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectBlocksParams p, c
     low = low + bin * width - slack;
     high = low + width + 2.f * slack;
     int above_high = 0;
-#pragma unroll 2
-    for (int i = threadIdx.x; i - lane < nb; i += T) {
-      const bool competes = i >= c0 && i < c1;
-      const float x = competes ? sc[i] : 0.f;
-      const bool in = competes && x > high, here = competes && !in && x >= low;
-      if (here) {
-        const int k = atomicAdd(&s_open[round & 1], 1);
+    for (int v = threadIdx.x; 4 * (v - lane) < nb; v += T) {
+      const float4 x = 4 * v < nb ? four(v) : make_float4(none, none, none, none);
+      unsigned bits = (x.x > high ? 1u : 0u) | (x.y > high ? 2u : 0u) | (x.z > high ? 4u : 0u) | (x.w > high ? 8u : 0u);
+      const unsigned here =
+          ((x.x >= low ? 1u : 0u) | (x.y >= low ? 2u : 0u) | (x.z >= low ? 4u : 0u) | (x.w >= low ? 8u : 0u)) & ~bits;
+      for (unsigned todo = here; todo != 0; todo &= todo - 1) {
+        const int j = __ffs(todo) - 1, k = atomicAdd(&s_open[round & 1], 1);
         if (k < 32) {
-          s_at[k] = i;
-          s_score[k] = x;
+          s_at[k] = 4 * v + j;
+          s_score[k] = j == 0 ? x.x : j == 1 ? x.y : j == 2 ? x.z : x.w;
         }
       }
-      const unsigned ins = __ballot_sync(FULL, in), kept = __ballot_sync(FULL, !competes && i < nb);
-      above_high += __popc(ins);
-      if (lane == 0) s_bits[i >> 5] = ins | kept;
+      above_high += __popc(bits);
+      if (edge(v)) {  // the kept ones
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (4 * v + j < nb && !competes(4 * v + j)) bits |= 1u << j;
+      }
+      // eight lanes a word
+      bits <<= 4 * (lane & 7);
+      bits |= __shfl_xor_sync(FULL, bits, 1);
+      bits |= __shfl_xor_sync(FULL, bits, 2);
+      bits |= __shfl_xor_sync(FULL, bits, 4);
+      if ((lane & 7) == 0 && 4 * v < nb) s_bits[v >> 3] = bits;
     }
+    above_high = __reduce_add_sync(FULL, above_high);
     if (lane == 0 && above_high > 0) atomicAdd(&s_over[round & 1], above_high);
-    for (int i = threadIdx.x; i < BINS; i += T) s_hist[round & 1 ^ 1][i] = 0;  // for the round after this one
     __syncthreads();
     open = s_open[round & 1];
     over = s_over[round & 1];
     few = open <= 32;
     if (!few) {
       if (!(high - low < 0.5f * range)) break;  // the error's width: they may as well be alike
+      const int other = (round & 1) ^ 1;
+      for (int i = threadIdx.x; i < BINS; i += T) s_hist[other][i] = 0;
       __syncthreads();
       if (threadIdx.x == 0) s_open[round & 1] = s_over[round & 1] = 0;
     }
@@ -906,7 +943,7 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectBlocksParams p, c
       for (int shift = 24; shift >= 0; shift -= 8) {
         clear();
         for (int i = c0 + threadIdx.x; i < c1; i += T) {
-          const uint32_t u = order_of(sc[i]);
+          const uint32_t u = order_of(score(i));
           if (((u ^ border) & mask) == 0) atomicAdd(&hist[u >> shift & 255], 1);
         }
         digit(left);
@@ -916,14 +953,14 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectBlocksParams p, c
       }
     }
     const float at = from_order(border), most = known ? at + 2.f * off : INFINITY, least = known ? at - 2.f * off : -INFINITY;
-    auto undecided = [&](int i) { return want > 0 && i >= c0 && i < c1 && (!known || (sc[i] <= most && sc[i] >= least)); };
+    auto undecided = [&](int i) { return want > 0 && i >= c0 && i < c1 && (!known || (score(i) <= most && score(i) >= least)); };
     __syncthreads();
     if (threadIdx.x == 0) s_open[0] = s_over[0] = 0;
     __syncthreads();
     int ins = 0, opens = 0;
     for (int w = warp; w < words; w += NW) {
       const int i = 32 * w + lane;
-      const bool kept = i < nb && (i < c0 || i >= c1), in = known && want > 0 && i >= c0 && i < c1 && sc[i] > most;
+      const bool kept = i < nb && (i < c0 || i >= c1), in = known && want > 0 && i >= c0 && i < c1 && score(i) > most;
       opens += __popc(__ballot_sync(FULL, undecided(i)));
       const unsigned in_bits = __ballot_sync(FULL, in), kept_bits = __ballot_sync(FULL, kept);
       ins += __popc(in_bits);
@@ -980,31 +1017,29 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectBlocksParams p, c
   }
   __syncthreads();
 
-  // ---- in ascending order: every warp counts, and writes its words
+  // ---- in ascending order: every warp counts, each takes the words, a lane a word, of every NW-th group of 32
   int base = 0;
-  for (int w0 = 0; w0 < words; w0 += 32) {
-    const unsigned bits = w0 + lane < words ? s_bits[w0 + lane] : 0u;
+  for (int w0 = 0, group = 0; w0 < words; w0 += 32, ++group) {
+    unsigned bits = w0 + lane < words ? s_bits[w0 + lane] : 0u;
     int upto = __popc(bits);
-    const int own = upto;
+    int place = base - upto;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(FULL, upto, o);
       if (lane >= o) upto += x;
     }
-    for (int j = warp; j < 32; j += NW) {
-      const unsigned word = __shfl_sync(FULL, bits, j);
-      const int place = base + __shfl_sync(FULL, upto - own, j) + __popc(word & ((1u << lane) - 1));
-      if (word >> lane & 1 && place < K) out[place] = 32 * (w0 + j) + lane;
-    }
+    place += upto;
     base += __shfl_sync(FULL, upto, 31);
+    if (group % NW != warp) continue;
+    for (; bits != 0; bits &= bits - 1, ++place)
+      if (place < K) out[place] = 32 * (w0 + lane) + __ffs(bits) - 1;
   }
 }
 
-template <int D, int T>
+template <int T, bool CACHED>
 cudaError_t select(const SelectBlocksParams& p, const Scratch& ws, cudaStream_t stream) {
-  const int cached = p.max_blocks <= CACHED ? p.max_blocks : 0;
-  const int bits = (2 * ((p.max_blocks + 31) / 32) + cached) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(select_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, bits);
+  const int smem = (cache_at(p.max_blocks) + (CACHED ? (p.max_blocks + 3) / 4 * 4 : 0)) * 4;
+  const cudaError_t e = cudaFuncSetAttribute(select_kernel<T, CACHED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1012,11 +1047,11 @@ cudaError_t select(const SelectBlocksParams& p, const Scratch& ws, cudaStream_t 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.T) * p.Hkv));
   cfg.blockDim = dim3(T);
-  cfg.dynamicSmemBytes = bits;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, select_kernel<D, T>, p, ws, cached);
+  return cudaLaunchKernelEx(&cfg, select_kernel<T, CACHED>, p, ws);
 }
 
 template <int D>
@@ -1053,9 +1088,11 @@ cudaError_t launch(const SelectBlocksParams& p, Scratch& ws, cudaStream_t stream
   ws.eps = 1.f / (1 << 18) + static_cast<float>(p.Hq / p.Hkv) / (1 << 24) + static_cast<float>(D / 8 + 2) / (1 << 22);
   const cudaError_t e = p.max_q <= FEW ? score_few<D>(p, ws, stream) : score_many<D>(p, ws, stream);
   if (e != cudaSuccess) return e;
-  // few rows leave the latency of one to be shortened; many, the CTAs an SM holds
-  const bool many = static_cast<int64_t>(p.T) * p.Hkv >= FEW_ROWS;
-  return many || p.max_blocks <= NARROW ? select<D, 128>(p, ws, stream) : select<D, 512>(p, ws, stream);
+  // Of few long rows the latency of one is to be shortened.  Of many, instructions count, which are fewer the fewer warps
+  // do a row's common work: 4096 rows of 2048 blocks take 51 us with 128 threads, 55 with 64, which leave too few warps.
+  if (p.max_blocks > CACHED_BLOCKS) return select<512, false>(p, ws, stream);
+  const bool many = static_cast<int64_t>(p.T) * p.Hkv >= MANY_ROWS;
+  return many || p.max_blocks <= NARROW ? select<128, true>(p, ws, stream) : select<512, true>(p, ws, stream);
 }
 
 }  // namespace
