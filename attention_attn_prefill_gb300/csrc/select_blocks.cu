@@ -28,6 +28,12 @@ namespace attn {
 
 __device__ uint32_t g_select_blocks_status;
 
+#ifdef ATTN_TEST_DROP_COPY
+// Test-only builds (never the product library): the first CTA of score_many_kernel leaves out its first row tile.  The
+// waits for it run out after ATTN_WAIT_LIMIT_NS.
+__device__ int g_test_drop_copy_select;
+#endif
+
 namespace {
 
 using shares::mma_16816;
@@ -538,6 +544,9 @@ __global__ void __launch_bounds__(ManyCfg<D>::WARPS * 32, 1)
         if (lane == 0) mbar_arrive_expect_tx(&b_full[stage], 2 * C::PANELS * bytes);
         __syncwarp();
         const uint8_t* image = ws.images + (tile_place(s.first, n, rt, RT) * p.Hkv + h) * C::B_BYTES;
+#ifdef ATTN_TEST_DROP_COPY
+        if (blockIdx.x == 0 && done + i == 0 && g_test_drop_copy_select != 0) continue;
+#endif
         if (lane < 2 * C::PANELS)
           bulk_load(tiles + C::B_OFF + stage * C::B_BYTES + lane * C::B_PANEL, image + lane * C::B_PANEL, bytes, &b_full[stage]);
         __syncwarp();
@@ -1096,6 +1105,12 @@ cudaError_t launch(const SelectBlocksParams& p, Scratch& ws, cudaStream_t stream
 }
 
 }  // namespace
+
+#ifdef ATTN_TEST_DROP_COPY
+extern "C" int attn_test_drop_copy_select(int what) {
+  return static_cast<int>(cudaMemcpyToSymbol(g_test_drop_copy_select, &what, sizeof(int)));
+}
+#endif
 
 size_t select_blocks_workspace_bytes(int64_t T, int64_t N, int64_t max_q, int64_t Hkv, int d, int64_t max_blocks) {
   const int RT = d == 256 ? ManyCfg<256>::RT : ManyCfg<128>::RT;
