@@ -209,13 +209,14 @@ def select_blocks_workspace_bytes(num_tokens: int, num_seqs: int, max_seqlen_q: 
 
 def select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
                   num_selected: int, first: int = 1, last: int = 2, cu_seqlens_q: torch.Tensor | None = None,
-                  max_seqlen_q: int = 1, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                  max_seqlen_q: int | None = None, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                   stream=None) -> torch.Tensor:
     """Blocks [T,Hkv,num_selected] int32 that each row of q [T,Hq,d] bf16 and KV head is to attend to, ascending, -1
     behind: the first `first` and last `last` blocks that the row sees, and those whose key bounds
     [num_blocks,Hkv,2,d] allow the highest scores; all where there are no more than num_selected.
 
-    cu_seqlens_q as for decode_blocks_f8, with at most max_seqlen_q rows a sequence."""
+    cu_seqlens_q as for decode_blocks_f8, with at most max_seqlen_q rows a sequence (without it any number: a bound of
+    up to four rows takes a faster way)."""
     dev, N = q.get_device(), seq_lens.numel()
     T, Hq, d = q.shape
     if dev < 0 or bounds.dtype is not _BF16 or bounds.get_device() != dev or not bounds.is_contiguous():
@@ -225,6 +226,8 @@ def select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tens
     num_blocks, Hkv = bounds.shape[:2]
     _check_tables(dev, block_table, seq_lens, N)
     cu = _check_rows(dev, q, cu_seqlens_q, N)
+    if max_seqlen_q is None:
+        max_seqlen_q = 1 if cu_seqlens_q is None else max(1, T)
     if out is None:
         out = _empty_on((T, Hkv, num_selected), _I32, dev, stream)
     elif (out.shape != (T, Hkv, num_selected) or out.dtype is not _I32 or out.get_device() != dev
