@@ -413,6 +413,8 @@ __global__ void __launch_bounds__(SUM_ROWS / 2 * 32) sum_heads_kernel(const Sele
   using C = ManyCfg<D>;
   const int rt = blockIdx.x % row_tiles, nh = blockIdx.x / row_tiles, n = nh / p.Hkv, h = nh % p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.Hq / p.Hkv;
+  // score_many_kernel gathers bounds meanwhile, and waits before it takes the images
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Span s = span_of(p, n, rt == 0 && h == 0 && threadIdx.x == 0);
 #pragma unroll 1
   for (int e = 0; e < 2; ++e) {
@@ -471,12 +473,11 @@ __global__ void __launch_bounds__(ManyCfg<D>::WARPS * 32, 1)
   const int warp = __shfl_sync(FULL, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int chunk = blockIdx.x % chunks, nh = blockIdx.x / chunks, n = nh / p.Hkv, h = nh % p.Hkv;
   const Span s = span_of(p, n, false);
-  const int rows = s.end - s.first;
-  if (rows <= 0) return;
-  const int nb = blocks_seen(s, s.end - 1);
-  if (nb <= p.K || chunk * 128 >= nb) return;  // every block is chosen, or none is this CTA's
-  if ((smem_u32(tiles) & 1023u) != 0) {         // swizzled tiles need 1 KB alignment
-    if (threadIdx.x == 0) set_error(&g_select_blocks_status, kDevMisaligned);
+  const int rows = s.end - s.first, nb = rows > 0 ? blocks_seen(s, s.end - 1) : 0;
+  const bool misaligned = (smem_u32(tiles) & 1023u) != 0;  // swizzled tiles need 1 KB alignment
+  if (misaligned && threadIdx.x == 0) set_error(&g_select_blocks_status, kDevMisaligned);
+  if (nb <= p.K || chunk * 128 >= nb || misaligned) {  // every block is chosen, or none is this CTA's
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // no CTA, and so not this kernel, ends before the one ahead of it
     return;
   }
   if (threadIdx.x == 0) {
@@ -527,6 +528,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::WARPS * 32, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
     fence_proxy_async_smem();
     __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the images are there
     // rows see more blocks the later they are: the first row tile with something to score here
     const int least = tile * 128 > p.K ? tile * 128 : p.K;
     int first = 0;
@@ -662,7 +664,7 @@ __host__ __device__ constexpr int cache_at(int max_blocks) { return (2 * ((max_b
 
 // T threads a row and KV head.  CACHED: shared memory holds its scores, else they are read again and again.
 template <int T, bool CACHED>
-__global__ void __launch_bounds__(T) select_kernel(const SelectBlocksParams p, const Scratch ws) {
+__global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const SelectBlocksParams p, const Scratch ws) {
   constexpr int NW = T / 32;
   extern __shared__ __align__(16) uint32_t s_bits[];  // [words] chosen blocks, [words] ties; then the scores
   __shared__ __align__(16) int s_hist[2][BINS];
@@ -769,19 +771,30 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectBlocksParams p, c
       s_q[D + c] = pos;
     }
   };
-  auto exact = [&](int i) {
+  auto load_bounds = [&](int i, uint32_t (&b)[8]) {  // words 32 k + lane of block i's
     int id = p.block_table[static_cast<int64_t>(n) * p.max_blocks + i];
     if (id < 0 || id >= p.num_blocks) id = 0;
-    const uint32_t* b = reinterpret_cast<const uint32_t*>(p.bounds + (static_cast<int64_t>(id) * p.Hkv + h) * 2 * D);
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(p.bounds + (static_cast<int64_t>(id) * p.Hkv + h) * 2 * D) + lane;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) b[k] = 32 * k < D ? from[32 * k] : 0u;
+  };
+  auto product = [&](const uint32_t (&b)[8]) {
     double sum = 0.0;
-#pragma unroll 4
-    for (int c = lane; c < D; c += 32) {
-      const float2 x = pair_of(b[c]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (32 * k >= D) break;
+      const float2 x = pair_of(b[k]);
+      const int c = 32 * k + lane;
       sum = fma(s_q[2 * c], static_cast<double>(x.x), fma(s_q[2 * c + 1], static_cast<double>(x.y), sum));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
     return order_of(sum);
+  };
+  auto exact = [&](int i) {
+    uint32_t b[8];
+    load_bounds(i, b);
+    return product(b);
   };
 
   // ---- Narrow the window [low, high] about the border, a bin of BINS at a time, until 32 blocks at most are in it.
@@ -902,15 +915,18 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectBlocksParams p, c
       if (all) among = 0;
     }
     __syncthreads();
-    if (s_among != 0) {  // by the exact scores, a warp a block
+    if (s_among != 0) {  // by the exact scores, a warp a block; the first one's bounds come while the heads are summed
+      unsigned todo = s_among;
+      for (int k = 0; k < warp && todo != 0; ++k) todo &= todo - 1;
+      uint32_t b[8];
+      if (todo != 0) load_bounds(s_at[__ffs(todo) - 1], b);
       sum_heads(threadIdx.x, T);
       __syncthreads();
-      unsigned todo = s_among;
-      for (int k = 0; todo != 0; todo &= todo - 1, ++k) {
-        if (k % NW != warp) continue;
+      for (bool first = true; todo != 0; first = false) {
         const int j = __ffs(todo) - 1;
-        const unsigned long long key = exact(s_at[j]);
+        const unsigned long long key = first ? product(b) : exact(s_at[j]);
         if (lane == 0) s_key[j] = key;
+        for (int k = 0; k < NW && todo != 0; ++k) todo &= todo - 1;
       }
       __syncthreads();
     }
@@ -1045,22 +1061,29 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectBlocksParams p, c
   }
 }
 
+// A launch as a programmatic dependent of the kernel before it
+template <class... Params, class... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), unsigned grid, unsigned threads, int smem, cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int T, bool CACHED>
 cudaError_t select(const SelectBlocksParams& p, const Scratch& ws, cudaStream_t stream) {
   const int smem = (cache_at(p.max_blocks) + (CACHED ? (p.max_blocks + 3) / 4 * 4 : 0)) * 4;
   const cudaError_t e = cudaFuncSetAttribute(select_kernel<T, CACHED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.T) * p.Hkv));
-  cfg.blockDim = dim3(T);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, select_kernel<T, CACHED>, p, ws);
+  return launch_behind(select_kernel<T, CACHED>, static_cast<unsigned>(static_cast<int64_t>(p.T) * p.Hkv), T, smem, stream, p,
+                       ws);
 }
 
 template <int D>
@@ -1087,8 +1110,8 @@ cudaError_t score_many(const SelectBlocksParams& p, const Scratch& ws, cudaStrea
   if (e != cudaSuccess) return e;
   const int64_t all = (p.max_blocks + 127) / 128, most = (SCORE_CTAS + pairs - 1) / pairs;
   const int chunks = static_cast<int>(all < most ? all : most);
-  score_many_kernel<D><<<static_cast<unsigned>(pairs * chunks), C::WARPS * 32, C::SMEM, stream>>>(p, ws, chunks);
-  return cudaGetLastError();
+  return launch_behind(score_many_kernel<D>, static_cast<unsigned>(pairs * chunks), C::WARPS * 32, C::SMEM, stream, p, ws,
+                       chunks);
 }
 
 template <int D>
@@ -1099,9 +1122,9 @@ cudaError_t launch(const SelectBlocksParams& p, Scratch& ws, cudaStream_t stream
   if (e != cudaSuccess) return e;
   // Of few long rows the latency of one is to be shortened.  Of many, instructions count, which are fewer the fewer warps
   // do a row's common work: 4096 rows of 2048 blocks take 51 us with 128 threads, 55 with 64, which leave too few warps.
-  if (p.max_blocks > CACHED_BLOCKS) return select<512, false>(p, ws, stream);
+  if (p.max_blocks > CACHED_BLOCKS) return select<1024, false>(p, ws, stream);
   const bool many = static_cast<int64_t>(p.T) * p.Hkv >= MANY_ROWS;
-  return many || p.max_blocks <= NARROW ? select<128, true>(p, ws, stream) : select<512, true>(p, ws, stream);
+  return many || p.max_blocks <= NARROW ? select<128, true>(p, ws, stream) : select<1024, true>(p, ws, stream);
 }
 
 }  // namespace
