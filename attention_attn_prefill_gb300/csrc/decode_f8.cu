@@ -13,8 +13,8 @@
 // of a KV head.  With P = 2 a step takes two pages and the columns hold up to four heads of both, so that one round
 // of exponentials and roundings serves both; a page's product with V has zeros in the other page's columns.
 //
-// Work: the (sequence, unit, step) list is cut into contiguous shares of equal weight, one a CTA (decode_shares.cuh);
-// the CTA's computing warps deal its steps among themselves.  One more warp requests the records (one bulk copy each)
+// Work: the (sequence, unit, step) list is cut into contiguous shares of equal weight, one a CTA (decode_shares.cuh), or
+// where they are short a CTA takes each row and unit whole; the CTA's computing warps deal its steps among themselves.  One more warp requests the records (one bulk copy each)
 // into the warps' rings, and merges the warps' states of a sequence when all have left it, so that the computing
 // warps never wait for each other.  Where a share's end cuts a sequence, the CTA leaves a partial, which a second
 // kernel, launched as a programmatic dependent, merges.  With listed blocks a query token is what a sequence is
@@ -53,13 +53,20 @@ constexpr float W_LIMIT = 16384.f;     // a weight p 2^b above 2^14 moves the ou
 constexpr float W_ROOM = 8.f;          // ... to where the largest is 2^8: fp16 keeps 11 bits down to 2^-14
 constexpr uint32_t Q_TOP = 14;         // a head's largest channel is put at 2^14 .. 2^15
 
+// How the list is dealt out.  SHARES: equal shares of it, one a CTA, and a second kernel that merges what a share's end
+// cuts.  WHOLE: a CTA takes all steps of one row and unit.  ALONE: so too, with as many warps as an SM holds.
+enum Deal { SHARES, WHOLE, ALONE };
+
 // P: pages a warp takes at a step; ROWS / P query heads.
-template <int D, int P>
+template <int D, int P, int DEAL>
 struct Cfg {
-  // Warps that compute (one more loads), steps in flight a warp, and CTAs an SM: what shared memory holds
-  static constexpr int NW = D == 256 ? 4 : D == 128 ? (P == 2 ? 5 : 7) : 5;
+  // Warps that compute (one more loads), steps in flight a warp, and CTAs an SM: what shared memory holds.  Measured on 64
+  // sequences of 512 to 8192, 32/8 heads, d = 128, warps x steps x CTAs: 5 x 2 x 2 98.8 us, 3 x 2 x 3 100.4, 4 x 3 x 2
+  // 103.9, 11 x 2 x 1 102.7 (more in flight is no faster), one page a step 7 x 2 x 2 100.6.
+  static constexpr int NW = DEAL == ALONE ? (D == 256 ? 8 : D == 128 && P == 2 ? 11 : 13)
+                                          : (D == 256 ? 4 : D == 128 && P == 1 ? 7 : 5);
   static constexpr int DEPTH = D == 64 ? 3 : 2;
-  static constexpr int CTAS = D == 64 ? 3 : 2;
+  static constexpr int CTAS = DEAL == ALONE ? 1 : D == 64 ? 3 : 2;
   static constexpr int THREADS = (NW + 1) * 32;
   static constexpr int TILE = ROWS / P;  // query heads a tile
   static constexpr int SLOTS = NW * DEPTH;
@@ -129,15 +136,15 @@ struct At : Cursor<P> {
   }
 };
 
-template <int D, int P, bool LISTED>
-__global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
+template <int D, int P, bool LISTED, int DEAL>
+__global__ void __launch_bounds__(Cfg<D, P, DEAL>::THREADS, Cfg<D, P, DEAL>::CTAS)
     decode_f8_kernel(const DecodeF8Params p, const Geometry geo) {
-  using C = Cfg<D, P>;
+  using C = Cfg<D, P, DEAL>;
   using R = Record<D>;
   constexpr int NW = C::NW, THREADS = C::THREADS, TILE = C::TILE, SLOTS = C::SLOTS;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_weight[NW + 1], s_steps[NW + 1], s_end[2], s_at;
-  __shared__ longlong2 s_before[LISTED ? 1 : THREADS];  // weight and steps of the warp's sequences before a thread's
+  __shared__ longlong2 s_before[LISTED || DEAL != SHARES ? 1 : THREADS];  // weight and steps of the warp's sequences before a thread's
   __shared__ int3 s_start;
   __shared__ int s_valid[SLOTS][P];  // listed blocks: tokens of each page of a slot that the query sees
   float* merge = reinterpret_cast<float*>(smem + C::MERGE_OFF);
@@ -162,12 +169,31 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
   // leaving its result cost.  Short lists make fewer shares than CTAs: of one step, they would only be more partials to
   // merge.  Share b is the weight from b * per on.
   const int b = blockIdx.x;
-  long long W, per;
+  long long W = 0, per = 1;
   auto cut_list = [&](long long steps) {
     const long long most = steps / 2, shares = most >= geo.grid ? geo.grid : most < 1 ? 1 : most;
     per = quotient(W + shares - 1, shares);
   };
-  if constexpr (LISTED) {
+  auto check_lens = [&]() {
+    for (int n = threadIdx.x; n < p.N; n += THREADS) {
+      const int L = p.seq_lens[n];
+      if (L < 0 || L > p.max_blocks * PAGE) set_error(&g_decode_f8_status, kDevBadSplit);
+      if (p.cu != nullptr) {
+        const int c0 = p.cu[n], c1 = p.cu[n + 1];
+        if (c0 < 0 || c1 < c0 || c1 > p.T) set_error(&g_decode_f8_status, kDevBadSeqlens);
+      }
+    }
+  };
+  if constexpr (DEAL != SHARES) {
+    if (b == 0) check_lens();
+    if (threadIdx.x == 0) {
+      const int row = b / units;
+      s_start = make_int3(row, b - row * units, 0);
+      s_at = 0;
+      s_end[0] = 0;
+      s_end[1] = LISTED ? (p.K + P - 1) / P : steps_of<P>(p.seq_lens, row, p.max_blocks);
+    }
+  } else if constexpr (LISTED) {
     const int S = (p.K + P - 1) / P;
     const long long pairs = static_cast<long long>(rows) * units;
     W = pairs * (S + SEGMENT);
@@ -183,16 +209,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
         s_at = pair * (S + SEGMENT);
       }
     }
-    if (b == 0) {
-      for (int n = threadIdx.x; n < p.N; n += THREADS) {
-        const int L = p.seq_lens[n];
-        if (L < 0 || L > p.max_blocks * PAGE) set_error(&g_decode_f8_status, kDevBadSplit);
-        if (p.cu != nullptr) {
-          const int c0 = p.cu[n], c1 = p.cu[n + 1];
-          if (c0 < 0 || c1 < c0 || c1 > p.T) set_error(&g_decode_f8_status, kDevBadSeqlens);
-        }
-      }
-    }
+    if (b == 0) check_lens();
   } else {
     // ---- total steps, and the sequence that holds this share's first one
     const int N = p.N;
@@ -285,11 +302,19 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
   }
   __syncthreads();
   // every CTA of this grid is resident: the combine's CTAs may queue up behind them
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (DEAL == SHARES) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Workspace ws = carve<D>(p.workspace, geo.grid);
   const int count = static_cast<int>(s_end[1] - s_end[0]);  // steps of this share
   if (count <= 0) {
-    if (threadIdx.x == 0 && !geo.by_unit) ws.desc[b] = make_int4(0, 0, -1, 0);
+    if constexpr (DEAL != SHARES) {  // an empty sequence
+      const int kvh = s_start.y / geo.tiles, h0 = s_start.y % geo.tiles * TILE, heads = min(TILE, G - h0);
+      const int64_t row = static_cast<int64_t>(s_start.x) * p.Hq + kvh * G + h0;
+      for (int i = threadIdx.x; i < heads * (D / 8); i += THREADS)
+        reinterpret_cast<uint4*>(p.o + row * D)[i] = make_uint4(0, 0, 0, 0);
+      if (p.lse != nullptr && threadIdx.x < heads) p.lse[row + threadIdx.x] = -INFINITY;
+    } else if (threadIdx.x == 0 && !geo.by_unit) {
+      ws.desc[b] = make_int4(0, 0, -1, 0);
+    }
     return;
   }
 
@@ -408,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
         const bool starts = seg.step == 0, ends = seg.step + seg_steps == seg.ns;
         const int kvh = seg.u / geo.tiles, h0 = seg.u % geo.tiles * TILE;
         const int heads = G - h0 < TILE ? G - h0 : TILE;
-        const int64_t part = 2 * b + (starts ? 1 : 0);
+        const int64_t part = 2 * static_cast<int64_t>(b) + (starts ? 1 : 0);
         // a row of no sequence has no result
         const bool lives = !LISTED || p.cu == nullptr || row_info(p, seg.n).n >= 0;
         // four at a time: one alone would wait for its loads (d = 256, 8 heads: 9700 cycles one by one)
@@ -441,7 +466,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
           for (int k = 0; k < AT_ONCE; ++k) {
             const int w = w0 + 32 * k, r = w / (D / 4), x = w % (D / 4) * 4;
             if (w >= heads * (D / 4)) break;
-            if (starts && ends) {
+            if (DEAL != SHARES || (starts && ends)) {
               if (lives) {
                 const int64_t row = static_cast<int64_t>(seg.n) * p.Hq + kvh * G + h0 + r;
                 *reinterpret_cast<uint2*>(p.o + row * D + x) = make_uint2(pack_bf16x2(O[k].x, O[k].y), pack_bf16x2(O[k].z, O[k].w));
@@ -462,7 +487,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
           // the share that holds the last step
           cut = make_int4(seg.n, seg.u, b, static_cast<int>(quotient(at + SEGMENT + seg.ns - 1, per)));
         }
-        if (geo.by_unit && starts && lane == 0)
+        if (DEAL == SHARES && geo.by_unit && starts && lane == 0)
           ws.desc[static_cast<int64_t>(seg.n) * units + seg.u] = ends || !lives ? make_int4(0, 0, -1, 0) : cut;
         at += SEGMENT + seg.ns;
         seg_i += seg_steps;
@@ -476,7 +501,7 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
       }
     }
     if (lane == 0) {
-      if (!geo.by_unit) ws.desc[b] = cut;
+      if (DEAL == SHARES && !geo.by_unit) ws.desc[b] = cut;
       if (!ok) set_error(&g_decode_f8_status, kDevWaitTimeout);
     }
     // Copies in flight must land before the CTA's shared memory is given back: the newest of each slot.
@@ -747,16 +772,26 @@ __global__ void __launch_bounds__(Cfg<D, P>::THREADS, Cfg<D, P>::CTAS)
 // CTAs of the grid: every SM filled
 template <int D>
 int grid_of_device() {
-  static_assert(Cfg<D, 1>::CTAS == 2 || D == 64, "one size of workspace for a head dim");
+  static_assert(Cfg<D, 1, SHARES>::CTAS == Cfg<D, D == 256 ? 1 : 2, SHARES>::CTAS, "one size of workspace for a head dim");
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return sms * Cfg<D, 1>::CTAS;
+  return sms * Cfg<D, 1, SHARES>::CTAS;
+}
+
+template <int D, int P, bool LISTED, int DEAL>
+cudaError_t start(const DecodeF8Params& p, const Geometry& geo, int64_t grid, cudaStream_t stream) {
+  using C = Cfg<D, P, DEAL>;
+  auto kern = decode_f8_kernel<D, P, LISTED, DEAL>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(grid), C::THREADS, C::ALLOC, stream>>>(p, geo);
+  return cudaGetLastError();
 }
 
 template <int D, int P, bool LISTED>
 cudaError_t launch(const DecodeF8Params& p, cudaStream_t stream) {
-  using C = Cfg<D, P>;
+  using C = Cfg<D, P, SHARES>;
   Geometry geo;
   geo.grid = grid_of_device<D>();
   if (geo.grid <= 0) return cudaErrorInvalidDevice;
@@ -764,12 +799,23 @@ cudaError_t launch(const DecodeF8Params& p, cudaStream_t stream) {
   geo.tile = C::TILE;
   geo.tiles = (p.Hq / p.Hkv + C::TILE - 1) / C::TILE;
   geo.units = p.Hkv * geo.tiles;
-  geo.by_unit = static_cast<int64_t>(rows) * geo.units * 8 <= geo.grid;
-  auto kern = decode_f8_kernel<D, P, LISTED>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
+  const int64_t pairs = static_cast<int64_t>(rows) * geo.units;
+  geo.by_unit = pairs * 8 <= geo.grid;
+  // What the host knows of the lengths is the table's width, or the list's: the most steps that a row and unit can have.
+  // Up to that the shorter ways are no slower, one launch instead of two, and no scan of the lengths.  Measured, us, 32/8
+  // heads, d = 128, equal lengths (SHARES, WHOLE, ALONE):
+  //   8 pairs:   16 tokens 9.5 4.9 5.7, 500 8.9 7.6 7.3, 1000 9.2 10.4 9.3, 2000 9.9 15.7 13.1
+  //   128 pairs: 16 tokens 10.8 5.5 6.4, 1000 14.1 10.7 9.8, 2000 20.4 20.0 16.5, 4000 30.6 34.7 27.1
+  //   512 pairs: 16 tokens 11.2 9.8, 1000 32.0 29.9, 2000 51.8 48.4 (of 100 to 2000: 33.4 34.4); 2048 pairs: 24.4 31.6
+  //   64 listed blocks: 8 pairs 8.5 12.0 10.2, 512 pairs 34.6 34.0.  d = 64, 512 pairs, 1000 tokens: 21.1 22.2
+  const int64_t steps = ((LISTED ? p.K : p.max_blocks) + P - 1) / P;
+  const bool whole = pairs <= 2 * geo.grid && steps <= (D == 64 ? 16 : 64);
+  if (whole && steps <= 8) return start<D, P, LISTED, WHOLE>(p, geo, pairs, stream);
+  if (pairs <= geo.grid / C::CTAS && steps <= (LISTED ? 24 : 33) + pairs / 2)
+    return start<D, P, LISTED, ALONE>(p, geo, pairs, stream);
+  if (whole && pairs > geo.grid / C::CTAS) return start<D, P, LISTED, WHOLE>(p, geo, pairs, stream);
+  const cudaError_t e = start<D, P, LISTED, SHARES>(p, geo, geo.grid, stream);
   if (e != cudaSuccess) return e;
-  kern<<<geo.grid, C::THREADS, C::ALLOC, stream>>>(p, geo);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_combine<D, C::TILE>(
       MergeParams{p.workspace, p.o, p.lse, LISTED ? nullptr : p.seq_lens, rows, p.Hq, p.Hkv, p.max_blocks}, geo, stream);
 }
