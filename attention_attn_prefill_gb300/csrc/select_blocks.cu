@@ -662,40 +662,46 @@ __device__ __forceinline__ unsigned long long order_of(double x) {
 // Words of shared memory before the scores: two bits a block, in whole 16 bytes
 __host__ __device__ constexpr int cache_at(int max_blocks) { return (2 * ((max_blocks + 31) / 32) + 3) / 4 * 4; }
 
-// T threads a row and KV head.  CACHED: shared memory holds its scores, else they are read again and again.
+// Every block that a row sees, and -1 behind
+template <int T>
+__device__ __forceinline__ void choose_all(const SelectBlocksParams& p, int64_t at, int nb) {
+  for (int i = threadIdx.x; i < p.K; i += T) p.blocks[at * p.K + i] = i < nb ? i : -1;
+}
+
+struct PickShared {
+  __align__(16) int hist[2][BINS];
+  double q[2 * 256];
+  unsigned long long key[32];
+  uint4 red[32];
+  float score[32];
+  int at[32], open[2], over[2], digit, above;
+  unsigned among;
+};
+
+// What picking needs of a row and KV head
+struct Row {
+  int r, h, n, nb;     // row, KV head, sequence; the blocks that it sees, more than it may choose
+  const float* scores;  // in global memory, rows of whole multiples of eight floats; null: in shared memory already
+  float q_norm, b_norm;  // b_norm: this thread's share of a maximum
+};
+
+// Picks the blocks of a row and KV head, by a CTA of T threads.  CACHED: shared memory holds its scores, else they are read
+// again and again.  s_bits: [words] chosen blocks, [words] ties; the scores from word cache_at on.
 template <int T, bool CACHED>
-__global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const SelectBlocksParams p, const Scratch ws) {
+__device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row, float eps, PickShared& sh, uint32_t* s_bits) {
   constexpr int NW = T / 32;
-  extern __shared__ __align__(16) uint32_t s_bits[];  // [words] chosen blocks, [words] ties; then the scores
-  __shared__ __align__(16) int s_hist[2][BINS];
-  __shared__ double s_q[2 * 256];
-  const int D = p.d;
-  __shared__ float s_score[32];
-  __shared__ int s_at[32], s_open[2], s_over[2], s_digit, s_above;
-  __shared__ unsigned s_among;
-  __shared__ unsigned long long s_key[32];
-  __shared__ uint4 s_red[NW];
+  const int D = p.d, nb = row.nb, K = p.K, r = row.r, h = row.h, n = row.n;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
-  const int n = p.cu == nullptr ? r : sequence_of(p, r);
-  const Span s = span_of(p, n, false);
-  for (int i = threadIdx.x; i < BINS / 4; i += T) reinterpret_cast<int4*>(s_hist[0])[i] = make_int4(0, 0, 0, 0);
-  if (threadIdx.x < 2) s_open[threadIdx.x] = s_over[threadIdx.x] = 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores are there
-  if (r < s.first || r >= s.end) return;  // of no sequence: left as it was
-  const int nb = blocks_seen(s, r), K = p.K;
-  int32_t* out = p.blocks + static_cast<int64_t>(blockIdx.x) * K;
-  if (nb <= K) {
-    for (int i = threadIdx.x; i < K; i += T) out[i] = i < nb ? i : -1;
-    return;
-  }
+  int32_t* out = p.blocks + (static_cast<int64_t>(r) * p.Hkv + h) * K;
   const int c0 = p.first, c1 = nb - p.last;  // the blocks that compete
   const int want = K - p.first - p.last;     // for so many places: fewer than they are
   const int words = (nb + 31) / 32;
   uint32_t* ties = s_bits + words;
+  for (int i = threadIdx.x; i < BINS / 4; i += T) reinterpret_cast<int4*>(sh.hist[0])[i] = make_int4(0, 0, 0, 0);
+  if (threadIdx.x < 2) sh.open[threadIdx.x] = sh.over[threadIdx.x] = 0;
 
   // ---- how far a score may be off, and the scores' range
-  const float* sc = ws.scores + static_cast<int64_t>(blockIdx.x) * ws.stride;
+  const float* sc = row.scores;
   float* cache = reinterpret_cast<float*>(s_bits + cache_at(p.max_blocks));
   const float none = __uint_as_float(0x7fffffffu);  // a NaN: neither above, below nor within a window
   auto competes = [&](int i) { return i >= c0 && i < c1; };
@@ -703,10 +709,10 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
     if constexpr (CACHED) return cache[i];
     else return competes(i) ? sc[i] : none;
   };
-  // four scores at a time, of blocks 4 v ..: rows are whole multiples of eight floats apart
+  // four scores at a time, of blocks 4 v ..
   auto edge = [&](int v) { return 4 * v < c0 || 4 * v + 4 > c1; };
   auto read_four = [&](int v) {
-    float4 x = *reinterpret_cast<const float4*>(sc + 4 * v);
+    float4 x = *reinterpret_cast<const float4*>((CACHED && sc == nullptr ? cache : sc) + 4 * v);
     if (edge(v)) {
       x.x = competes(4 * v) ? x.x : none;
       x.y = competes(4 * v + 1) ? x.y : none;
@@ -721,10 +727,6 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
   };
   float low = INFINITY, high = -INFINITY, off;
   {
-    const float* norms = ws.b_norm + (static_cast<int64_t>(n) * p.Hkv + h) * ws.tiles;
-    const float q_norm = ws.q_norm[blockIdx.x];
-    uint32_t most = 0;  // norms by their bits
-    for (int i = threadIdx.x; i < (nb + 15) / 16; i += T) most = max(most, __float_as_uint(norms[i]));
 #pragma unroll 2
     for (int v = threadIdx.x; 4 * v < nb; v += T) {
       const float4 x = read_four(v);
@@ -732,20 +734,18 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
       low = fminf(fminf(low, fminf(x.x, x.y)), fminf(x.z, x.w));
       high = fmaxf(fmaxf(high, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
     }
-    uint32_t least = order_of(low), top = order_of(high);
-    most = __reduce_max_sync(FULL, most);
-    least = __reduce_min_sync(FULL, least);
-    top = __reduce_max_sync(FULL, top);
-    if (lane == 0) s_red[warp] = make_uint4(most, least, top, 0);
+    uint32_t most = __reduce_max_sync(FULL, __float_as_uint(row.b_norm));  // norms by their bits
+    uint32_t least = __reduce_min_sync(FULL, order_of(low)), top = __reduce_max_sync(FULL, order_of(high));
+    if (lane == 0) sh.red[warp] = make_uint4(most, least, top, 0);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
-      const uint4 x = s_red[i];
+      const uint4 x = sh.red[i];
       most = max(most, x.x);
       least = min(least, x.y);
       top = max(top, x.z);
     }
-    off = ws.eps * q_norm * __uint_as_float(most);
+    off = eps * row.q_norm * __uint_as_float(most);
     low = from_order(least);
     high = from_order(top);
   }
@@ -767,8 +767,8 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
           pos += x[e] < 0.f ? 0.f : x[e];
         }
       }
-      s_q[c] = neg;
-      s_q[D + c] = pos;
+      sh.q[c] = neg;
+      sh.q[D + c] = pos;
     }
   };
   auto load_bounds = [&](int i, uint32_t (&b)[8]) {  // words 32 k + lane of block i's
@@ -785,7 +785,7 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
       if (32 * k >= D) break;
       const float2 x = pair_of(b[k]);
       const int c = 32 * k + lane;
-      sum = fma(s_q[2 * c], static_cast<double>(x.x), fma(s_q[2 * c + 1], static_cast<double>(x.y), sum));
+      sum = fma(sh.q[2 * c], static_cast<double>(x.x), fma(sh.q[2 * c + 1], static_cast<double>(x.y), sum));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
   bool few = false;
   int open = 0, over = 0;  // in the window; above it
   for (int round = 0; known && want > 0 && !few; ++round) {
-    int* hist = s_hist[round & 1];
+    int* hist = sh.hist[round & 1];
     const float range = high - low, per_bin = BINS / range;
     if (!(range < INFINITY && per_bin < INFINITY)) break;  // all alike, or past float32
     auto count = [&](float x) {
@@ -852,10 +852,10 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
       const unsigned here =
           ((x.x >= low ? 1u : 0u) | (x.y >= low ? 2u : 0u) | (x.z >= low ? 4u : 0u) | (x.w >= low ? 8u : 0u)) & ~bits;
       for (unsigned todo = here; todo != 0; todo &= todo - 1) {
-        const int j = __ffs(todo) - 1, k = atomicAdd(&s_open[round & 1], 1);
+        const int j = __ffs(todo) - 1, k = atomicAdd(&sh.open[round & 1], 1);
         if (k < 32) {
-          s_at[k] = 4 * v + j;
-          s_score[k] = j == 0 ? x.x : j == 1 ? x.y : j == 2 ? x.z : x.w;
+          sh.at[k] = 4 * v + j;
+          sh.score[k] = j == 0 ? x.x : j == 1 ? x.y : j == 2 ? x.z : x.w;
         }
       }
       above_high += __popc(bits);
@@ -872,17 +872,17 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
       if ((lane & 7) == 0 && 4 * v < nb) s_bits[v >> 3] = bits;
     }
     above_high = __reduce_add_sync(FULL, above_high);
-    if (lane == 0 && above_high > 0) atomicAdd(&s_over[round & 1], above_high);
+    if (lane == 0 && above_high > 0) atomicAdd(&sh.over[round & 1], above_high);
     __syncthreads();
-    open = s_open[round & 1];
-    over = s_over[round & 1];
+    open = sh.open[round & 1];
+    over = sh.over[round & 1];
     few = open <= 32;
     if (!few) {
       if (!(high - low < 0.5f * range)) break;  // the error's width: they may as well be alike
       const int other = (round & 1) ^ 1;
-      for (int i = threadIdx.x; i < BINS; i += T) s_hist[other][i] = 0;
+      for (int i = threadIdx.x; i < BINS; i += T) sh.hist[other][i] = 0;
       __syncthreads();
-      if (threadIdx.x == 0) s_open[round & 1] = s_over[round & 1] = 0;
+      if (threadIdx.x == 0) sh.open[round & 1] = sh.over[round & 1] = 0;
     }
   }
 
@@ -894,8 +894,8 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
     unsigned among = 0;
     if (warp == 0) {
       const bool mine = lane < open;
-      const float x = mine ? s_score[lane] : -INFINITY;
-      if (mine) i = s_at[lane];
+      const float x = mine ? sh.score[lane] : -INFINITY;
+      if (mine) i = sh.at[lane];
       int rank = 0;
       for (int j = 0; j < open; ++j) {
         const float y = __shfl_sync(FULL, x, j);
@@ -908,30 +908,30 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
       among = __ballot_sync(FULL, close);
       rest = places - __popc(__ballot_sync(FULL, sure));
       const bool all = __popc(among) == rest;
-      if (lane == 0) s_among = all || off == 0.f ? 0u : among;
+      if (lane == 0) sh.among = all || off == 0.f ? 0u : among;
       if (all && (sure || close)) choose(i);
       close = close && !all;
       sure = sure && !all;
       if (all) among = 0;
     }
     __syncthreads();
-    if (s_among != 0) {  // by the exact scores, a warp a block; the first one's bounds come while the heads are summed
-      unsigned todo = s_among;
+    if (sh.among != 0) {  // by the exact scores, a warp a block; the first one's bounds come while the heads are summed
+      unsigned todo = sh.among;
       for (int k = 0; k < warp && todo != 0; ++k) todo &= todo - 1;
       uint32_t b[8];
-      if (todo != 0) load_bounds(s_at[__ffs(todo) - 1], b);
+      if (todo != 0) load_bounds(sh.at[__ffs(todo) - 1], b);
       sum_heads(threadIdx.x, T);
       __syncthreads();
       for (bool first = true; todo != 0; first = false) {
         const int j = __ffs(todo) - 1;
-        const unsigned long long key = first ? product(b) : exact(s_at[j]);
-        if (lane == 0) s_key[j] = key;
+        const unsigned long long key = first ? product(b) : exact(sh.at[j]);
+        if (lane == 0) sh.key[j] = key;
         for (int k = 0; k < NW && todo != 0; ++k) todo &= todo - 1;
       }
       __syncthreads();
     }
     if (among != 0) {
-      const unsigned long long key = close && off != 0.f ? s_key[lane] : 0ull;  // where the bound is 0 every score is
+      const unsigned long long key = close && off != 0.f ? sh.key[lane] : 0ull;  // where the bound is 0 every score is
       int before = 0;  // that go before this one
       for (unsigned todo = among; todo != 0; todo &= todo - 1) {
         const int j = __ffs(todo) - 1;
@@ -945,14 +945,14 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
     // ---- Many at the border, or none: NaN or infinities, pages that are alike, or no place but the kept ones'.  The
     // border digit by digit, of the scores and then, among those that they leave open, of the exact scores, each computed
     // again for every digit.
-    int* hist = s_hist[0];
+    int* hist = sh.hist[0];
     auto digit = [&](int left) {  // the one that holds the left-th largest
       __syncthreads();
       if (threadIdx.x == 0) {
         int above = 0, at = 255;
         while (at > 0 && above + hist[at] < left) above += hist[at--];
-        s_digit = at;
-        s_above = above;
+        sh.digit = at;
+        sh.above = above;
       }
       __syncthreads();
     };
@@ -972,15 +972,15 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
           if (((u ^ border) & mask) == 0) atomicAdd(&hist[u >> shift & 255], 1);
         }
         digit(left);
-        border |= static_cast<uint32_t>(s_digit) << shift;
+        border |= static_cast<uint32_t>(sh.digit) << shift;
         mask |= 255u << shift;
-        left -= s_above;
+        left -= sh.above;
       }
     }
     const float at = from_order(border), most = known ? at + 2.f * off : INFINITY, least = known ? at - 2.f * off : -INFINITY;
     auto undecided = [&](int i) { return want > 0 && i >= c0 && i < c1 && (!known || (score(i) <= most && score(i) >= least)); };
     __syncthreads();
-    if (threadIdx.x == 0) s_open[0] = s_over[0] = 0;
+    if (threadIdx.x == 0) sh.open[0] = sh.over[0] = 0;
     __syncthreads();
     int ins = 0, opens = 0;
     for (int w = warp; w < words; w += NW) {
@@ -992,12 +992,12 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
       if (lane == 0) s_bits[w] = in_bits | kept_bits;
     }
     if (lane == 0) {
-      atomicAdd(&s_over[0], ins);
-      atomicAdd(&s_open[0], opens);
+      atomicAdd(&sh.over[0], ins);
+      atomicAdd(&sh.open[0], opens);
     }
     __syncthreads();
-    const int places = want - s_over[0];
-    const bool score_again = places < s_open[0] && !(known && off == 0.f);  // with a bound of 0 every score is 0
+    const int places = want - sh.over[0];
+    const bool score_again = places < sh.open[0] && !(known && off == 0.f);  // with a bound of 0 every score is 0
     unsigned long long key_at = 0, mask = 0;
     int left = places;
     if (score_again) {
@@ -1010,9 +1010,9 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
             if (lane == 0 && ((key ^ key_at) & mask) == 0) atomicAdd(&hist[key >> shift & 255], 1);
           }
         digit(left);
-        key_at |= static_cast<unsigned long long>(s_digit) << shift;
+        key_at |= static_cast<unsigned long long>(sh.digit) << shift;
         mask |= 255ull << shift;
-        left -= s_above;
+        left -= sh.above;
       }
     }
     for (int w = warp; w < words; w += NW) {
@@ -1061,6 +1061,163 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
   }
 }
 
+template <int T, bool CACHED>
+__global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const SelectBlocksParams p, const Scratch ws) {
+  extern __shared__ __align__(16) uint32_t s_bits[];
+  __shared__ PickShared shared;
+  Row row;
+  row.r = blockIdx.x / p.Hkv;
+  row.h = blockIdx.x % p.Hkv;
+  row.n = p.cu == nullptr ? row.r : sequence_of(p, row.r);
+  const Span s = span_of(p, row.n, false);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores are there
+  if (row.r < s.first || row.r >= s.end) return;       // of no sequence: left as it was
+  row.nb = blocks_seen(s, row.r);
+  if (row.nb <= p.K) {
+    choose_all<T>(p, blockIdx.x, row.nb);
+    return;
+  }
+  const float* norms = ws.b_norm + (static_cast<int64_t>(row.n) * p.Hkv + row.h) * ws.tiles;
+  row.q_norm = ws.q_norm[blockIdx.x];
+  row.b_norm = 0.f;
+  for (int i = threadIdx.x; i < (row.nb + 15) / 16; i += T) row.b_norm = fmaxf(row.b_norm, norms[i]);
+  row.scores = ws.scores + static_cast<int64_t>(blockIdx.x) * ws.stride;
+  pick<T, CACHED>(p, row, ws.eps, shared, s_bits);
+}
+
+// Short sequences of one row each: a CTA scores the blocks of a row and KV head and picks among them, in one launch.  A
+// warp takes 16 blocks at a time, their bounds from HBM straight to registers, in the order of the matrix product's left
+// operand.
+template <int D, int T>
+__global__ void __launch_bounds__(T, 512 / T) select_one_kernel(const SelectBlocksParams p, float eps) {
+  constexpr int NW = T / 32, KK = 2 * D / 32, PART = KK < 8 ? KK : 8, PARTS = KK / PART;
+  extern __shared__ __align__(16) uint32_t s_bits[];
+  __shared__ PickShared shared;
+  __shared__ __align__(16) uint32_t s_qb[KK * 2 * 16];  // Q-, Q+ as two bf16 numbers each: [KK][2 columns][16 words]
+  __shared__ float s_squares[NW];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  Row row;
+  const int n = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
+  const Span s = span_of(p, n, h == 0 && threadIdx.x == 0);
+  if (s.end <= s.first) return;
+  row.r = s.first;
+  row.h = h;
+  row.n = n;
+  row.nb = blocks_seen(s, s.first);
+  row.scores = nullptr;
+  const int nb = row.nb;
+  if (nb <= p.K) {
+    choose_all<T>(p, static_cast<int64_t>(row.r) * p.Hkv + h, nb);
+    return;
+  }
+  auto page_of = [&](int tile) {  // of block 16 tile + lane % 16; page 0 where there is none
+    const int blk = tile * 16 + (lane & 15);
+    int id = blk < nb ? p.block_table[static_cast<int64_t>(n) * p.max_blocks + blk] : 0;
+    if (id < 0 || id >= p.num_blocks) {
+      set_error(&g_select_blocks_status, kDevBadPage);
+      id = 0;
+    }
+    return id;
+  };
+  uint32_t a[PART][2][4];
+  auto load = [&](int id, int part) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int64_t page = __shfl_sync(FULL, id, g + 8 * e);
+      const __nv_bfloat16* from = p.bounds + (page * p.Hkv + h) * 2 * D + 32 * PART * part + 8 * t;
+#pragma unroll
+      for (int k = 0; k < PART; ++k) {
+        const uint4 x = *reinterpret_cast<const uint4*>(from + 32 * k);
+        a[k][e][0] = x.x; a[k][e][1] = x.y; a[k][e][2] = x.z; a[k][e][3] = x.w;
+      }
+    }
+  };
+  int tile = warp, id = tile * 16 < nb ? page_of(tile) : 0;
+  // ---- the sums over heads, a pair of channels a thread; four heads' loads in flight
+  const int G = p.Hq / p.Hkv;
+  float squares = 0.f;
+  uint32_t any = 0;
+  if (threadIdx.x < D / 2) {
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(p.q + (static_cast<int64_t>(row.r) * p.Hq + h * G) * D) + threadIdx.x;
+    float neg[2] = {0.f, 0.f}, pos[2] = {0.f, 0.f};
+    for (int e0 = 0; e0 < G; e0 += 4) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = e0 + e < G ? from[(e0 + e) * (D / 2)] : 0u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) add_parts(w[e], neg, pos);
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const float* x = half ? pos : neg;
+      const uint32_t hi = pack_bf16x2(x[0], x[1]);
+      const float2 z = pair_of(hi);
+      const int word = half * (D / 2) + threadIdx.x;
+      s_qb[word / 16 * 32 + word % 16] = hi;
+      s_qb[word / 16 * 32 + 16 + word % 16] = pack_bf16x2(x[0] - z.x, x[1] - z.y);
+      squares = fmaf(x[0], x[0], fmaf(x[1], x[1], squares));
+      any |= hi & 0x7fff7fffu;
+    }
+  }
+  if (tile * 16 < nb) load(id, 0);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) squares += __shfl_xor_sync(FULL, squares, o);
+  if (__any_sync(FULL, any != 0) && squares < LEAST_NORM * LEAST_NORM) squares = LEAST_NORM * LEAST_NORM;
+  if (lane == 0) s_squares[warp] = squares;
+  __syncthreads();
+  squares = 0.f;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) squares += s_squares[i];
+  row.q_norm = sqrtf(squares);
+  row.b_norm = 0.f;
+
+  float* cache = reinterpret_cast<float*>(s_bits + cache_at(p.max_blocks));
+  while (tile * 16 < nb) {
+    const int next = tile + NW, next_id = next * 16 < nb ? page_of(next) : 0;
+    float acc[2][4] = {}, norm[2] = {0.f, 0.f};
+#pragma unroll
+    for (int part = 0; part < PARTS; ++part) {
+      if (part > 0) load(id, part);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t sum[2] = {0u, 0u};
+#pragma unroll
+        for (int k = 0; k < PART; ++k)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) sum[w & 1] = add_squares(a[k][e][w], sum[w & 1]);
+        const float2 x = pair_of(sum[0]), y = pair_of(sum[1]);
+        norm[e] += (x.x + x.y) + (y.x + y.y);
+      }
+#pragma unroll
+      for (int k = 0; k < PART; ++k) {
+        uint4 b = make_uint4(0, 0, 0, 0);  // the columns behind the second are 0
+        if (g < 2) b = *reinterpret_cast<const uint4*>(s_qb + (part * PART + k) * 32 + g * 16 + t * 4);
+        mma_16816<false>(acc[0], a[k][0][0], a[k][1][0], a[k][0][1], a[k][1][1], b.x, b.y);
+        mma_16816<false>(acc[1], a[k][0][2], a[k][1][2], a[k][0][3], a[k][1][3], b.z, b.w);
+      }
+    }
+    const int blk = tile * 16 + g;
+    if (t == 0) {
+      if (blk < nb) cache[blk] = (acc[0][0] + acc[1][0]) + (acc[0][1] + acc[1][1]);
+      if (blk + 8 < nb) cache[blk + 8] = (acc[0][2] + acc[1][2]) + (acc[0][3] + acc[1][3]);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      norm[e] += __shfl_xor_sync(FULL, norm[e], 1);
+      norm[e] += __shfl_xor_sync(FULL, norm[e], 2);
+      if (!(norm[e] < INFINITY)) norm[e] = INFINITY;  // NaN too
+      if (blk + 8 * e < nb) row.b_norm = fmaxf(row.b_norm, norm[e]);
+    }
+    tile = next;
+    id = next_id;
+    if (tile * 16 < nb) load(id, 0);
+  }
+  // the sum of squares may have been an eighth too small
+  row.b_norm = fmaxf(1.1f * sqrtf(row.b_norm), LEAST_NORM);
+  __syncthreads();
+  pick<T, true>(p, row, eps, shared, s_bits);
+}
+
 // A launch as a programmatic dependent of the kernel before it
 template <class... Params, class... Args>
 cudaError_t launch_behind(void (*kernel)(Params...), unsigned grid, unsigned threads, int smem, cudaStream_t stream, Args... args) {
@@ -1086,14 +1243,20 @@ cudaError_t select(const SelectBlocksParams& p, const Scratch& ws, cudaStream_t 
                        ws);
 }
 
+template <int D, int T>
+cudaError_t select_one(const SelectBlocksParams& p, float eps, cudaStream_t stream) {
+  const int smem = (cache_at(p.max_blocks) + (p.max_blocks + 3) / 4 * 4) * 4;
+  const cudaError_t e = cudaFuncSetAttribute(select_one_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  select_one_kernel<D, T><<<static_cast<unsigned>(static_cast<int64_t>(p.N) * p.Hkv), T, smem, stream>>>(p, eps);
+  return cudaGetLastError();
+}
+
 template <int D>
-cudaError_t score_few(const SelectBlocksParams& p, const Scratch& ws, cudaStream_t stream) {
+cudaError_t score_few(const SelectBlocksParams& p, const Scratch& ws, int sms, cudaStream_t stream) {
   using C = FewCfg<D>;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int warps = C::warps(p.max_q), smem = warps * C::warp_bytes(p.max_q);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(score_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = cudaFuncSetAttribute(score_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   score_few_kernel<D><<<sms, warps * 32, smem, stream>>>(p, ws);
   return cudaGetLastError();
@@ -1118,7 +1281,19 @@ template <int D>
 cudaError_t launch(const SelectBlocksParams& p, Scratch& ws, cudaStream_t stream) {
   // the two roundings of Q+-, the sums over heads, and 2 d / 16 products of 16 terms with their final addition
   ws.eps = 1.f / (1 << 18) + static_cast<float>(p.Hq / p.Hkv) / (1 << 24) + static_cast<float>(D / 8 + 2) / (1 << 22);
-  const cudaError_t e = p.max_q <= FEW ? score_few<D>(p, ws, stream) : score_many<D>(p, ws, stream);
+  const int64_t pairs = static_cast<int64_t>(p.N) * p.Hkv;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // One launch as long as every row and KV head has a CTA at once and tables are short enough for a CTA to read a row's
+  // bounds alone.  Both sides at d = 128, one against two launches: 128 rows times heads of 250 blocks 10.4 and 14.9 us, of
+  // 1000 26.3 and 26.1, of 2000 45.7 and 38.5; 8 of 250 8.8 and 11.2, of 500 10.9 and 10.5, of 1000 17.2 and 12.3; 256 of
+  // 500 21.7 and 26.4.  Of more, smaller CTAs: 512 of 125 12.1 and 18.3, of 250 22.0 and 26.5, of 32 to 512 30.9 and 27.5,
+  // where the longest is waited for; 2048 of 125 45.0 and 43.2.
+  if (p.max_q == 1 && pairs <= 2 * sms && p.max_blocks <= 250 + 8 * pairs) return select_one<D, 256>(p, ws.eps, stream);
+  if (p.max_q == 1 && pairs <= 4 * sms && p.max_blocks <= 256) return select_one<D, 128>(p, ws.eps, stream);
+  e = p.max_q <= FEW ? score_few<D>(p, ws, sms, stream) : score_many<D>(p, ws, stream);
   if (e != cudaSuccess) return e;
   // Of few long rows the latency of one is to be shortened.  Of many, instructions count, which are fewer the fewer warps
   // do a row's common work: 4096 rows of 2048 blocks take 51 us with 128 threads, 55 with 64, which leave too few warps.

@@ -211,6 +211,57 @@ def test_select_of_many_and_of_long_sequences(attn, gpu, N, length, Hkv, d, K):
         assert attn.device_status(clear=True) == 5
 
 
+@pytest.mark.parametrize("N,Hkv,d,width", [
+    (1, 1, 128, 258), (1, 1, 128, 259), (1, 2, 64, 266), (3, 5, 256, 370), (2, 8, 128, 378), (16, 8, 128, 1274), (38, 8, 64, 300),
+    (304, 1, 256, 40), (305, 1, 256, 40), (51, 6, 128, 256), (76, 8, 128, 256), (77, 8, 128, 256), (608, 1, 64, 100),
+    (609, 1, 64, 100), (400, 1, 128, 257), (100, 4, 256, 255)])
+def test_select_of_one_row_each(attn, gpu, N, Hkv, d, width):
+    """Either side of the sizes that one launch takes: some sequences without a row, without tokens, with fewer blocks than
+    are chosen, with bounds that are no numbers or infinite, and with queries of zeros."""
+    gen = torch.Generator(device=gpu).manual_seed(N * width + d)
+    rng = np.random.default_rng(N * width + d)
+    K, first, last = 17, 2, 1
+    lens = [int(x) for x in rng.integers(1, 16 * width + 1, N)]
+    lens[0], lens[-1] = 16 * width, lens[-1] if N < 4 else 0
+    for n in range(2, N, 9):
+        lens[n] = int(rng.integers(1, 16 * K + 20))
+    rows = [0 if N > 4 and n % 11 == 5 else 1 for n in range(N)]
+    cu = np.concatenate([[0], np.cumsum(rows)]).tolist()
+    blocks = 3 * width
+    b = torch.randn((blocks, Hkv, 2, d), generator=gen, device=gpu).sort(2).values.to(torch.bfloat16)
+    b[torch.rand(blocks, generator=gen, device=gpu) < 0.3] = b[0].clone()                  # many alike
+    table = torch.randint(0, blocks, (N, width), generator=gen, device=gpu, dtype=torch.int32)
+    q = _randn((cu[-1], 3 * Hkv, d), gen, gpu)
+    q[cu[-1] // 3] = 0
+    out = torch.full((cu[-1], Hkv, K), 7, dtype=torch.int32, device=gpu)
+    for odd in (None, math.inf, math.nan):
+        if odd is not None:
+            b[1, :, 1, 3] = odd                            # a query that is 0 there has 0 inf in its sum: not a number
+            q[:, :, 3] = q[:, :, 3].abs().clamp(min=0.5)
+        got = attn.select_blocks(q, b, table, _i32(lens, gpu), K, first=first, last=last, cu_seqlens_q=_i32(cu, gpu),
+                                 max_seqlen_q=1, out=out)
+        for n in range(N) if N < 20 else sorted({0, 1, 2, 5, 11, N // 2, N - 2, N - 1}):
+            if rows[n]:
+                want = _wanted_odd(q[cu[n]:cu[n] + 1], b, table[n:n + 1], lens[n], K, first, last)
+                assert torch.equal(got[cu[n]], want), (odd, n)
+    assert attn.device_status() == 0
+
+
+def _wanted_odd(q, bounds, table, length, K, first, last):
+    """_wanted for one row, with NaN above all other scores."""
+    nb = _pages(length)
+    if nb <= K:
+        return _wanted(q, bounds, table, [0, 1], [length], K, first, last)[0]
+    H, d = bounds.shape[1], q.shape[-1]
+    x, b = q[0].double().view(H, -1, d), bounds[table[0, :nb].long()].double()
+    s = (x.clamp(max=0).sum(1) * b[:, :, 0]).sum(-1) + (x.clamp(min=0).sum(1) * b[:, :, 1]).sum(-1)
+    key = torch.where(s.isnan(), math.inf, s)
+    key[:first], key[nb - last:] = math.inf, math.inf
+    order = [sorted(range(nb), key=lambda i: (0 if i < first or i >= nb - last else 1 if nan[i] else 2, -col[i], i))[:K]
+             for nan, col in zip(s.isnan().T.tolist(), key.T.tolist())]
+    return torch.tensor([sorted(o) for o in order], dtype=torch.int32, device=q.device)
+
+
 def test_select_of_a_chunk_in_a_wide_table(attn, gpu):
     """A prompt's chunk whose sequence fills a small part of its table, beside one that fills it."""
     gen = torch.Generator(device=gpu).manual_seed(5)
@@ -375,7 +426,8 @@ def _timed(call):
 @pytest.mark.parametrize("drop", [1, 2])
 @pytest.mark.parametrize("listed", [False, True])
 @pytest.mark.parametrize("N,length,Hq,Hkv,d", [(3, 700, 8, 2, 128), (9000, 16, 4, 2, 64), (9000, 16, 5, 1, 128),
-                                               (5000, 16, 2, 1, 256)])
+                                               (5000, 16, 2, 1, 256), (300, 16, 4, 2, 64), (200, 100, 5, 1, 128),
+                                               (120, 40, 4, 2, 256)])
 def test_decode_waits_that_run_out(attn, gpu, waitlib, drop, listed, N, length, Hq, Hkv, d):
     lib = waitlib
     gen, cache, bounds, table = _setup(attn, gpu, [length] * 3, Hkv, d, seed=2)
