@@ -44,7 +44,7 @@ constexpr int FEW = 4;             // rows a sequence up to which score_few_kern
 constexpr int BINS = 512;          // of a window of scores
 constexpr int CACHED_BLOCKS = 12288;  // scores of a row that shared memory holds
 constexpr int NARROW = 1024;       // columns of a block table up to which 128 threads take a row
-constexpr int64_t MANY_ROWS = 1024;  // rows times heads from which on they do so for any table
+constexpr int64_t MANY_ROWS = 256;  // rows times heads from which on they do so for any table
 // Norms below this count as this: squares of smaller numbers may vanish, and a bound that is too large does no harm
 constexpr float LEAST_NORM = 1e-14f;
 constexpr int64_t SCORE_CTAS = 152 * 4;  // of the grid, about: a block table may be far wider than its sequences
@@ -1297,6 +1297,8 @@ cudaError_t launch(const SelectBlocksParams& p, Scratch& ws, cudaStream_t stream
   if (e != cudaSuccess) return e;
   // Of few long rows the latency of one is to be shortened.  Of many, instructions count, which are fewer the fewer warps
   // do a row's common work: 4096 rows of 2048 blocks take 51 us with 128 threads, 55 with 64, which leave too few warps.
+  // Both calls of 128 and 1024 threads, d = 64: 128 rows of 2500 blocks 32.5 and 29.2 us, 256 48.1 and 52.1, 800 113 and
+  // 149; of 8125 128 72.5 and 62.9, 256 122.9 and 121.8, 512 221 and 239.
   if (p.max_blocks > CACHED_BLOCKS) return select<1024, false>(p, ws, stream);
   const bool many = static_cast<int64_t>(p.T) * p.Hkv >= MANY_ROWS;
   return many || p.max_blocks <= NARROW ? select<128, true>(p, ws, stream) : select<1024, true>(p, ws, stream);
