@@ -728,8 +728,8 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
   float low = INFINITY, high = -INFINITY, off;
   {
 #pragma unroll 2
-    for (int v = threadIdx.x; 4 * v < nb; v += T) {
-      const float4 x = read_four(v);
+    for (int v = threadIdx.x; 4 * v < (CACHED ? 32 * words : nb); v += T) {
+      const float4 x = 4 * v < nb ? read_four(v) : make_float4(none, none, none, none);
       if constexpr (CACHED) *reinterpret_cast<float4*>(cache + 4 * v) = x;
       low = fminf(fminf(low, fminf(x.x, x.y)), fminf(x.z, x.w));
       high = fmaxf(fmaxf(high, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
@@ -738,13 +738,10 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
     uint32_t least = __reduce_min_sync(FULL, order_of(low)), top = __reduce_max_sync(FULL, order_of(high));
     if (lane == 0) sh.red[warp] = make_uint4(most, least, top, 0);
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      const uint4 x = sh.red[i];
-      most = max(most, x.x);
-      least = min(least, x.y);
-      top = max(top, x.z);
-    }
+    const uint4 x = sh.red[lane % NW];
+    most = __reduce_max_sync(FULL, x.x);
+    least = __reduce_min_sync(FULL, x.y);
+    top = __reduce_max_sync(FULL, x.z);
     off = eps * row.q_norm * __uint_as_float(most);
     low = from_order(least);
     high = from_order(top);
@@ -803,12 +800,13 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
   int open = 0, over = 0;  // in the window; above it
   for (int round = 0; known && want > 0 && !few; ++round) {
     int* hist = sh.hist[round & 1];
-    const float range = high - low, per_bin = BINS / range;
-    if (!(range < INFINITY && per_bin < INFINITY)) break;  // all alike, or past float32
+    // 4 BINS - 1 steps, of which a bin takes four: a score's, rounded to the nearest by adding 3 2^22, is in the sum's last bits
+    const float range = high - low, per_step = (4 * BINS - 1) / range;
+    if (!(range < INFINITY && per_step < INFINITY)) break;  // all alike, or past float32
     auto count = [&](float x) {
       if (x >= low && x <= high) {
-        const int bin = static_cast<int>((x - low) * per_bin);
-        atomicAdd(&hist[bin < BINS ? bin : BINS - 1], 1);
+        const int step = __float_as_int(fmaf(x - low, per_step, 12582912.f));
+        atomicAdd(&hist[(step & (4 * BINS - 1)) >> 2], 1);
       }
     };
     for (int v = threadIdx.x; 4 * v < nb; v += T) {
@@ -819,59 +817,55 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
       count(x.w);
     }
     __syncthreads();
-    // every warp finds the bin of the border: lane 0 holds the highest
-    constexpr int PER = BINS / 32;
-    int c[PER], sum = 0, bin = -1;
+    // a warp finds the bin of the border, each for itself where they are few: lane 0 holds the highest
+    int bin = -1;
+    if (NW <= 8 || warp == 0) {
+      constexpr int PER = BINS / 32;
+      int c[PER], sum = 0;
 #pragma unroll
-    for (int j = 0; j < PER; j += 4) {
-      const int4 x = *reinterpret_cast<const int4*>(hist + BINS - PER * (lane + 1) + j);
-      c[j] = x.x; c[j + 1] = x.y; c[j + 2] = x.z; c[j + 3] = x.w;
-      sum += x.x + x.y + x.z + x.w;
-    }
-    int above = sum;
+      for (int j = 0; j < PER; j += 4) {
+        const int4 x = *reinterpret_cast<const int4*>(hist + BINS - PER * (lane + 1) + j);
+        c[j] = x.x; c[j + 1] = x.y; c[j + 2] = x.z; c[j + 3] = x.w;
+        sum += x.x + x.y + x.z + x.w;
+      }
+      int above = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(FULL, above, o);
-      if (lane >= o) above += x;
-    }
-    above += over - sum;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(FULL, above, o);
+        if (lane >= o) above += x;
+      }
+      above += over - sum;
 #pragma unroll
-    for (int j = PER - 1; j >= 0; --j) {
-      if (above < want && want <= above + c[j]) bin = BINS - PER * (lane + 1) + j;
-      above += c[j];
+      for (int j = PER - 1; j >= 0; --j) {
+        if (above < want && want <= above + c[j]) bin = BINS - PER * (lane + 1) + j;
+        above += c[j];
+      }
+      bin = __reduce_max_sync(FULL, bin);
     }
-    bin = __reduce_max_sync(FULL, bin);
+    if constexpr (NW > 8) {
+      if (threadIdx.x == 0) sh.digit = bin;
+      __syncthreads();
+      bin = sh.digit;
+    }
     // its blocks, and those within the twofold error (and a rounding of the bin's ends, 2^-6 of a bin) of it
-    const float width = range / BINS, slack = 2.f * off + width * (1.f / 64);
-    low = low + bin * width - slack;
-    high = low + width + 2.f * slack;
+    const float step = range / (4 * BINS - 1), slack = 2.f * off + step * (1.f / 16);
+    low = low + (4 * bin - 0.5f) * step - slack;
+    high = low + 4.f * step + 2.f * slack;
     int above_high = 0;
-    for (int v = threadIdx.x; 4 * (v - lane) < nb; v += T) {
-      const float4 x = 4 * v < nb ? four(v) : make_float4(none, none, none, none);
-      unsigned bits = (x.x > high ? 1u : 0u) | (x.y > high ? 2u : 0u) | (x.z > high ? 4u : 0u) | (x.w > high ? 8u : 0u);
-      const unsigned here =
-          ((x.x >= low ? 1u : 0u) | (x.y >= low ? 2u : 0u) | (x.z >= low ? 4u : 0u) | (x.w >= low ? 8u : 0u)) & ~bits;
-      for (unsigned todo = here; todo != 0; todo &= todo - 1) {
-        const int j = __ffs(todo) - 1, k = atomicAdd(&sh.open[round & 1], 1);
+    for (int w = warp; w < words; w += NW) {
+      const float x = score(32 * w + lane);
+      const bool above = x > high;
+      if (x >= low && !above) {
+        const int k = atomicAdd(&sh.open[round & 1], 1);
         if (k < 32) {
-          sh.at[k] = 4 * v + j;
-          sh.score[k] = j == 0 ? x.x : j == 1 ? x.y : j == 2 ? x.z : x.w;
+          sh.at[k] = 32 * w + lane;
+          sh.score[k] = x;
         }
       }
+      const unsigned bits = __ballot_sync(FULL, above);
       above_high += __popc(bits);
-      if (edge(v)) {  // the kept ones
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (4 * v + j < nb && !competes(4 * v + j)) bits |= 1u << j;
-      }
-      // eight lanes a word
-      bits <<= 4 * (lane & 7);
-      bits |= __shfl_xor_sync(FULL, bits, 1);
-      bits |= __shfl_xor_sync(FULL, bits, 2);
-      bits |= __shfl_xor_sync(FULL, bits, 4);
-      if ((lane & 7) == 0 && 4 * v < nb) s_bits[v >> 3] = bits;
+      if (lane == 0) s_bits[w] = bits;
     }
-    above_high = __reduce_add_sync(FULL, above_high);
     if (lane == 0 && above_high > 0) atomicAdd(&sh.over[round & 1], above_high);
     __syncthreads();
     open = sh.open[round & 1];
@@ -889,6 +883,7 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
   if (few) {
     // ---- a warp settles it, a lane a block
     const int places = want - over;  // 1 <= places <= open
+    for (int i = threadIdx.x; i < p.first + p.last; i += T) choose(i < p.first ? i : nb - p.last + i - p.first);
     bool sure = false, close = false;
     int i = 0x7fffffff, rest = 0;
     unsigned among = 0;
@@ -1047,6 +1042,10 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
   for (int w0 = 0, group = 0; w0 < words; w0 += 32, ++group) {
     unsigned bits = w0 + lane < words ? s_bits[w0 + lane] : 0u;
     int upto = __popc(bits);
+    if (group % NW != warp) {
+      base += __reduce_add_sync(FULL, upto);
+      continue;
+    }
     int place = base - upto;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -1055,7 +1054,6 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
     }
     place += upto;
     base += __shfl_sync(FULL, upto, 31);
-    if (group % NW != warp) continue;
     for (; bits != 0; bits &= bits - 1, ++place)
       if (place < K) out[place] = 32 * (w0 + lane) + __ffs(bits) - 1;
   }
@@ -1236,7 +1234,7 @@ cudaError_t launch_behind(void (*kernel)(Params...), unsigned grid, unsigned thr
 
 template <int T, bool CACHED>
 cudaError_t select(const SelectBlocksParams& p, const Scratch& ws, cudaStream_t stream) {
-  const int smem = (cache_at(p.max_blocks) + (CACHED ? (p.max_blocks + 3) / 4 * 4 : 0)) * 4;
+  const int smem = (cache_at(p.max_blocks) + (CACHED ? (p.max_blocks + 31) / 32 * 32 : 0)) * 4;
   const cudaError_t e = cudaFuncSetAttribute(select_kernel<T, CACHED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_behind(select_kernel<T, CACHED>, static_cast<unsigned>(static_cast<int64_t>(p.T) * p.Hkv), T, smem, stream, p,
@@ -1245,7 +1243,7 @@ cudaError_t select(const SelectBlocksParams& p, const Scratch& ws, cudaStream_t 
 
 template <int D, int T>
 cudaError_t select_one(const SelectBlocksParams& p, float eps, cudaStream_t stream) {
-  const int smem = (cache_at(p.max_blocks) + (p.max_blocks + 3) / 4 * 4) * 4;
+  const int smem = (cache_at(p.max_blocks) + (p.max_blocks + 31) / 32 * 32) * 4;
   const cudaError_t e = cudaFuncSetAttribute(select_one_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   select_one_kernel<D, T><<<static_cast<unsigned>(static_cast<int64_t>(p.N) * p.Hkv), T, smem, stream>>>(p, eps);
