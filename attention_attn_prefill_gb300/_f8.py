@@ -234,8 +234,8 @@ def select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tens
           or not out.is_contiguous()):
         _explain(dev, (out, _I32, "out (of shape [T, Hkv, num_selected])"))
     if workspace is None:
-        workspace = _empty_on(max(1, select_blocks_workspace_bytes(T, N, max_seqlen_q, Hkv, d, block_table.shape[1])), _U8, dev, stream,
-                              returned=False)
+        need = select_blocks_workspace_bytes(T, N, max_seqlen_q, Hkv, d, block_table.shape[1])
+        workspace = _empty_on(max(1, need), _U8, dev, stream, returned=False)
     elif workspace.dtype is not _U8 or workspace.get_device() != dev or not workspace.is_contiguous():
         _explain(dev, (workspace, _U8, "workspace"))
     if T == 0:  # a step without tokens

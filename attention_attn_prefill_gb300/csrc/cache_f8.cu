@@ -10,6 +10,11 @@
 // it.  The keys' warp also keeps the smallest and largest key of the page in each channel, which block selection
 // scores by; the reduction over tokens halves the channels a lane holds at each step, 7 exchanges for 16 channels.
 // Read-back: a warp at a record.
+//
+// Measured (GB300, copy rate 6796 GB/s): the write of 32002 tokens, 8 heads, d = 128, and their read-back, 402 MB in
+// all, 63.2 us in a captured graph, 6.4 TB/s.  Alone and from a cold L2 31 and 29 us: the write uses half of the
+// issue slots, the read-back a third; both wait for memory.  64 tokens written and 64 sequences of up to 250 read
+// back: 12.4 us (7.9 at the copy rate), two launches with their start and end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -14,7 +14,13 @@
 // 128 blocks by 64 rows a tcgen05 tile.  Either way
 //   |score - exact| <= eps ||Q|| ||b||,  b = (lo, hi) of a block, by Cauchy and Schwarz on the sum of |terms|.
 // Select kernel: a CTA puts the scores of its row and head into bins over their range, gathers the few in and about the
-// bin that holds the border, and a warp settles the border among them.
+// bin that holds the border, and a warp settles the border among them.  Few short sequences of one row each take one
+// launch, a CTA scoring and picking: select_one_kernel.
+//
+// Measured (GB300, calls in a captured graph, copy rate 6796 GB/s): 64 rows over 512 to 8192 tokens, 32/8 heads, d = 128,
+// 27.4 us, of which the scores' kernel takes about 17 (72 MB of bounds: 10.6 at the copy rate) and the rest is the pick's
+// chain of dependent steps; 8 rows over 6335 to 122863 tokens, 16/2 heads, d = 256, 29.0 (9.8); 512 rows of one
+// sequence of 32768, 32/8 heads, 50.9, of which the pick takes about 25 (4096 rows of 2048 scores), the products 20.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -44,7 +50,6 @@ constexpr int FEW = 4;             // rows a sequence up to which score_few_kern
 constexpr int BINS = 512;          // of a window of scores
 constexpr int CACHED_BLOCKS = 12288;  // scores of a row that shared memory holds
 constexpr int NARROW = 1024;       // columns of a block table up to which 128 threads take a row
-constexpr int64_t MANY_ROWS = 256;  // rows times heads from which on they do so for any table
 // Norms below this count as this: squares of smaller numbers may vanish, and a bound that is too large does no harm
 constexpr float LEAST_NORM = 1e-14f;
 constexpr int64_t SCORE_CTAS = 152 * 4;  // of the grid, about: a block table may be far wider than its sequences
@@ -1286,19 +1291,19 @@ cudaError_t launch(const SelectBlocksParams& p, Scratch& ws, cudaStream_t stream
   if (e != cudaSuccess) return e;
   // One launch as long as every row and KV head has a CTA at once and tables are short enough for a CTA to read a row's
   // bounds alone.  Both sides at d = 128, one against two launches: 128 rows times heads of 250 blocks 10.4 and 14.9 us, of
-  // 1000 26.3 and 26.1, of 2000 45.7 and 38.5; 8 of 250 8.8 and 11.2, of 500 10.9 and 10.5, of 1000 17.2 and 12.3; 256 of
-  // 500 21.7 and 26.4.  Of more, smaller CTAs: 512 of 125 12.1 and 18.3, of 250 22.0 and 26.5, of 32 to 512 30.9 and 27.5,
-  // where the longest is waited for; 2048 of 125 45.0 and 43.2.
+  // 1000 26.3 and 26.1; 8 of 250 8.8 and 11.2, of 500 10.9 and 10.5, of 1000 17.2 and 12.3; 256 of 500 21.7 and 26.4.  Of
+  // more, smaller CTAs: 512 of 125 12.1 and 18.3, of 250 22.0 and 26.5, of 32 to 512 30.9 and 27.5, where the longest is
+  // waited for; 2048 of 125 45.0 and 43.2.
   if (p.max_q == 1 && pairs <= 2 * sms && p.max_blocks <= 250 + 8 * pairs) return select_one<D, 256>(p, ws.eps, stream);
   if (p.max_q == 1 && pairs <= 4 * sms && p.max_blocks <= 256) return select_one<D, 128>(p, ws.eps, stream);
   e = p.max_q <= FEW ? score_few<D>(p, ws, sms, stream) : score_many<D>(p, ws, stream);
   if (e != cudaSuccess) return e;
   // Of few long rows the latency of one is to be shortened.  Of many, instructions count, which are fewer the fewer warps
   // do a row's common work: 4096 rows of 2048 blocks take 51 us with 128 threads, 55 with 64, which leave too few warps.
-  // Both calls of 128 and 1024 threads, d = 64: 128 rows of 2500 blocks 32.5 and 29.2 us, 256 48.1 and 52.1, 800 113 and
-  // 149; of 8125 128 72.5 and 62.9, 256 122.9 and 121.8, 512 221 and 239.
+  // The whole call with 128 and with 1024 threads, d = 64: 128 rows of 2500 blocks 31.9 and 26.0 us, 256 47.6 and 46.1, 512
+  // 80.8 and 89.3, 800 112 and 132; of 8125 128 71.8 and 59.3, 256 122.3 and 116.6, 512 220.8 and 228.2, 800 346 and 352.
   if (p.max_blocks > CACHED_BLOCKS) return select<1024, false>(p, ws, stream);
-  const bool many = static_cast<int64_t>(p.T) * p.Hkv >= MANY_ROWS;
+  const bool many = static_cast<int64_t>(p.T) * p.Hkv > 2 * sms;  // more than 1024 threads each can take at once
   return many || p.max_blocks <= NARROW ? select<128, true>(p, ws, stream) : select<1024, true>(p, ws, stream);
 }
 

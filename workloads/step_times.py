@@ -1,9 +1,9 @@
 """Times of the serving-step operators on this GPU: `python -m workloads.step_times [4-bit|8-bit] [name ...]`.
 
 For each case of perf/operators.py (4-bit) and of perf/more_operators.py (8-bit), and for head counts that they do not
-list, the time of a call among 20 in a captured graph, over two sets of inputs in turn (those of the large cases exceed L2, those of the small ones stay in
-it), median of nine replays after two.  The decode cases are timed on a bf16 cache of the same lengths too, by the
-same method, with the group size that decode_auto_split_tokens picks.
+list, the time of a call among 20 in a captured graph, over two sets of inputs in turn (those of the large cases
+exceed L2, those of the small ones stay in it), median of nine replays after two.  The decode cases are timed on a bf16
+cache of the same lengths too, by the same method, with the group size that decode_auto_split_tokens picks.
 """
 from __future__ import annotations
 
