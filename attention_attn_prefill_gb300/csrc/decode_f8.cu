@@ -59,8 +59,9 @@ constexpr float W_ROOM = 8.f;          // ... to where the largest is 2^8: fp16 
 constexpr uint32_t Q_TOP = 14;         // a head's largest channel is put at 2^14 .. 2^15
 
 // How the list is dealt out.  SHARES: equal shares of it, one a CTA, and a second kernel that merges what a share's end
-// cuts.  WHOLE: a CTA takes all steps of one row and unit.  ALONE: so too, with as many warps as an SM holds.
-enum Deal { SHARES, WHOLE, ALONE };
+// cuts.  Else a CTA takes all steps of one row and unit: ALONE with as many warps as an SM holds, WHOLE with the warps of
+// a share, MANY with fewer, so that more CTAs fit.
+enum Deal { SHARES, WHOLE, ALONE, MANY };
 
 // P: pages a warp takes at a step; ROWS / P query heads.
 template <int D, int P, int DEAL>
@@ -68,10 +69,11 @@ struct Cfg {
   // Warps that compute (one more loads), steps in flight a warp, and CTAs an SM: what shared memory holds.  Measured on 64
   // sequences of 512 to 8192, 32/8 heads, d = 128, warps x steps x CTAs: 5 x 2 x 2 98.8 us, 3 x 2 x 3 100.4, 4 x 3 x 2
   // 103.9, 11 x 2 x 1 102.7 (more in flight is no faster), one page a step 7 x 2 x 2 100.6.
-  static constexpr int NW = DEAL == ALONE ? (D == 256 ? 8 : D == 128 && P == 2 ? 11 : 13)
-                                          : (D == 256 ? 4 : D == 128 && P == 1 ? 7 : 5);
+  static constexpr int NW = DEAL == ALONE  ? (D == 256 ? 8 : D == 128 && P == 2 ? 11 : 13)
+                            : DEAL == MANY ? (D == 256 ? 2 : 3)
+                                           : (D == 256 ? 4 : D == 128 && P == 1 ? 7 : 5);
   static constexpr int DEPTH = D == 64 ? 3 : 2;
-  static constexpr int CTAS = DEAL == ALONE ? 1 : D == 64 ? 3 : 2;
+  static constexpr int CTAS = DEAL == ALONE ? 1 : DEAL == MANY ? (D == 64 ? 5 : 4) : D == 64 ? 3 : 2;
   static constexpr int THREADS = (NW + 1) * 32;
   static constexpr int TILE = ROWS / P;  // query heads a tile
   static constexpr int SLOTS = NW * DEPTH;
@@ -81,7 +83,7 @@ struct Cfg {
   static constexpr int MERGE_OFF = SLOTS * STAGE;
   static constexpr int BAR_OFF = MERGE_OFF + NW * MERGE * 4;
   static constexpr int ALLOC = BAR_OFF + (2 * SLOTS + 2) * 8;
-  static_assert(CTAS * (ALLOC + 1024 + 24 * THREADS) <= 228 * 1024, "shared memory budget");
+  static_assert(CTAS * (ALLOC + 1024 + (DEAL == SHARES ? 24 * THREADS : 384)) <= 228 * 1024, "shared memory budget");
 };
 
 // 64-bit division costs over a hundred instructions, and the lists of all but the largest batches are counted in 32 bits
@@ -323,6 +325,58 @@ __global__ void __launch_bounds__(Cfg<D, P, DEAL>::THREADS, Cfg<D, P, DEAL>::CTA
     return;
   }
 
+  // The warps' states of a segment, left in the merge buffer, become a result or a partial: threads `first` of `of`
+  auto merge_states = [&](int n, int u, bool starts, bool ends, bool lives, int first, int of) {
+    const int kvh = u / geo.tiles, h0 = u % geo.tiles * TILE;
+    const int heads = G - h0 < TILE ? G - h0 : TILE;
+    const int64_t part = 2 * static_cast<int64_t>(b) + (starts ? 1 : 0);
+    // four at a time: one alone would wait for its loads (d = 256, 8 heads, by one warp: 9700 cycles one by one)
+    constexpr int AT_ONCE = 4;
+    for (int w0 = first; w0 < heads * (D / 4); w0 += of * AT_ONCE) {
+      float M[AT_ONCE], L[AT_ONCE];
+      float4 O[AT_ONCE];
+#pragma unroll
+      for (int k = 0; k < AT_ONCE; ++k) {
+        const int w = w0 + of * k, r = w < heads * (D / 4) ? w / (D / 4) : 0, x = w % (D / 4) * 4;
+        M[k] = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < NW; ++v) M[k] = fmaxf(M[k], merge[v * C::MERGE + r]);
+        L[k] = 0.f;
+        O[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < NW; ++v) {
+          const float* src = merge + v * C::MERGE;
+          const float l = src[ROWS + r];
+          const float wl = l == 0.f ? 0.f : l * ex2_approx(src[r] - M[k]);  // 0: a warp without tokens
+          const float4 y = *reinterpret_cast<const float4*>(src + 2 * ROWS + r * C::OROW + x);
+          L[k] += wl;
+          O[k].x = fmaf(y.x, wl, O[k].x); O[k].y = fmaf(y.y, wl, O[k].y);
+          O[k].z = fmaf(y.z, wl, O[k].z); O[k].w = fmaf(y.w, wl, O[k].w);
+        }
+        const float inv = L[k] == 0.f ? 0.f : 1.f / L[k];
+        O[k].x *= inv; O[k].y *= inv; O[k].z *= inv; O[k].w *= inv;
+      }
+#pragma unroll
+      for (int k = 0; k < AT_ONCE; ++k) {
+        const int w = w0 + of * k, r = w / (D / 4), x = w % (D / 4) * 4;
+        if (w >= heads * (D / 4)) break;
+        if (DEAL != SHARES || (starts && ends)) {
+          if (lives) {
+            const int64_t row = static_cast<int64_t>(n) * p.Hq + kvh * G + h0 + r;
+            *reinterpret_cast<uint2*>(p.o + row * D + x) = make_uint2(pack_bf16x2(O[k].x, O[k].y), pack_bf16x2(O[k].z, O[k].w));
+            if (x == 0 && p.lse != nullptr) p.lse[row] = (M[k] + log2f(L[k])) * LN2;
+          }
+        } else {
+          *reinterpret_cast<float4*>(ws.o + (part * ROWS + r) * D + x) = O[k];
+          if (x == 0) {
+            ws.m[part * ROWS + r] = M[k];
+            ws.l[part * ROWS + r] = L[k];
+          }
+        }
+      }
+    }
+  };
+
   At<P, LISTED> cur;  // the share's first step
   cur.begin(p, s_start.x, s_start.y, s_start.z);
 
@@ -436,56 +490,10 @@ __global__ void __launch_bounds__(Cfg<D, P, DEAL>::THREADS, Cfg<D, P, DEAL>::CTA
         seg_phase ^= 1;
         const int seg_steps = seg.ns - seg.step < count - seg_i ? seg.ns - seg.step : count - seg_i;
         const bool starts = seg.step == 0, ends = seg.step + seg_steps == seg.ns;
-        const int kvh = seg.u / geo.tiles, h0 = seg.u % geo.tiles * TILE;
-        const int heads = G - h0 < TILE ? G - h0 : TILE;
-        const int64_t part = 2 * static_cast<int64_t>(b) + (starts ? 1 : 0);
         // a row of no sequence has no result
         const bool lives = !LISTED || p.cu == nullptr || row_info(p, seg.n).n >= 0;
-        // four at a time: one alone would wait for its loads (d = 256, 8 heads: 9700 cycles one by one)
-        constexpr int AT_ONCE = 4;
-        for (int w0 = lane; w0 < heads * (D / 4); w0 += 32 * AT_ONCE) {
-          float M[AT_ONCE], L[AT_ONCE];
-          float4 O[AT_ONCE];
-#pragma unroll
-          for (int k = 0; k < AT_ONCE; ++k) {
-            const int w = w0 + 32 * k, r = w < heads * (D / 4) ? w / (D / 4) : 0, x = w % (D / 4) * 4;
-            M[k] = -INFINITY;
-#pragma unroll
-            for (int v = 0; v < NW; ++v) M[k] = fmaxf(M[k], merge[v * C::MERGE + r]);
-            L[k] = 0.f;
-            O[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int v = 0; v < NW; ++v) {
-              const float* src = merge + v * C::MERGE;
-              const float l = src[ROWS + r];
-              const float wl = l == 0.f ? 0.f : l * ex2_approx(src[r] - M[k]);  // 0: a warp without tokens
-              const float4 y = *reinterpret_cast<const float4*>(src + 2 * ROWS + r * C::OROW + x);
-              L[k] += wl;
-              O[k].x = fmaf(y.x, wl, O[k].x); O[k].y = fmaf(y.y, wl, O[k].y);
-              O[k].z = fmaf(y.z, wl, O[k].z); O[k].w = fmaf(y.w, wl, O[k].w);
-            }
-            const float inv = L[k] == 0.f ? 0.f : 1.f / L[k];
-            O[k].x *= inv; O[k].y *= inv; O[k].z *= inv; O[k].w *= inv;
-          }
-#pragma unroll
-          for (int k = 0; k < AT_ONCE; ++k) {
-            const int w = w0 + 32 * k, r = w / (D / 4), x = w % (D / 4) * 4;
-            if (w >= heads * (D / 4)) break;
-            if (DEAL != SHARES || (starts && ends)) {
-              if (lives) {
-                const int64_t row = static_cast<int64_t>(seg.n) * p.Hq + kvh * G + h0 + r;
-                *reinterpret_cast<uint2*>(p.o + row * D + x) = make_uint2(pack_bf16x2(O[k].x, O[k].y), pack_bf16x2(O[k].z, O[k].w));
-                if (x == 0 && p.lse != nullptr) p.lse[row] = (M[k] + log2f(L[k])) * LN2;
-              }
-            } else {
-              *reinterpret_cast<float4*>(ws.o + (part * ROWS + r) * D + x) = O[k];
-              if (x == 0) {
-                ws.m[part * ROWS + r] = M[k];
-                ws.l[part * ROWS + r] = L[k];
-              }
-            }
-          }
-        }
+        // the last segment's states are merged by the warps that left them
+        if (seg_i + seg_steps < count) merge_states(seg.n, seg.u, starts, ends, lives, lane, 32);
         __syncwarp();
         if (lane == 0) mbar_arrive(rec_free);
         if (starts && !ends && lives) {
@@ -524,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<D, P, DEAL>::THREADS, Cfg<D, P, DEAL>::CTA
   int i = warp;        // share index of this warp's next step
   int stage_k = 0;     // its ring stage: slot warp + NW stage_k ...
   uint32_t phase = 0;  // ... and the parity of that slot's barriers
-  uint32_t free_phase = 0;
+  uint32_t free_phase = 0, seg_index = 0;
   for (int seg = 0; seg < count;) {
     const int seg_n = cur.n, seg_u = cur.u, first_step = cur.step;
     const int seg_steps = cur.ns - first_step < count - seg ? cur.ns - first_step : count - seg;
@@ -768,6 +776,13 @@ __global__ void __launch_bounds__(Cfg<D, P, DEAL>::THREADS, Cfg<D, P, DEAL>::CTA
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(rec_full);
+    if (seg_end == count) {  // nothing is left to do: all warps merge, in a fraction of the time that one takes
+      ok = __all_sync(FULL, mbar_wait(rec_full, seg_index & 1));
+      if (!ok) break;
+      const bool lives = !LISTED || p.cu == nullptr || row_info(p, seg_n).n >= 0;
+      merge_states(seg_n, seg_u, first_step == 0, first_step + seg_steps == cur.ns, lives, warp * 32 + lane, NW * 32);
+    }
+    ++seg_index;
     seg = seg_end;
     if (seg < count) cur.go(seg_steps, p, units);
   }
@@ -806,19 +821,23 @@ cudaError_t launch(const DecodeF8Params& p, cudaStream_t stream) {
   geo.units = p.Hkv * geo.tiles;
   const int64_t pairs = static_cast<int64_t>(rows) * geo.units;
   geo.by_unit = pairs * 8 <= geo.grid;
-  // What the host knows of the lengths is the table's width, or the list's: the most steps that a row and unit can have.
-  // Up to that the shorter ways are no slower, one launch instead of two, and no scan of the lengths.  Measured, us, 32/8
-  // heads, d = 128, equal lengths (SHARES, WHOLE, ALONE):
-  //   8 pairs:   16 tokens 9.5 4.9 5.7, 500 8.9 7.6 7.3, 1000 9.2 10.4 9.3, 2000 9.9 15.7 13.1
-  //   128 pairs: 16 tokens 10.8 5.5 6.4, 1000 14.1 10.7 9.8, 2000 20.4 20.0 16.5, 4000 30.6 34.7 27.1
-  //   512 pairs: 16 tokens 11.2 9.8, 1000 32.0 29.9, 2000 51.8 48.4 (of 100 to 2000: 33.4 34.4); 2048 pairs: 24.4 31.6
-  //   64 listed blocks: 8 pairs 8.5 12.0 10.2, 512 pairs 34.6 34.0.  d = 64, 512 pairs, 1000 tokens: 21.1 22.2
-  const int64_t steps = ((LISTED ? p.K : p.max_blocks) + P - 1) / P;
-  const bool whole = pairs <= 2 * geo.grid && steps <= (D == 64 ? 16 : 64);
-  if (whole && steps <= 8) return start<D, P, LISTED, WHOLE>(p, geo, pairs, stream);
-  if (pairs <= geo.grid / C::CTAS && steps <= (LISTED ? 24 : 33) + pairs / 2)
-    return start<D, P, LISTED, ALONE>(p, geo, pairs, stream);
-  if (whole && pairs > geo.grid / C::CTAS) return start<D, P, LISTED, WHOLE>(p, geo, pairs, stream);
+  // What the host knows of the lengths is the table's width, or the list's: the most pages of a row and unit.  A CTA to each
+  // row and unit takes one launch instead of two, no scan of the lengths and no merge, but where the last round of CTAs is
+  // not a full one the GPU idles for its time: `lost`, in pages.
+  const int64_t pages = LISTED ? p.K : p.max_blocks, steps = (pages + P - 1) / P;
+  const int sms = geo.grid / C::CTAS;
+  auto lost = [&](int64_t ctas) {  // with so many at a time
+    const int64_t places = (pairs + ctas - 1) / ctas * ctas;
+    return pages * (places - pairs) / ctas;
+  };
+  if (pairs <= sms && steps <= 8) return start<D, P, LISTED, WHOLE>(p, geo, pairs, stream);
+  if (pairs <= sms && steps <= (LISTED ? 14 : 33) + pairs / 2) return start<D, P, LISTED, ALONE>(p, geo, pairs, stream);
+  if (LISTED || pages <= 128) {  // a table may be far wider than most of its sequences
+    const int64_t many = sms * Cfg<D, P, MANY>::CTAS, rounds = (pairs + many - 1) / many;
+    if (pairs <= geo.grid && lost(geo.grid) <= (LISTED ? 56 : 45)) return start<D, P, LISTED, WHOLE>(p, geo, pairs, stream);
+    if (pairs > geo.grid && lost(many) <= 45 * (rounds > 2 ? rounds - 1 : 1))
+      return start<D, P, LISTED, MANY>(p, geo, pairs, stream);
+  }
   const cudaError_t e = start<D, P, LISTED, SHARES>(p, geo, geo.grid, stream);
   if (e != cudaSuccess) return e;
   return launch_combine<D, C::TILE>(
