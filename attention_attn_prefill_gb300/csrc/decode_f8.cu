@@ -16,15 +16,16 @@
 // Work: the (sequence, unit, step) list is cut into contiguous shares of equal weight, one a CTA (decode_shares.cuh),
 // or where they are short a CTA takes each row and unit whole; the CTA's computing warps deal its steps among
 // themselves.  One more warp requests the records (one bulk copy each) into the warps' rings, and merges the warps'
-// states of a sequence when all have left it, so that the computing warps never wait for each other.  Where a share's
+// states of a sequence when all have left it, so that the computing warps never wait for each other; the last sequence's
+// states, behind which there is no work to hide the merge, all warps merge.  Where a share's
 // end cuts a sequence, the CTA leaves a partial, which a second kernel, launched as a programmatic dependent, merges.
 // With listed blocks a query token is what a sequence is otherwise, each of its units has the steps that the list's
 // width takes, and the loading warp says how many tokens of each page the query sees.
 //
 // Bound by reading the records.  Measured (GB300, calls in a captured graph, copy rate 6796 GB/s): 64 sequences of 512
-// to 8192, 32/8 heads, d = 128, 98.0 us, 5.85 TB/s; 8 of 6335 to 122863, 16/2 heads, d = 256, 90.9 us, 5.84 TB/s.  The
+// to 8192, 32/8 heads, d = 128, 96.0 us, 5.98 TB/s; 8 of 6335 to 122863, 16/2 heads, d = 256, 86.8 us, 6.11 TB/s.  The
 // kernel itself reads at 6.1 TB/s with 31% of the issue slots used; start, merge and CTAs that end earlier than others
-// are the rest.  64 listed blocks of each row and head, 133 MB: 33.4 us, 4.0 TB/s, two rounds of CTAs of unequal length.
+// are the rest.  64 listed blocks of each row and head, 133 MB: 27.9 us, 4.77 TB/s, a CTA each; 1 sequence of 1009 8.3 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -66,8 +67,8 @@ enum Deal { SHARES, WHOLE, ALONE, MANY };
 // P: pages a warp takes at a step; ROWS / P query heads.
 template <int D, int P, int DEAL>
 struct Cfg {
-  // Warps that compute (one more loads), steps in flight a warp, and CTAs an SM: what shared memory holds.  Measured on 64
-  // sequences of 512 to 8192, 32/8 heads, d = 128, warps x steps x CTAs: 5 x 2 x 2 98.8 us, 3 x 2 x 3 100.4, 4 x 3 x 2
+  // Warps that compute (one more loads), steps in flight a warp, and CTAs an SM: what shared memory holds.  SHARES, measured
+  // on 64 sequences of 512 to 8192, 32/8 heads, d = 128, warps x steps x CTAs: 5 x 2 x 2 98.8 us, 3 x 2 x 3 100.4, 4 x 3 x 2
   // 103.9, 11 x 2 x 1 102.7 (more in flight is no faster), one page a step 7 x 2 x 2 100.6.
   static constexpr int NW = DEAL == ALONE  ? (D == 256 ? 8 : D == 128 && P == 2 ? 11 : 13)
                             : DEAL == MANY ? (D == 256 ? 2 : 3)
@@ -822,8 +823,17 @@ cudaError_t launch(const DecodeF8Params& p, cudaStream_t stream) {
   const int64_t pairs = static_cast<int64_t>(rows) * geo.units;
   geo.by_unit = pairs * 8 <= geo.grid;
   // What the host knows of the lengths is the table's width, or the list's: the most pages of a row and unit.  A CTA to each
-  // row and unit takes one launch instead of two, no scan of the lengths and no merge, but where the last round of CTAs is
-  // not a full one the GPU idles for its time: `lost`, in pages.
+  // row and unit takes one launch instead of two, no scan of the lengths and no merge of partials, but where the last round
+  // of CTAs is not a full one the GPU idles for its time: `lost`, in pages.  Measured, us, d = 128, 32/8 heads, equal lengths
+  // (SHARES, ALONE, WHOLE, MANY):
+  //     8 rows and units: 17 tokens 9.0 5.2 4.4 4.2, 500 8.2 6.7 7.1 7.6, 1000 8.5 8.4 9.8 10.9, 2000 9.1 12.4 15.4 17.8
+  //   128: 100 tokens 8.4 5.6 4.8 5.1, 1000 13.6 8.7 10.0 11.2, 2000 19.9 16.0 19.5 24.9, 64 listed blocks 14.3 10.4 12.2 14.0
+  //   256: 1000 tokens 21.0 19.7 15.6 17.6, 2000 30.7 29.0 25.2 29.0, 64 listed blocks 22.3 22.8 17.4 19.3
+  //   512: 100 tokens 12.5 17.8 9.2 6.7, 1000 31.3 37.7 28.8 25.5, 2000 51.0 56.4 47.4 44.0, of 100 to 2000 32.9 36.3 33.3
+  //        32.6, of 500 to 8000 93.7 98.9 109 113; 64 listed blocks 34.1 44.7 32.4 27.8, 128 54.5 65.8 52.3 47.2
+  //   640: 64 listed blocks 40.2 54.6 45.1 41.7; 896: 50.9 67.7 51.0 49.4, 2000 tokens 80.1 87.5 76.0 79.5;
+  //   1200: 64 listed blocks 63.5 89.3 66.9 57.8; 2400: 1000 tokens 104 142 111 99
+  // and the other head dims and group sizes alike: over 637 cases the rule takes 0.77 of the time of SHARES alone.
   const int64_t pages = LISTED ? p.K : p.max_blocks, steps = (pages + P - 1) / P;
   const int sms = geo.grid / C::CTAS;
   auto lost = [&](int64_t ctas) {  // with so many at a time
@@ -837,6 +847,7 @@ cudaError_t launch(const DecodeF8Params& p, cudaStream_t stream) {
     if (pairs <= geo.grid && lost(geo.grid) <= (LISTED ? 56 : 45)) return start<D, P, LISTED, WHOLE>(p, geo, pairs, stream);
     if (pairs > geo.grid && lost(many) <= 45 * (rounds > 2 ? rounds - 1 : 1))
       return start<D, P, LISTED, MANY>(p, geo, pairs, stream);
+    if (pairs > geo.grid && rounds <= 2 && lost(geo.grid) <= 10) return start<D, P, LISTED, WHOLE>(p, geo, pairs, stream);
   }
   const cudaError_t e = start<D, P, LISTED, SHARES>(p, geo, geo.grid, stream);
   if (e != cudaSuccess) return e;

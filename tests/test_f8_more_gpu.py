@@ -103,6 +103,32 @@ def test_decode_in_many_shares(attn, gpu, lens, Hq, Hkv, d):
             _check_rows(ob[n, rows], lb[n, rows], q[n, rows], k[:, h], v[:, h], d ** -0.5, d)
 
 
+@pytest.mark.parametrize("N,longest,Hq,Hkv,d", [
+    (1, 130, 4, 1, 128), (20, 700, 8, 2, 64), (70, 900, 8, 2, 128), (100, 333, 20, 2, 128), (110, 600, 4, 2, 256),
+    (200, 500, 16, 2, 128), (280, 300, 8, 2, 64), (600, 250, 5, 1, 64), (150, 200, 48, 3, 128), (260, 150, 8, 2, 256),
+    (1300, 60, 4, 1, 128), (900, 64, 6, 1, 256), (449, 1800, 8, 2, 64)])
+def test_decode_dealt_out(attn, gpu, N, longest, Hq, Hkv, d):
+    """Rows and heads on either side of the numbers of CTAs that the device holds, with sequences without tokens between."""
+    lens = [longest] + [0 if n % 5 == 3 else 1 + (n * 7919) % longest for n in range(1, N)]
+    gen, cache, bounds, table = _setup(attn, gpu, lens, Hkv, d, seed=N)
+    q, sl = _randn((N, Hq, d), gen, gpu), _i32(lens, gpu)
+    o, lse = attn.decode_paged_f8(q, cache, table, sl)
+    width = table.shape[1]
+    every = torch.arange(width, dtype=torch.int32, device=gpu).expand(N, Hkv, width).contiguous()
+    ob, lb = attn.decode_blocks_f8(q, cache, table, sl, every)
+    G = Hq // Hkv
+    for n in range(N) if N < 40 else sorted({0, 1, 3, 4, 8, N // 3, N // 2, N - 3, N - 2, N - 1}):
+        if lens[n] == 0:
+            assert not o[n].any() and not ob[n].any() and (lse[n] == -math.inf).all() and (lb[n] == -math.inf).all()
+            continue
+        k, v = (x[0, :lens[n]].double() for x in _values(attn, cache, table[n:n + 1], [lens[n]], gpu))
+        for h in range(Hkv):
+            rows = slice(h * G, (h + 1) * G)
+            _check_rows(o[n, rows], lse[n, rows], q[n, rows], k[:, h], v[:, h], d ** -0.5, d)
+            _check_rows(ob[n, rows], lb[n, rows], q[n, rows], k[:, h], v[:, h], d ** -0.5, d)
+    assert attn.device_status() == 0
+
+
 @pytest.mark.parametrize("N,rows,length,Hq,Hkv,d,K", [
     (3, 1, 9000, 8, 2, 128, 100), (40, 4, 2000, 4, 1, 64, 31), (2, 300, 4000, 16, 2, 128, 9), (700, 1, 40, 2, 1, 256, 2),
     (1, 1, 60000, 5, 1, 128, 999), (5, 7, 3000, 40, 4, 64, 64),
@@ -427,7 +453,8 @@ def _timed(call):
 @pytest.mark.parametrize("listed", [False, True])
 @pytest.mark.parametrize("N,length,Hq,Hkv,d", [(3, 700, 8, 2, 128), (9000, 16, 4, 2, 64), (9000, 16, 5, 1, 128),
                                                (5000, 16, 2, 1, 256), (300, 16, 4, 2, 64), (200, 100, 5, 1, 128),
-                                               (120, 40, 4, 2, 256)])
+                                               (120, 40, 4, 2, 256), (3, 3000, 8, 2, 128), (2, 2500, 5, 1, 64),
+                                               (3, 2500, 4, 1, 256)])
 def test_decode_waits_that_run_out(attn, gpu, waitlib, drop, listed, N, length, Hq, Hkv, d):
     lib = waitlib
     gen, cache, bounds, table = _setup(attn, gpu, [length] * 3, Hkv, d, seed=2)
