@@ -392,10 +392,15 @@ __global__ void __launch_bounds__(FewCfg<D>::MOST_WARPS * 32, 1) score_few_kerne
 }
 
 // ---- more rows: the tensor cores take 128 blocks by RT rows at a time
-template <int D>
+// What shared memory holds, in us: d = 128, 32 sequences of 4000 tokens with 64 rows, 8 KV heads, 36.2 with one CTA an SM and
+// two tiles of 64 rows in flight, 28.9 with two CTAs and one tile of 32 (SMALL); a sequence of 65536 with 2048 rows 113 and
+// 152.  d = 64, 64 rows either way: 26.2 with one CTA, 17.8 with two; 111 and 80.
+template <int D, bool SMALL>
 struct ManyCfg {
-  static constexpr int RT = D == 256 ? 32 : 64;     // rows of a tile
-  static constexpr int STAGES = D == 256 ? 1 : 2;   // row tiles in flight
+  static_assert(!SMALL || D == 128, "the others have one form");
+  static constexpr int RT = D == 256 || SMALL ? 32 : 64;         // rows of a tile
+  static constexpr int STAGES = D == 128 && !SMALL ? 2 : 1;      // row tiles in flight
+  static constexpr int CTAS = D == 64 || SMALL ? 2 : 1;          // an SM
   static constexpr int PANELS = 2 * D / 64;         // 128-byte columns of the 2 d terms
   static constexpr int A_PANEL = 128 * 128, B_PANEL = RT * 128;
   static constexpr int A_BYTES = PANELS * A_PANEL;
@@ -406,6 +411,7 @@ struct ManyCfg {
   static constexpr uint32_t TMEM_COLS = 2 * RT;     // two accumulators
   static constexpr int EPILOGUE = 4, LOADER = 4, ISSUER = 5, WARPS = 6;
 };
+constexpr int SMALL_ROWS = 128;  // rows a sequence up to which the SMALL form may be taken
 constexpr int SUM_ROWS = 16;  // rows a CTA of the kernel that sums the heads takes
 
 // Place of row tile i of a sequence whose first row is `first`, among all tiles' images: no two share one
@@ -413,9 +419,9 @@ __host__ __device__ constexpr int64_t tile_place(int64_t first, int64_t n, int64
 
 // Q-, Q+ of a row and KV head, each as two bf16 numbers, into the image of its row tile: [part][panel][row][128 bytes],
 // as the tensor core reads it from shared memory (16-byte pieces exchanged within 128 bytes, by the row)
-template <int D>
+template <int D, bool SMALL>
 __global__ void __launch_bounds__(SUM_ROWS / 2 * 32) sum_heads_kernel(const SelectBlocksParams p, const Scratch ws, int row_tiles) {
-  using C = ManyCfg<D>;
+  using C = ManyCfg<D, SMALL>;
   const int rt = blockIdx.x % row_tiles, nh = blockIdx.x / row_tiles, n = nh / p.Hkv, h = nh % p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.Hq / p.Hkv;
   // score_many_kernel gathers bounds meanwhile, and waits before it takes the images
@@ -460,11 +466,12 @@ __global__ void __launch_bounds__(SUM_ROWS / 2 * 32) sum_heads_kernel(const Sele
 }
 
 // A CTA takes every `chunks`-th tile of 128 blocks of a sequence and KV head: its bounds are gathered through the block
-// table once and multiplied with one row tile after another, which arrive in bulk copies.
-template <int D>
-__global__ void __launch_bounds__(ManyCfg<D>::WARPS * 32, 1)
-    score_many_kernel(const SelectBlocksParams p, const Scratch ws, int chunks) {
-  using C = ManyCfg<D>;
+// table once and multiplied with one row tile after another, which arrive in bulk copies.  Where there are few tiles of
+// blocks, `splits` CTAs take each, and every splits-th row tile.
+template <int D, bool SMALL>
+__global__ void __launch_bounds__(ManyCfg<D, SMALL>::WARPS * 32, ManyCfg<D, SMALL>::CTAS)
+    score_many_kernel(const SelectBlocksParams p, const Scratch ws, int chunks, int splits) {
+  using C = ManyCfg<D, SMALL>;
   constexpr int RT = C::RT, STAGES = C::STAGES, THREADS = C::WARPS * 32;
   extern __shared__ __align__(1024) uint8_t tiles[];
   __shared__ uint64_t bars[2 * STAGES + 2 * 2 + 1];
@@ -476,7 +483,8 @@ __global__ void __launch_bounds__(ManyCfg<D>::WARPS * 32, 1)
   uint64_t* d_empty = d_full + 2;       // [2]: its scores have been read
   uint64_t* all_done = d_empty + 2;
   const int warp = __shfl_sync(FULL, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int chunk = blockIdx.x % chunks, nh = blockIdx.x / chunks, n = nh / p.Hkv, h = nh % p.Hkv;
+  const int split = blockIdx.x % splits, part = blockIdx.x / splits;
+  const int chunk = part % chunks, nh = part / chunks, n = nh / p.Hkv, h = nh % p.Hkv;
   const Span s = span_of(p, n, false);
   const int rows = s.end - s.first, nb = rows > 0 ? blocks_seen(s, s.end - 1) : 0;
   const bool misaligned = (smem_u32(tiles) & 1023u) != 0;  // swizzled tiles need 1 KB alignment
@@ -538,14 +546,15 @@ __global__ void __launch_bounds__(ManyCfg<D>::WARPS * 32, 1)
     const int least = tile * 128 > p.K ? tile * 128 : p.K;
     int first = 0;
     while (blocks_seen(s, min(s.first + (first + 1) * RT, s.end) - 1) <= least) ++first;
-    const int count = row_tiles - first;
+    // every splits-th of them, the first one for this CTA
+    const int mine = first + split, count = row_tiles > mine ? (row_tiles - mine + splits - 1) / splits : 0;
 
     if (warp == C::LOADER) {
       for (int i = 0; i < count && ok; ++i) {
         const int stage = (done + i) % STAGES;
         ok = wait(&b_empty[stage], ((done + i) / STAGES & 1) ^ 1);
         if (!ok) break;
-        const int rt = first + i, left = rows - rt * RT;
+        const int rt = mine + i * splits, left = rows - rt * RT;
         // eight rows at a time, as the exchange of pieces goes; what lies behind the last row is not looked at
         const uint32_t bytes = (left < RT ? (left + 7) / 8 * 8 : RT) * 128;
         if (lane == 0) mbar_arrive_expect_tx(&b_full[stage], 2 * C::PANELS * bytes);
@@ -604,7 +613,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::WARPS * 32, 1)
       float* staging = reinterpret_cast<float*>(tiles + C::OUT_OFF);
       const int held = ws.stride - tile * 128 < 128 ? static_cast<int>(ws.stride) - tile * 128 : 128;  // a multiple of 8
       for (int i = 0; i < count; ++i) {
-        const int buf = (done + i) & 1, row = (first + i) * RT + r;  // whose scores this thread sends off
+        const int buf = (done + i) & 1, row = (mine + i * splits) * RT + r;  // whose scores this thread sends off
         if (ok) ok = wait(&d_full[buf], (done + i) / 2 & 1);         // after a wait that ran out: none, all the same steps
         tc_fence_after();
         tma_store_wait_read0();
@@ -674,8 +683,11 @@ __device__ __forceinline__ void choose_all(const SelectBlocksParams& p, int64_t 
 }
 
 struct PickShared {
-  __align__(16) int hist[2][BINS];
-  double q[2 * 256];
+  union {
+    __align__(16) int hist[2][BINS];
+    double q[2 * 256];  // the sums over heads, once the bins are done with
+  };
+  int digits[256];
   unsigned long long key[32];
   uint4 red[32];
   float score[32];
@@ -945,7 +957,7 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
     // ---- Many at the border, or none: NaN or infinities, pages that are alike, or no place but the kept ones'.  The
     // border digit by digit, of the scores and then, among those that they leave open, of the exact scores, each computed
     // again for every digit.
-    int* hist = sh.hist[0];
+    int* hist = sh.digits;
     auto digit = [&](int left) {  // the one that holds the left-th largest
       __syncthreads();
       if (threadIdx.x == 0) {
@@ -1265,19 +1277,24 @@ cudaError_t score_few(const SelectBlocksParams& p, const Scratch& ws, int sms, c
   return cudaGetLastError();
 }
 
-template <int D>
-cudaError_t score_many(const SelectBlocksParams& p, const Scratch& ws, cudaStream_t stream) {
-  using C = ManyCfg<D>;
-  const int row_tiles = (p.max_q + SUM_ROWS - 1) / SUM_ROWS;
+template <int D, bool SMALL>
+cudaError_t score_many(const SelectBlocksParams& p, const Scratch& ws, int sms, cudaStream_t stream) {
+  using C = ManyCfg<D, SMALL>;
+  const int sum_tiles = (p.max_q + SUM_ROWS - 1) / SUM_ROWS, row_tiles = (p.max_q + C::RT - 1) / C::RT;
   const int64_t pairs = static_cast<int64_t>(p.N) * p.Hkv;
-  sum_heads_kernel<D><<<static_cast<unsigned>(pairs * row_tiles), SUM_ROWS / 2 * 32, 0, stream>>>(p, ws, row_tiles);
+  sum_heads_kernel<D, SMALL><<<static_cast<unsigned>(pairs * sum_tiles), SUM_ROWS / 2 * 32, 0, stream>>>(p, ws, sum_tiles);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(score_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  auto kern = score_many_kernel<D, SMALL>;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t all = (p.max_blocks + 127) / 128, most = (SCORE_CTAS + pairs - 1) / pairs;
   const int chunks = static_cast<int>(all < most ? all : most);
-  return launch_behind(score_many_kernel<D>, static_cast<unsigned>(pairs * chunks), C::WARPS * 32, C::SMEM, stream, p, ws,
-                       chunks);
+  // where the device holds more CTAs than there are tiles: d = 128, a sequence of 8192 tokens, 8 KV heads, 512 rows 12.7 us
+  // against 19.7, of 16384 tokens with 4096 rows 69.5 against 115.7
+  const int64_t fit = static_cast<int64_t>(sms) * C::CTAS / (pairs * chunks), most_splits = fit < row_tiles ? fit : row_tiles;
+  const int splits = most_splits > 1 ? static_cast<int>(most_splits) : 1;
+  return launch_behind(kern, static_cast<unsigned>(pairs * chunks * splits), C::WARPS * 32, C::SMEM, stream, p, ws, chunks,
+                       splits);
 }
 
 template <int D>
@@ -1296,7 +1313,11 @@ cudaError_t launch(const SelectBlocksParams& p, Scratch& ws, cudaStream_t stream
   // waited for; 2048 of 125 45.0 and 43.2.
   if (p.max_q == 1 && pairs <= 2 * sms && p.max_blocks <= 250 + 8 * pairs) return select_one<D, 256>(p, ws.eps, stream);
   if (p.max_q == 1 && pairs <= 4 * sms && p.max_blocks <= 256) return select_one<D, 128>(p, ws.eps, stream);
-  e = p.max_q <= FEW ? score_few<D>(p, ws, sms, stream) : score_many<D>(p, ws, stream);
+  // few rows and more tiles of blocks than SMs: gathering the bounds counts, and two CTAs an SM overlap that
+  const bool small = D == 128 && p.max_q <= SMALL_ROWS && pairs * ((p.max_blocks + 127) / 128) > sms;
+  e = p.max_q <= FEW ? score_few<D>(p, ws, sms, stream)
+      : small        ? score_many<D, D == 128>(p, ws, sms, stream)
+                     : score_many<D, false>(p, ws, sms, stream);
   if (e != cudaSuccess) return e;
   // Of few long rows the latency of one is to be shortened.  Of many, instructions count, which are fewer the fewer warps
   // do a row's common work: 4096 rows of 2048 blocks take 51 us with 128 threads, 55 with 64, which leave too few warps.
@@ -1316,7 +1337,9 @@ extern "C" int attn_test_drop_copy_select(int what) {
 #endif
 
 size_t select_blocks_workspace_bytes(int64_t T, int64_t N, int64_t max_q, int64_t Hkv, int d, int64_t max_blocks) {
-  const int RT = d == 256 ? ManyCfg<256>::RT : ManyCfg<128>::RT;
+  // (for any number of rows: the SMALL form takes no more)
+  const int RT = d == 256 ? ManyCfg<256, false>::RT : ManyCfg<128, false>::RT;
+  static_assert(ManyCfg<64, false>::RT == ManyCfg<128, false>::RT, "one size for both");
   const int64_t images = max_q <= FEW ? 0 : tile_place(T, N, 1, RT);
   return up256(T * Hkv * score_stride(max_blocks) * 4) + up256(T * Hkv * 4) + up256(N * Hkv * ((max_blocks + 15) / 16) * 4) +
          images * Hkv * RT * 8 * d;
