@@ -101,14 +101,8 @@ __device__ __forceinline__ RowInfo row_info(const DecodeF8Params& p, int r) {
   RowInfo x{r, 0};
   int behind = 0;  // query tokens of the sequence behind this one
   if (p.cu != nullptr) {
-    int lo = 0, hi = p.N;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.cu[mid] <= r) lo = mid;
-      else hi = mid;
-    }
-    const int end = p.cu[lo + 1];
-    x.n = p.cu[lo] <= r && r < end ? lo : -1;
+    const int n = sequence_of(p.cu, p.N, r), end = p.cu[n + 1];
+    x.n = p.cu[n] <= r && r < end ? n : -1;
     behind = end - 1 - r;
   }
   if (x.n >= 0) {

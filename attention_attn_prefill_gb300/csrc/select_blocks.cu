@@ -13,14 +13,14 @@
 // step) are bound by reading the bounds: score_few_kernel.  More (a prompt's chunk) by the products: score_many_kernel,
 // 128 blocks by 64 rows a tcgen05 tile.  Either way
 //   |score - exact| <= eps ||Q|| ||b||,  b = (lo, hi) of a block, by Cauchy and Schwarz on the sum of |terms|.
-// Select kernel: a CTA puts the scores of its row and head into bins over their range, gathers the few in and about the
-// bin that holds the border, and a warp settles the border among them.  Few short sequences of one row each take one
+// Pick: a CTA, or where there are many a warp, puts the scores of its row and head into bins over their range, gathers
+// the few in and about the bin that holds the border, and a warp settles the border among them.  Few short sequences of one row each take one
 // launch, a CTA scoring and picking: select_one_kernel.
 //
 // Measured (GB300, calls in a captured graph, copy rate 6796 GB/s): 64 rows over 512 to 8192 tokens, 32/8 heads, d = 128,
-// 27.4 us, of which the scores' kernel takes about 17 (72 MB of bounds: 10.6 at the copy rate) and the rest is the pick's
-// chain of dependent steps; 8 rows over 6335 to 122863 tokens, 16/2 heads, d = 256, 29.0 (9.8); 512 rows of one
-// sequence of 32768, 32/8 heads, 50.9, of which the pick takes about 25 (4096 rows of 2048 scores), the products 20.
+// 27.4 us, of which the scores take 17.5 (72 MB of bounds: 10.6 at the copy rate) and the pick's chain of dependent steps
+// the rest; 8 rows over 6335 to 122863 tokens, 16/2 heads, d = 256, 29.0 (9.8), of which the scores 16.3; 512 rows of one
+// sequence of 32768, 32/8 heads, 49.6, of which the scores 20.4 (4096 rows of 2048: 33 MB written) and the pick 29.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -43,12 +43,14 @@ __device__ int g_test_drop_copy_select;
 namespace {
 
 using shares::mma_16816;
+using shares::sequence_of;
 
 constexpr uint32_t FULL = 0xffffffffu;
 constexpr int PAGE = 16;
 constexpr int FEW = 4;             // rows a sequence up to which score_few_kernel takes them
 constexpr int BINS = 512;          // of a window of scores
 constexpr int CACHED_BLOCKS = 12288;  // scores of a row that shared memory holds
+constexpr int64_t WARP_ROWS = 1024;   // rows times heads from which on a warp takes each, if its registers hold the scores
 constexpr int NARROW = 1024;       // columns of a block table up to which 128 threads take a row
 // Norms below this count as this: squares of smaller numbers may vanish, and a bound that is too large does no harm
 constexpr float LEAST_NORM = 1e-14f;
@@ -87,16 +89,6 @@ __device__ __forceinline__ Span span_of(const SelectBlocksParams& p, int n, bool
 __device__ __forceinline__ int blocks_seen(const Span& s, int r) {
   const int seen = s.len - (s.end - 1 - r);
   return seen <= 0 ? 0 : (seen + PAGE - 1) / PAGE;
-}
-
-__device__ __forceinline__ int sequence_of(const SelectBlocksParams& p, int r) {
-  int lo = 0, hi = p.N;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.cu[mid] <= r) lo = mid;
-    else hi = mid;
-  }
-  return lo;
 }
 
 __device__ __forceinline__ float2 pair_of(uint32_t w) {
@@ -679,7 +671,7 @@ __host__ __device__ constexpr int cache_at(int max_blocks) { return (2 * ((max_b
 // Every block that a row sees, and -1 behind
 template <int T>
 __device__ __forceinline__ void choose_all(const SelectBlocksParams& p, int64_t at, int nb) {
-  for (int i = threadIdx.x; i < p.K; i += T) p.blocks[at * p.K + i] = i < nb ? i : -1;
+  for (int i = threadIdx.x % T; i < p.K; i += T) p.blocks[at * p.K + i] = i < nb ? i : -1;
 }
 
 struct PickShared {
@@ -702,20 +694,237 @@ struct Row {
   float q_norm, b_norm;  // b_norm: this thread's share of a maximum
 };
 
+// All threads of a row: a warp of a CTA, or a CTA
+template <int T>
+__device__ __forceinline__ void sync_row() {
+  if constexpr (T == 32) __syncwarp();
+  else __syncthreads();
+}
+
+// A bit for each number below n of a word's 32
+__device__ __forceinline__ unsigned below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1; }
+
+// Counts a score within [low, high]: 4 BINS - 1 steps, of which a bin takes four.  Adding 3 2^22 rounds a score's step to the
+// nearest, and leaves it in the sum's last bits.
+__device__ __forceinline__ void count_step(int* hist, float x, float low, float high, float per_step) {
+  if (x >= low && x <= high) {
+    const int step = __float_as_int(fmaf(x - low, per_step, 12582912.f));
+    atomicAdd(&hist[(step & (4 * BINS - 1)) >> 2], 1);
+  }
+}
+// The bin that holds the border, by a warp: lane 0 holds the highest
+__device__ __forceinline__ int border_bin(const int* hist, int over, int want, int lane) {
+  constexpr int PER = BINS / 32;
+  int c[PER], sum = 0, bin = -1;
+#pragma unroll
+  for (int j = 0; j < PER; j += 4) {
+    const int4 x = *reinterpret_cast<const int4*>(hist + BINS - PER * (lane + 1) + j);
+    c[j] = x.x; c[j + 1] = x.y; c[j + 2] = x.z; c[j + 3] = x.w;
+    sum += x.x + x.y + x.z + x.w;
+  }
+  int above = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(FULL, above, o);
+    if (lane >= o) above += x;
+  }
+  above += over - sum;
+#pragma unroll
+  for (int j = PER - 1; j >= 0; --j) {
+    if (above < want && want <= above + c[j]) bin = BINS - PER * (lane + 1) + j;
+    above += c[j];
+  }
+  return __reduce_max_sync(FULL, bin);
+}
+// [low, high] becomes a bin of it, and what is within the twofold error (and a rounding of the bin's ends, 2^-6 of a bin)
+__device__ __forceinline__ void narrow(int bin, float range, float off, float& low, float& high) {
+  const float step = range / (4 * BINS - 1), slack = 2.f * off + step * (1.f / 16);
+  low = low + (4 * bin - 0.5f) * step - slack;
+  high = low + 4.f * step + 2.f * slack;
+}
+
+// The window's blocks, a lane each: those that are sure of one of `places`, and those close to the border
+struct Border {
+  int block, rest;     // this lane's; places that the sure ones leave
+  bool sure, close;
+  unsigned among;      // the close ones' lanes; 0 where they all have a place
+};
+__device__ __forceinline__ Border settle(const PickShared& sh, int open, int places, float off, int lane) {
+  Border b;
+  const bool mine = lane < open;
+  const float x = mine ? sh.score[lane] : -INFINITY;
+  b.block = mine ? sh.at[lane] : 0x7fffffff;
+  int rank = 0;
+  for (int j = 0; j < open; ++j) {
+    const float y = __shfl_sync(FULL, x, j);
+    const int k = __shfl_sync(FULL, b.block, j);
+    rank += y > x || (y == x && k < b.block) ? 1 : 0;
+  }
+  const float border = __shfl_sync(FULL, x, __ffs(__ballot_sync(FULL, mine && rank == places - 1)) - 1);
+  b.sure = mine && x > border + 2.f * off;
+  b.close = mine && !b.sure && x >= border - 2.f * off;
+  b.among = __ballot_sync(FULL, b.close);
+  b.rest = places - __popc(__ballot_sync(FULL, b.sure));
+  if (__popc(b.among) == b.rest) b.among = 0;
+  return b;
+}
+// Whether this lane's block has a place, by the close ones' exact scores
+__device__ __forceinline__ bool takes(const Border& b, unsigned long long key) {
+  int before = 0;  // that go before this one
+  for (unsigned todo = b.among; todo != 0; todo &= todo - 1) {
+    const int j = __ffs(todo) - 1;
+    const unsigned long long y = __shfl_sync(FULL, key, j);
+    const int k = __shfl_sync(FULL, b.block, j);
+    before += y > key || (y == key && k < b.block) ? 1 : 0;
+  }
+  return b.sure || (b.close && before < b.rest);
+}
+
+// hi + lo += x, with what the sum drops
+__device__ __forceinline__ void add_exactly(float& hi, float& lo, float x) {
+  const float s = hi + x, b = s - hi;
+  lo += (hi - (s - b)) + (x - b);
+  hi = s;
+}
+
+// The close blocks' scores to 40 bits, as sums of two floats (Dekker's and Knuth's exact sums and products): 64-bit arithmetic
+// has a hundredth of the rate here, and a warp that settled its row's border by it took 10 to 20 us.  What remains close is
+// left to it.  By a warp: lane l has words 32 k + l of a block's bounds, of which D / 32 there are; norms: ||Q|| times the
+// largest ||b||.  The loads go ahead of the sums: table entries, then the queries, four heads at a time, and the first
+// block's bounds.
+__device__ __forceinline__ void refine(const SelectBlocksParams& p, const Row& row, float norms, Border& at, int lane) {
+  const int D = p.d, G = p.Hq / p.Hkv;
+  int id = 0;
+  if (at.close) id = p.block_table[static_cast<int64_t>(row.n) * p.max_blocks + at.block];
+  if (id < 0 || id >= p.num_blocks) id = 0;
+  uint32_t lo[4], hi[4];  // of channels 2 (32 x + lane) and the next
+  auto load_bounds = [&](int lane_of) {
+    const int64_t page = __shfl_sync(FULL, id, lane_of);
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(p.bounds + (page * p.Hkv + row.h) * 2 * D) + lane;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      lo[x] = 64 * x < D ? from[32 * x] : 0u;
+      hi[x] = 64 * x < D ? from[D / 2 + 32 * x] : 0u;
+    }
+  };
+  const uint32_t* heads = reinterpret_cast<const uint32_t*>(p.q + (static_cast<int64_t>(row.r) * p.Hq + row.h * G) * D) + lane;
+  float neg[4][2][2] = {}, pos[4][2][2] = {};  // sums over heads: [x][channel][first and second float]
+  for (int e0 = 0; e0 < G; e0 += 4) {
+    uint32_t y[4][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) y[e][x] = e0 + e < G && 64 * x < D ? heads[(e0 + e) * (D / 2) + 32 * x] : 0u;
+    if (e0 == 0) load_bounds(__ffs(at.among) - 1);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (64 * x >= D) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 z = pair_of(y[e][x]);
+        add_exactly(neg[x][0][0], neg[x][0][1], fminf(z.x, 0.f));
+        add_exactly(neg[x][1][0], neg[x][1][1], fminf(z.y, 0.f));
+        add_exactly(pos[x][0][0], pos[x][0][1], fmaxf(z.x, 0.f));
+        add_exactly(pos[x][1][0], pos[x][1][1], fmaxf(z.y, 0.f));
+      }
+    }
+  }
+  float s = 0.f, t = 0.f;  // this lane's block's score
+  for (unsigned todo = at.among; todo != 0;) {
+    const int j = __ffs(todo) - 1;
+    todo &= todo - 1;
+    float a = 0.f, b = 0.f;
+    auto add = [&](const float (&q)[2], float k) {
+      const float product = q[0] * k;
+      b += fmaf(q[1], k, fmaf(q[0], k, -product));
+      add_exactly(a, b, product);
+    };
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (64 * x >= D) continue;
+      const float2 l = pair_of(lo[x]), h = pair_of(hi[x]);
+      add(neg[x][0], l.x);
+      add(neg[x][1], l.y);
+      add(pos[x][0], h.x);
+      add(pos[x][1], h.y);
+    }
+    if (todo != 0) load_bounds(__ffs(todo) - 1);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float other = __shfl_xor_sync(FULL, a, o);
+      b += __shfl_xor_sync(FULL, b, o);
+      add_exactly(a, b, other);
+    }
+    if (lane == j) {
+      s = a + b;
+      t = b - (s - a);
+    }
+  }
+  // ordered by the first float, then by the second: the first is the sum rounded
+  const unsigned long long key = static_cast<unsigned long long>(order_of(s)) << 32 | order_of(t);
+  int before = 0;
+  for (unsigned todo = at.among; todo != 0; todo &= todo - 1) {
+    const int j = __ffs(todo) - 1;
+    const unsigned long long y = __shfl_sync(FULL, key, j);
+    const int k = __shfl_sync(FULL, at.block, j);
+    before += y > key || (y == key && k < at.block) ? 1 : 0;
+  }
+  const int border = __ffs(__ballot_sync(FULL, at.close && before == at.rest - 1)) - 1;
+  const float above = (s - __shfl_sync(FULL, s, border)) + (t - __shfl_sync(FULL, t, border));
+  // 18 additions of errors and G of the queries', each within 2^-24 of 2^-24 of the terms' sum, and a sum of 18 of them
+  const float off = norms * (1.f / (1ull << 38) + static_cast<float>(G) / (1ull << 46));
+  const bool sure = at.close && above > 2.f * off, close = at.close && !sure && above >= -2.f * off;
+  at.sure = at.sure || sure;
+  at.close = close;
+  at.among = __ballot_sync(FULL, close);
+  at.rest -= __popc(__ballot_sync(FULL, sure));
+  if (__popc(at.among) == at.rest) at.among = 0;
+}
+
+// The close blocks' scores in 64 bits, this lane's block's; of pages that are alike, mostly
+__device__ __noinline__ unsigned long long exact_keys(const SelectBlocksParams& p, int r, int h, int n, int block, unsigned among,
+                                                      int lane) {
+  const int D = p.d, G = p.Hq / p.Hkv;
+  const uint32_t* heads = reinterpret_cast<const uint32_t*>(p.q + (static_cast<int64_t>(r) * p.Hq + h * G) * D);
+  unsigned long long key = 0;
+  for (unsigned todo = among; todo != 0; todo &= todo - 1) {
+    const int j = __ffs(todo) - 1;
+    int id = p.block_table[static_cast<int64_t>(n) * p.max_blocks + __shfl_sync(FULL, block, j)];
+    if (id < 0 || id >= p.num_blocks) id = 0;
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(p.bounds + (static_cast<int64_t>(id) * p.Hkv + h) * 2 * D);
+    double sum = 0.0;
+    for (int w = lane; w < D; w += 32) {  // terms 2 w and 2 w + 1 of the 2 d
+      const bool low = 2 * w < D;
+      double q[2] = {0.0, 0.0};
+      for (int g = 0; g < G; ++g) {
+        const float2 z = pair_of(heads[g * (D / 2) + (low ? w : w - D / 2)]);
+        q[0] += low ? fminf(z.x, 0.f) : fmaxf(z.x, 0.f);
+        q[1] += low ? fminf(z.y, 0.f) : fmaxf(z.y, 0.f);
+      }
+      const float2 k = pair_of(from[w]);
+      sum = fma(q[0], static_cast<double>(k.x), fma(q[1], static_cast<double>(k.y), sum));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+    if (lane == j) key = order_of(sum);
+  }
+  return key;
+}
+
 // Picks the blocks of a row and KV head, by a CTA of T threads.  CACHED: shared memory holds its scores, else they are read
 // again and again.  s_bits: [words] chosen blocks, [words] ties; the scores from word cache_at on.
 template <int T, bool CACHED>
 __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row, float eps, PickShared& sh, uint32_t* s_bits) {
   constexpr int NW = T / 32;
   const int D = p.d, nb = row.nb, K = p.K, r = row.r, h = row.h, n = row.n;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = T == 32 ? threadIdx.x & 31 : threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int32_t* out = p.blocks + (static_cast<int64_t>(r) * p.Hkv + h) * K;
   const int c0 = p.first, c1 = nb - p.last;  // the blocks that compete
   const int want = K - p.first - p.last;     // for so many places: fewer than they are
   const int words = (nb + 31) / 32;
   uint32_t* ties = s_bits + words;
-  for (int i = threadIdx.x; i < BINS / 4; i += T) reinterpret_cast<int4*>(sh.hist[0])[i] = make_int4(0, 0, 0, 0);
-  if (threadIdx.x < 2) sh.open[threadIdx.x] = sh.over[threadIdx.x] = 0;
+  for (int i = tid; i < BINS / 4; i += T) reinterpret_cast<int4*>(sh.hist[0])[i] = make_int4(0, 0, 0, 0);
+  if (tid < 2) sh.open[tid] = sh.over[tid] = 0;
 
   // ---- how far a score may be off, and the scores' range
   const float* sc = row.scores;
@@ -745,7 +954,7 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
   float low = INFINITY, high = -INFINITY, off;
   {
 #pragma unroll 2
-    for (int v = threadIdx.x; 4 * v < (CACHED ? 32 * words : nb); v += T) {
+    for (int v = tid; 4 * v < (CACHED ? 32 * words : nb); v += T) {
       const float4 x = 4 * v < nb ? read_four(v) : make_float4(none, none, none, none);
       if constexpr (CACHED) *reinterpret_cast<float4*>(cache + 4 * v) = x;
       low = fminf(fminf(low, fminf(x.x, x.y)), fminf(x.z, x.w));
@@ -754,7 +963,7 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
     uint32_t most = __reduce_max_sync(FULL, __float_as_uint(row.b_norm));  // norms by their bits
     uint32_t least = __reduce_min_sync(FULL, order_of(low)), top = __reduce_max_sync(FULL, order_of(high));
     if (lane == 0) sh.red[warp] = make_uint4(most, least, top, 0);
-    __syncthreads();
+    sync_row<T>();
     const uint4 x = sh.red[lane % NW];
     most = __reduce_max_sync(FULL, x.x);
     least = __reduce_min_sync(FULL, x.y);
@@ -817,57 +1026,26 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
   int open = 0, over = 0;  // in the window; above it
   for (int round = 0; known && want > 0 && !few; ++round) {
     int* hist = sh.hist[round & 1];
-    // 4 BINS - 1 steps, of which a bin takes four: a score's, rounded to the nearest by adding 3 2^22, is in the sum's last bits
     const float range = high - low, per_step = (4 * BINS - 1) / range;
     if (!(range < INFINITY && per_step < INFINITY)) break;  // all alike, or past float32
-    auto count = [&](float x) {
-      if (x >= low && x <= high) {
-        const int step = __float_as_int(fmaf(x - low, per_step, 12582912.f));
-        atomicAdd(&hist[(step & (4 * BINS - 1)) >> 2], 1);
-      }
-    };
-    for (int v = threadIdx.x; 4 * v < nb; v += T) {
+    auto count = [&](float x) { count_step(hist, x, low, high, per_step); };
+    for (int v = tid; 4 * v < nb; v += T) {
       const float4 x = four(v);
       count(x.x);
       count(x.y);
       count(x.z);
       count(x.w);
     }
-    __syncthreads();
+    sync_row<T>();
     // a warp finds the bin of the border, each for itself where they are few: lane 0 holds the highest
     int bin = -1;
-    if (NW <= 8 || warp == 0) {
-      constexpr int PER = BINS / 32;
-      int c[PER], sum = 0;
-#pragma unroll
-      for (int j = 0; j < PER; j += 4) {
-        const int4 x = *reinterpret_cast<const int4*>(hist + BINS - PER * (lane + 1) + j);
-        c[j] = x.x; c[j + 1] = x.y; c[j + 2] = x.z; c[j + 3] = x.w;
-        sum += x.x + x.y + x.z + x.w;
-      }
-      int above = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(FULL, above, o);
-        if (lane >= o) above += x;
-      }
-      above += over - sum;
-#pragma unroll
-      for (int j = PER - 1; j >= 0; --j) {
-        if (above < want && want <= above + c[j]) bin = BINS - PER * (lane + 1) + j;
-        above += c[j];
-      }
-      bin = __reduce_max_sync(FULL, bin);
-    }
+    if (NW <= 8 || warp == 0) bin = border_bin(hist, over, want, lane);
     if constexpr (NW > 8) {
-      if (threadIdx.x == 0) sh.digit = bin;
-      __syncthreads();
+      if (tid == 0) sh.digit = bin;
+      sync_row<T>();
       bin = sh.digit;
     }
-    // its blocks, and those within the twofold error (and a rounding of the bin's ends, 2^-6 of a bin) of it
-    const float step = range / (4 * BINS - 1), slack = 2.f * off + step * (1.f / 16);
-    low = low + (4 * bin - 0.5f) * step - slack;
-    high = low + 4.f * step + 2.f * slack;
+    narrow(bin, range, off, low, high);
     int above_high = 0;
     for (int w = warp; w < words; w += NW) {
       const float x = score(32 * w + lane);
@@ -884,74 +1062,48 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
       if (lane == 0) s_bits[w] = bits;
     }
     if (lane == 0 && above_high > 0) atomicAdd(&sh.over[round & 1], above_high);
-    __syncthreads();
+    sync_row<T>();
     open = sh.open[round & 1];
     over = sh.over[round & 1];
     few = open <= 32;
     if (!few) {
       if (!(high - low < 0.5f * range)) break;  // the error's width: they may as well be alike
       const int other = (round & 1) ^ 1;
-      for (int i = threadIdx.x; i < BINS; i += T) sh.hist[other][i] = 0;
-      __syncthreads();
-      if (threadIdx.x == 0) sh.open[round & 1] = sh.over[round & 1] = 0;
+      for (int i = tid; i < BINS; i += T) sh.hist[other][i] = 0;
+      sync_row<T>();
+      if (tid == 0) sh.open[round & 1] = sh.over[round & 1] = 0;
     }
   }
 
   if (few) {
     // ---- a warp settles it, a lane a block
     const int places = want - over;  // 1 <= places <= open
-    for (int i = threadIdx.x; i < p.first + p.last; i += T) choose(i < p.first ? i : nb - p.last + i - p.first);
-    bool sure = false, close = false;
-    int i = 0x7fffffff, rest = 0;
-    unsigned among = 0;
+    for (int i = tid; i < p.first + p.last; i += T) choose(i < p.first ? i : nb - p.last + i - p.first);
+    Border at;
     if (warp == 0) {
-      const bool mine = lane < open;
-      const float x = mine ? sh.score[lane] : -INFINITY;
-      if (mine) i = sh.at[lane];
-      int rank = 0;
-      for (int j = 0; j < open; ++j) {
-        const float y = __shfl_sync(FULL, x, j);
-        const int k = __shfl_sync(FULL, i, j);
-        rank += y > x || (y == x && k < i) ? 1 : 0;
-      }
-      const float border = __shfl_sync(FULL, x, __ffs(__ballot_sync(FULL, mine && rank == places - 1)) - 1);
-      sure = mine && x > border + 2.f * off;
-      close = mine && !sure && x >= border - 2.f * off;
-      among = __ballot_sync(FULL, close);
-      rest = places - __popc(__ballot_sync(FULL, sure));
-      const bool all = __popc(among) == rest;
-      if (lane == 0) sh.among = all || off == 0.f ? 0u : among;
-      if (all && (sure || close)) choose(i);
-      close = close && !all;
-      sure = sure && !all;
-      if (all) among = 0;
+      at = settle(sh, open, places, off, lane);
+      if (lane == 0) sh.among = off == 0.f ? 0u : at.among;
+      if (at.among == 0 && (at.sure || at.close)) choose(at.block);
     }
-    __syncthreads();
+    sync_row<T>();
     if (sh.among != 0) {  // by the exact scores, a warp a block; the first one's bounds come while the heads are summed
       unsigned todo = sh.among;
       for (int k = 0; k < warp && todo != 0; ++k) todo &= todo - 1;
       uint32_t b[8];
       if (todo != 0) load_bounds(sh.at[__ffs(todo) - 1], b);
-      sum_heads(threadIdx.x, T);
-      __syncthreads();
+      sum_heads(tid, T);
+      sync_row<T>();
       for (bool first = true; todo != 0; first = false) {
         const int j = __ffs(todo) - 1;
         const unsigned long long key = first ? product(b) : exact(sh.at[j]);
         if (lane == 0) sh.key[j] = key;
         for (int k = 0; k < NW && todo != 0; ++k) todo &= todo - 1;
       }
-      __syncthreads();
+      sync_row<T>();
     }
-    if (among != 0) {
-      const unsigned long long key = close && off != 0.f ? sh.key[lane] : 0ull;  // where the bound is 0 every score is
-      int before = 0;  // that go before this one
-      for (unsigned todo = among; todo != 0; todo &= todo - 1) {
-        const int j = __ffs(todo) - 1;
-        const unsigned long long y = __shfl_sync(FULL, key, j);
-        const int k = __shfl_sync(FULL, i, j);
-        before += y > key || (y == key && k < i) ? 1 : 0;
-      }
-      if (sure || (close && before < rest)) choose(i);
+    if (warp == 0 && at.among != 0) {
+      const unsigned long long key = at.close && off != 0.f ? sh.key[lane] : 0ull;  // where the bound is 0 every score is
+      if (takes(at, key)) choose(at.block);
     }
   } else {
     // ---- Many at the border, or none: NaN or infinities, pages that are alike, or no place but the kept ones'.  The
@@ -959,19 +1111,19 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
     // again for every digit.
     int* hist = sh.digits;
     auto digit = [&](int left) {  // the one that holds the left-th largest
-      __syncthreads();
-      if (threadIdx.x == 0) {
+      sync_row<T>();
+      if (tid == 0) {
         int above = 0, at = 255;
         while (at > 0 && above + hist[at] < left) above += hist[at--];
         sh.digit = at;
         sh.above = above;
       }
-      __syncthreads();
+      sync_row<T>();
     };
     auto clear = [&]() {
-      __syncthreads();
-      for (int i = threadIdx.x; i < 256; i += T) hist[i] = 0;
-      __syncthreads();
+      sync_row<T>();
+      for (int i = tid; i < 256; i += T) hist[i] = 0;
+      sync_row<T>();
     };
     uint32_t border = 0;
     if (known && want > 0) {
@@ -979,7 +1131,7 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
       int left = want;
       for (int shift = 24; shift >= 0; shift -= 8) {
         clear();
-        for (int i = c0 + threadIdx.x; i < c1; i += T) {
+        for (int i = c0 + tid; i < c1; i += T) {
           const uint32_t u = order_of(score(i));
           if (((u ^ border) & mask) == 0) atomicAdd(&hist[u >> shift & 255], 1);
         }
@@ -991,9 +1143,9 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
     }
     const float at = from_order(border), most = known ? at + 2.f * off : INFINITY, least = known ? at - 2.f * off : -INFINITY;
     auto undecided = [&](int i) { return want > 0 && i >= c0 && i < c1 && (!known || (score(i) <= most && score(i) >= least)); };
-    __syncthreads();
-    if (threadIdx.x == 0) sh.open[0] = sh.over[0] = 0;
-    __syncthreads();
+    sync_row<T>();
+    if (tid == 0) sh.open[0] = sh.over[0] = 0;
+    sync_row<T>();
     int ins = 0, opens = 0;
     for (int w = warp; w < words; w += NW) {
       const int i = 32 * w + lane;
@@ -1007,13 +1159,13 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
       atomicAdd(&sh.over[0], ins);
       atomicAdd(&sh.open[0], opens);
     }
-    __syncthreads();
+    sync_row<T>();
     const int places = want - sh.over[0];
     const bool score_again = places < sh.open[0] && !(known && off == 0.f);  // with a bound of 0 every score is 0
     unsigned long long key_at = 0, mask = 0;
     int left = places;
     if (score_again) {
-      sum_heads(threadIdx.x, T);
+      sum_heads(tid, T);
       for (int shift = 56; shift >= 0; shift -= 8) {
         clear();
         for (int w = warp; w < words; w += NW)
@@ -1043,7 +1195,7 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
         ties[w] = tie;
       }
     }
-    __syncthreads();
+    sync_row<T>();
     if (warp == 0)  // the lowest of those that tie
       for (int w = 0; w < words && left > 0; ++w) {
         unsigned tie = ties[w];
@@ -1052,7 +1204,7 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
         if (lane == 0) s_bits[w] |= tie;
       }
   }
-  __syncthreads();
+  sync_row<T>();
 
   // ---- in ascending order: every warp counts, each takes the words, a lane a word, of every NW-th group of 32
   int base = 0;
@@ -1076,6 +1228,136 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
   }
 }
 
+// The same by a warp that holds the scores in registers, 32 NR at most; `sc` may be shared memory.  False, and nothing done,
+// where there is more to it: NaN or infinities, many alike at the border, or no place but the kept blocks'.
+template <int NR>
+__device__ __forceinline__ bool pick_warp(const SelectBlocksParams& p, const Row& row, const float* sc, float eps, PickShared& sh) {
+  constexpr int NW = (NR + 31) / 32;  // words of chosen blocks a lane: word 32 k + lane
+  const int lane = threadIdx.x & 31, nb = row.nb, c0 = p.first, c1 = nb - p.last, want = p.K - p.first - p.last;
+  if (want == 0) return false;
+  const float none = __uint_as_float(0x7fffffffu);  // a NaN: neither above, below nor within a window
+  float x[NR], low = INFINITY, high = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    x[j] = none;
+    if (32 * j < nb && static_cast<unsigned>(32 * j + lane - c0) < static_cast<unsigned>(c1 - c0)) x[j] = sc[32 * j + lane];
+  }
+  int* hist = sh.hist[0];
+  auto clear = [&]() {
+#pragma unroll
+    for (int k = 0; k < BINS / 128; ++k) reinterpret_cast<int4*>(hist)[32 * k + lane] = make_int4(0, 0, 0, 0);
+    __syncwarp();
+  };
+  clear();
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    low = fminf(low, x[j]);
+    high = fmaxf(high, x[j]);
+  }
+  low = from_order(__reduce_min_sync(FULL, order_of(low)));
+  high = from_order(__reduce_max_sync(FULL, order_of(high)));
+  const float off = eps * row.q_norm * __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(row.b_norm)));
+  if (!(off < INFINITY)) return false;
+  unsigned bits[NW];
+  int open = 0, over = 0;  // in the window; above it
+  for (;;) {
+    const float range = high - low, per_step = (4 * BINS - 1) / range;
+    if (!(range < INFINITY && per_step < INFINITY)) return false;
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+      if (32 * j < nb) count_step(hist, x[j], low, high, per_step);
+    __syncwarp();
+    narrow(border_bin(hist, over, want, lane), range, off, low, high);
+    open = over = 0;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) bits[k] = 0;
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+      if (32 * j >= nb) continue;
+      const bool above = x[j] > high, in = x[j] >= low && !above;
+      const unsigned word = __ballot_sync(FULL, above), ins = __ballot_sync(FULL, in);
+      if (lane == j % 32) bits[j / 32] = word;
+      over += __popc(word);
+      if (ins == 0) continue;
+      const int k = open + __popc(ins & ((1u << lane) - 1));
+      if (in && k < 32) {
+        sh.at[k] = 32 * j + lane;
+        sh.score[k] = x[j];
+      }
+      open += __popc(ins);
+    }
+    __syncwarp();
+    if (open <= 32) break;
+    if (!(high - low < 0.5f * range)) return false;  // the error's width: they may as well be alike
+    clear();
+  }
+  Border at = settle(sh, open, want - over, off, lane);
+  if (at.among != 0 && off != 0.f) refine(p, row, off / eps, at, lane);
+  bool chosen = at.sure || at.close;
+  if (at.among != 0) {
+    // where the bound is 0 every score is
+    const unsigned long long key = off != 0.f ? exact_keys(p, row.r, row.h, row.n, at.block, at.among, lane) : 0ull;
+    chosen = takes(at, key);
+  }
+  for (unsigned todo = __ballot_sync(FULL, chosen); todo != 0; todo &= todo - 1) {
+    const int block = __shfl_sync(FULL, at.block, __ffs(todo) - 1);
+#pragma unroll
+    for (int k = 0; k < NW; ++k)
+      if (block >> 5 == 32 * k + lane) bits[k] |= 1u << (block & 31);
+  }
+  int32_t* out = p.blocks + (static_cast<int64_t>(row.r) * p.Hkv + row.h) * p.K;
+  int base = 0;
+#pragma unroll
+  for (int k = 0; k < NW; ++k) {
+    const int b0 = 32 * (32 * k + lane);  // the word's first block; the kept ones are those outside [c0, c1)
+    unsigned word = bits[k] | ~below(c1 - b0) | below(c0 - b0);
+    word &= below(nb - b0);
+    int upto = __popc(word), place = base - upto;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(FULL, upto, o);
+      if (lane >= o) upto += y;
+    }
+    place += upto;
+    base += __shfl_sync(FULL, upto, 31);
+    for (; word != 0; word &= word - 1, ++place)
+      if (place < p.K) out[place] = b0 + __ffs(word) - 1;
+  }
+  return true;
+}
+
+// A warp a row and KV head, four a CTA
+template <int NR>
+__global__ void __launch_bounds__(128, NR == 16 ? 6 : NR == 32 ? 5 : 4) select_warps_kernel(const SelectBlocksParams p, const Scratch ws) {
+  extern __shared__ __align__(16) uint32_t s_words[];
+  __shared__ PickShared shared[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + warp;
+  const bool beyond = at >= static_cast<int64_t>(p.T) * p.Hkv;
+  if (beyond) at = 0;
+  Row row;
+  row.r = static_cast<int>(at / p.Hkv);
+  row.h = static_cast<int>(at - static_cast<int64_t>(row.r) * p.Hkv);
+  row.n = p.cu == nullptr ? row.r : sequence_of(p.cu, p.N, row.r);
+  const Span s = span_of(p, row.n, false);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores are there
+  if (beyond || row.r < s.first || row.r >= s.end) return;  // of no sequence: left as it was
+  row.nb = blocks_seen(s, row.r);
+  if (row.nb <= p.K) {
+    choose_all<32>(p, at, row.nb);
+    return;
+  }
+  const float* norms = ws.b_norm + (static_cast<int64_t>(row.n) * p.Hkv + row.h) * ws.tiles;
+  row.q_norm = ws.q_norm[at];
+  row.b_norm = 0.f;
+#pragma unroll
+  for (int k = 0; k < (NR * 2 + 31) / 32; ++k)
+    if (32 * k + lane < (row.nb + 15) / 16) row.b_norm = fmaxf(row.b_norm, norms[32 * k + lane]);
+  row.scores = ws.scores + at * ws.stride;
+  if (!pick_warp<NR>(p, row, row.scores, ws.eps, shared[warp]))
+    pick<32, false>(p, row, ws.eps, shared[warp], s_words + warp * cache_at(p.max_blocks));
+}
+
 template <int T, bool CACHED>
 __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const SelectBlocksParams p, const Scratch ws) {
   extern __shared__ __align__(16) uint32_t s_bits[];
@@ -1083,7 +1365,7 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
   Row row;
   row.r = blockIdx.x / p.Hkv;
   row.h = blockIdx.x % p.Hkv;
-  row.n = p.cu == nullptr ? row.r : sequence_of(p, row.r);
+  row.n = p.cu == nullptr ? row.r : sequence_of(p.cu, p.N, row.r);
   const Span s = span_of(p, row.n, false);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores are there
   if (row.r < s.first || row.r >= s.end) return;       // of no sequence: left as it was
@@ -1258,6 +1540,13 @@ cudaError_t select(const SelectBlocksParams& p, const Scratch& ws, cudaStream_t 
                        ws);
 }
 
+template <int NR>
+cudaError_t select_warps(const SelectBlocksParams& p, const Scratch& ws, cudaStream_t stream) {
+  const int smem = 4 * cache_at(p.max_blocks) * 4;
+  return launch_behind(select_warps_kernel<NR>, static_cast<unsigned>((static_cast<int64_t>(p.T) * p.Hkv + 3) / 4), 128, smem,
+                       stream, p, ws);
+}
+
 template <int D, int T>
 cudaError_t select_one(const SelectBlocksParams& p, float eps, cudaStream_t stream) {
   const int smem = (cache_at(p.max_blocks) + (p.max_blocks + 31) / 32 * 32) * 4;
@@ -1323,6 +1612,17 @@ cudaError_t launch(const SelectBlocksParams& p, Scratch& ws, cudaStream_t stream
   // do a row's common work: 4096 rows of 2048 blocks take 51 us with 128 threads, 55 with 64, which leave too few warps.
   // The whole call with 128 and with 1024 threads, d = 64: 128 rows of 2500 blocks 31.9 and 26.0 us, 256 47.6 and 46.1, 512
   // 80.8 and 89.3, 800 112 and 132; of 8125 128 71.8 and 59.3, 256 122.3 and 116.6, 512 220.8 and 228.2, 800 346 and 352.
+  // A warp a row, its scores in registers, has no barriers and does a row's common work once; a CTA a row has more rows'
+  // latencies under way where they are few.  Warp and CTA, us, d = 128: 16384 rows of 250 blocks 65 and 96, of 500 63 and 92,
+  // 32768 of 1000 160 and 220, 16384 of 2000 166 and 170; 1024 of 500 16.0 and 17.6, of 1000 18.7 and 20.7; decode steps of
+  // 2048 rows and heads, 500 108 and 111, 2000 361 and 366; 512, 500 39.4 and 38.1; 64, 1000 18.1 and 19.0, 2000 26.5 and 21.6
+  if (static_cast<int64_t>(p.T) * p.Hkv >= WARP_ROWS) {
+    if (p.max_blocks <= 512) return select_warps<16>(p, ws, stream);
+    if (p.max_blocks <= 1024) return select_warps<32>(p, ws, stream);
+    if (p.max_blocks <= 1536) return select_warps<48>(p, ws, stream);
+    if (p.max_blocks <= 2048) return select_warps<64>(p, ws, stream);
+    if (p.max_blocks <= 2560) return select_warps<80>(p, ws, stream);
+  }
   if (p.max_blocks > CACHED_BLOCKS) return select<1024, false>(p, ws, stream);
   const bool many = static_cast<int64_t>(p.T) * p.Hkv > 2 * sms;  // more than 1024 threads each can take at once
   return many || p.max_blocks <= NARROW ? select<128, true>(p, ws, stream) : select<1024, true>(p, ws, stream);

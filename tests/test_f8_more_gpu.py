@@ -273,6 +273,51 @@ def test_select_of_one_row_each(attn, gpu, N, Hkv, d, width):
     assert attn.device_status() == 0
 
 
+@pytest.mark.parametrize("rows,Hq,Hkv,d,width,K", [
+    (700, 4, 2, 128, 60, 9), (1100, 3, 1, 64, 512, 40), (600, 8, 2, 256, 513, 33), (520, 4, 2, 128, 1024, 64),
+    (400, 3, 3, 64, 1300, 700), (350, 15, 3, 128, 1850, 5), (260, 8, 4, 128, 2560, 90), (1050, 2, 1, 256, 2561, 20)])
+@pytest.mark.parametrize("kind", ["plain", "far", "alike", "close", "odd"])
+def test_select_of_many_rows(attn, gpu, rows, Hq, Hkv, d, width, K, kind):
+    """As many rows and heads as are taken a warp each.  far: a few pages are far above all others; alike: a third of the pages
+    are copies of one, whose scores tie; close: those copies differ in a channel that adds a part in 10^11 to 10^13 to
+    the scores, which 64 bits (a part in 10^16, 512 additions) resolve; odd: bounds that are infinite or no number, queries of zeros and infinities."""
+    gen = torch.Generator(device=gpu).manual_seed(rows + width)
+    parts = [rows - 90, 0, 90]
+    lens, cu = [16 * width - 5, 30, 16 * (width // 2)], [0, rows - 90, rows - 90, rows]
+    first, last = 1, 2
+    blocks = width + 7
+    b = torch.randn((blocks, Hkv, 2, d), generator=gen, device=gpu).sort(2).values
+    if kind == "far":
+        b[torch.randperm(blocks, generator=gen, device=gpu)[:3]] *= 1e4
+    b = b.to(torch.bfloat16)
+    if kind in ("alike", "close"):
+        copies = torch.rand(blocks, generator=gen, device=gpu) < 0.34
+        b[copies] = b[0].clone()
+        if kind == "close":
+            b[copies, :, :, 7] = torch.randn((int(copies.sum()), Hkv, 1), generator=gen, device=gpu).to(torch.bfloat16)
+    table = torch.stack([torch.randperm(blocks, generator=gen, device=gpu)[:width] for _ in lens]).to(torch.int32)
+    q = _randn((rows, Hq, d), gen, gpu)
+    some = sorted({0, 1, 17, rows // 3, rows - 91, rows - 90, rows - 2, rows - 1})
+    if kind == "close":
+        q[:, :, 7] = q[:, :, 7].abs().clamp(min=0.1) * 1e-10
+    if kind == "odd":
+        q[:, :, 3] = q[:, :, 3].abs().clamp(min=0.5)
+        b[2, :, 1, 3], b[5, :, 1, 3] = math.inf, math.nan
+        q[17], q[rows - 2, 0, 5] = 0, math.inf
+    got = attn.select_blocks(q, b, table, _i32(lens, gpu), K, first=first, last=last, cu_seqlens_q=_i32(cu, gpu),
+                             max_seqlen_q=rows - 90)
+    assert attn.device_status() == 0
+    for r in some:
+        n = 0 if r < rows - 90 else 2
+        want = _wanted_odd(q[r:r + 1], b, table[n:n + 1], lens[n] - (cu[n + 1] - 1 - r), K, first, last)
+        assert torch.equal(got[r], want), r
+    nb = torch.tensor([_pages(lens[0 if r < rows - 90 else 2] - (cu[1 if r < rows - 90 else 3] - 1 - r)) for r in range(rows)],
+                      device=gpu)[:, None, None]
+    assert ((got >= 0).sum(-1, keepdim=True) == nb.clamp(max=K)).all() and (got < nb).all()
+    full = got[(nb > K).flatten()]
+    assert (full[..., 1:] > full[..., :-1]).all()
+
+
 def _wanted_odd(q, bounds, table, length, K, first, last):
     """_wanted for one row, with NaN above all other scores."""
     nb = _pages(length)
