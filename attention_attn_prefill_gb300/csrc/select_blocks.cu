@@ -1161,7 +1161,45 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
     }
     sync_row<T>();
     const int places = want - sh.over[0];
-    const bool score_again = places < sh.open[0] && !(known && off == 0.f);  // with a bound of 0 every score is 0
+    bool score_again = places < sh.open[0] && !(known && off == 0.f);  // with a bound of 0 every score is 0
+    if (score_again) {
+      // Pages with the same bounds have the same score, and a cache that nothing was written to has no others: 512 rows of
+      // 2048 such pages, 8 heads, took 126 ms by exact scores.
+      if (tid == 0) sh.among = 0;
+      sync_row<T>();
+      const uint32_t* bounds = reinterpret_cast<const uint32_t*>(p.bounds);
+      auto page_of = [&](int i) {
+        int id = p.block_table[static_cast<int64_t>(n) * p.max_blocks + i];
+        if (id < 0 || id >= p.num_blocks) id = 0;
+        return id;
+      };
+      int first = -1;  // the lowest of them
+      for (int w = 0; first < 0; ++w) {
+        const unsigned todo = __ballot_sync(FULL, undecided(32 * w + lane));
+        if (todo != 0) first = page_of(32 * w + __ffs(todo) - 1);
+      }
+      uint32_t like[8], differs = 0;
+      auto words_of = [&](int page, uint32_t (&x)[8]) {
+        const uint32_t* from = bounds + (static_cast<int64_t>(page) * p.Hkv + h) * D + lane;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = 32 * k < D ? from[32 * k] : 0u;
+      };
+      words_of(first, like);
+      for (int w = warp; w < words; w += NW) {
+        const bool mine = undecided(32 * w + lane);
+        const int page = mine ? page_of(32 * w + lane) : first;
+        for (unsigned todo = __ballot_sync(FULL, mine); todo != 0; todo &= todo - 1) {
+          uint32_t x[8];
+          words_of(__shfl_sync(FULL, page, __ffs(todo) - 1), x);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) differs |= x[k] ^ like[k];
+        }
+        if (__any_sync(FULL, differs != 0)) break;
+      }
+      if (differs != 0) atomicOr(&sh.among, 1u);
+      sync_row<T>();
+      score_again = sh.among != 0;
+    }
     unsigned long long key_at = 0, mask = 0;
     int left = places;
     if (score_again) {
