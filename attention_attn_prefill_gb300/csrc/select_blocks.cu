@@ -20,7 +20,7 @@
 // Measured (GB300, calls in a captured graph, copy rate 6796 GB/s): 64 rows over 512 to 8192 tokens, 32/8 heads, d = 128,
 // 27.4 us, of which the scores take 17.5 (72 MB of bounds: 10.6 at the copy rate) and the pick's chain of dependent steps
 // the rest; 8 rows over 6335 to 122863 tokens, 16/2 heads, d = 256, 29.0 (9.8), of which the scores 16.3; 512 rows of one
-// sequence of 32768, 32/8 heads, 49.6, of which the scores 20.4 (4096 rows of 2048: 33 MB written) and the pick 29.
+// sequence of 32768, 32/8 heads, 44.3, of which the scores 20.4 (4096 rows of 2048: 33 MB written) and the pick 24.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -701,6 +701,17 @@ __device__ __forceinline__ void sync_row() {
   else __syncthreads();
 }
 
+// Bit j of lane l goes to bit l of lane j
+__device__ __forceinline__ unsigned transpose_32x32(unsigned w, int lane) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const unsigned keep = s == 16 ? 0xffffu : s == 8 ? 0xff00ffu : s == 4 ? 0xf0f0f0fu : s == 2 ? 0x33333333u : 0x55555555u;
+    const unsigned y = __shfl_xor_sync(FULL, w, s);
+    w = lane & s ? (w & ~keep) | (y >> s & keep) : (w & keep) | (y << s & ~keep);
+  }
+  return w;
+}
+
 // A bit for each number below n of a word's 32
 __device__ __forceinline__ unsigned below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1; }
 
@@ -1296,39 +1307,56 @@ __device__ __forceinline__ bool pick_warp(const SelectBlocksParams& p, const Row
   high = from_order(__reduce_max_sync(FULL, order_of(high)));
   const float off = eps * row.q_norm * __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(row.b_norm)));
   if (!(off < INFINITY)) return false;
-  unsigned bits[NW];
-  int open = 0, over = 0;  // in the window; above it
+  unsigned bits[NW], in[NW];  // of this lane's scores: bit j % 32 of number j / 32; above the window, within it
+  int open = 0, over = 0;     // how many are in the window; above it
   for (;;) {
     const float range = high - low, per_step = (4 * BINS - 1) / range;
     if (!(range < INFINITY && per_step < INFINITY)) return false;
 #pragma unroll
-    for (int j = 0; j < NR; ++j)
-      if (32 * j < nb) count_step(hist, x[j], low, high, per_step);
+    for (int j = 0; j < NR; ++j) count_step(hist, x[j], low, high, per_step);
     __syncwarp();
     narrow(border_bin(hist, over, want, lane), range, off, low, high);
-    open = over = 0;
 #pragma unroll
-    for (int k = 0; k < NW; ++k) bits[k] = 0;
+    for (int k = 0; k < NW; ++k) bits[k] = in[k] = 0;
 #pragma unroll
     for (int j = 0; j < NR; ++j) {
-      if (32 * j >= nb) continue;
-      const bool above = x[j] > high, in = x[j] >= low && !above;
-      const unsigned word = __ballot_sync(FULL, above), ins = __ballot_sync(FULL, in);
-      if (lane == j % 32) bits[j / 32] = word;
-      over += __popc(word);
-      if (ins == 0) continue;
-      const int k = open + __popc(ins & ((1u << lane) - 1));
-      if (in && k < 32) {
-        sh.at[k] = 32 * j + lane;
-        sh.score[k] = x[j];
-      }
-      open += __popc(ins);
+      if (x[j] > high) bits[j / 32] |= 1u << j % 32;
+      if (x[j] >= low) in[j / 32] |= 1u << j % 32;
     }
-    __syncwarp();
-    if (open <= 32) break;
+    open = over = 0;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      in[k] &= ~bits[k];
+      open += __popc(in[k]);
+      over += __popc(bits[k]);
+    }
+    int place = open;  // in the list of those in the window, after the lanes' before
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(FULL, place, o);
+      if (lane >= o) place += y;
+    }
+    place -= open;
+    open = __shfl_sync(FULL, place + open, 31);
+    over = __reduce_add_sync(FULL, over);
+    if (open <= 32) {
+#pragma unroll
+      for (int k = 0; k < NW; ++k)
+        for (; in[k] != 0; in[k] &= in[k] - 1, ++place) {
+          const int i = 32 * (32 * k + __ffs(in[k]) - 1) + lane;
+          sh.at[place] = i;
+          sh.score[place] = sc[i];
+        }
+      __syncwarp();
+      break;
+    }
     if (!(high - low < 0.5f * range)) return false;  // the error's width: they may as well be alike
+    __syncwarp();
     clear();
   }
+  // block 32 j + l is bit j of lane l's: to bit l of lane j's
+#pragma unroll
+  for (int k = 0; k < NW; ++k) bits[k] = transpose_32x32(bits[k], lane);
   Border at = settle(sh, open, want - over, off, lane);
   if (at.among != 0 && off != 0.f) refine(p, row, off / eps, at, lane);
   bool chosen = at.sure || at.close;
@@ -1374,7 +1402,7 @@ __global__ void __launch_bounds__(128, NR == 16 ? 6 : NR == 32 ? 5 : 4) select_w
   const bool beyond = at >= static_cast<int64_t>(p.T) * p.Hkv;
   if (beyond) at = 0;
   Row row;
-  row.r = static_cast<int>(at / p.Hkv);
+  row.r = static_cast<int>(static_cast<unsigned>(at) / static_cast<unsigned>(p.Hkv));  // rows times heads are below 2^31
   row.h = static_cast<int>(at - static_cast<int64_t>(row.r) * p.Hkv);
   row.n = p.cu == nullptr ? row.r : sequence_of(p.cu, p.N, row.r);
   const Span s = span_of(p, row.n, false);
@@ -1651,9 +1679,10 @@ cudaError_t launch(const SelectBlocksParams& p, Scratch& ws, cudaStream_t stream
   // The whole call with 128 and with 1024 threads, d = 64: 128 rows of 2500 blocks 31.9 and 26.0 us, 256 47.6 and 46.1, 512
   // 80.8 and 89.3, 800 112 and 132; of 8125 128 71.8 and 59.3, 256 122.3 and 116.6, 512 220.8 and 228.2, 800 346 and 352.
   // A warp a row, its scores in registers, has no barriers and does a row's common work once; a CTA a row has more rows'
-  // latencies under way where they are few.  Warp and CTA, us, d = 128: 16384 rows of 250 blocks 65 and 96, of 500 63 and 92,
-  // 32768 of 1000 160 and 220, 16384 of 2000 166 and 170; 1024 of 500 16.0 and 17.6, of 1000 18.7 and 20.7; decode steps of
-  // 2048 rows and heads, 500 108 and 111, 2000 361 and 366; 512, 500 39.4 and 38.1; 64, 1000 18.1 and 19.0, 2000 26.5 and 21.6
+  // latencies under way where they are few.  Warp and CTA, us, d = 128: 16384 rows of 250 blocks 64 and 96, of 500 61 and 92,
+  // of 2000 130 and 170, 32768 of 1000 143 and 220; 1024 of 1000 17.4 and 20.7, of 2000 20.6 and 23.8; decode steps of 2048
+  // rows and heads, 1000 blocks 202 and 204, 2000 384 and 386; 512 of 375 33.0 and 32.1, of 1000 61.4 and 62.6; 64 of 2000
+  // 26.3 and 23.7.
   if (static_cast<int64_t>(p.T) * p.Hkv >= WARP_ROWS) {
     if (p.max_blocks <= 512) return select_warps<16>(p, ws, stream);
     if (p.max_blocks <= 1024) return select_warps<32>(p, ws, stream);
