@@ -14,8 +14,8 @@
 // 128 blocks by 64 rows a tcgen05 tile.  Either way
 //   |score - exact| <= eps ||Q|| ||b||,  b = (lo, hi) of a block, by Cauchy and Schwarz on the sum of |terms|.
 // Pick: a CTA, or where there are many a warp, puts the scores of its row and head into bins over their range, gathers
-// the few in and about the bin that holds the border, and a warp settles the border among them.  Few short sequences of one row each take one
-// launch, a CTA scoring and picking: select_one_kernel.
+// the few in and about the bin that holds the border, and a warp settles the border among them.  Few short sequences of
+// one row each take one launch, a CTA scoring and picking: select_one_kernel.
 //
 // Measured (GB300, calls in a captured graph, copy rate 6796 GB/s): 64 rows over 512 to 8192 tokens, 32/8 heads, d = 128,
 // 27.4 us, of which the scores take 17.5 (72 MB of bounds: 10.6 at the copy rate) and the pick's chain of dependent steps
@@ -799,7 +799,7 @@ __device__ __forceinline__ void add_exactly(float& hi, float& lo, float x) {
 }
 
 // The close blocks' scores to 40 bits, as sums of two floats (Dekker's and Knuth's exact sums and products): 64-bit arithmetic
-// has a hundredth of the rate here, and a warp that settled its row's border by it took 10 to 20 us.  What remains close is
+// has a sixtieth of the rate here, and a warp that settled its row's border by it took 10 to 20 us.  What remains close is
 // left to it.  By a warp: lane l has words 32 k + l of a block's bounds, of which D / 32 there are; norms: ||Q|| times the
 // largest ||b||.  The loads go ahead of the sums: table entries, then the queries, four heads at a time, and the first
 // block's bounds.
