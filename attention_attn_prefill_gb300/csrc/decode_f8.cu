@@ -100,13 +100,15 @@ struct RowInfo {
 __device__ __forceinline__ RowInfo row_info(const DecodeF8Params& p, int r) {
   RowInfo x{r, 0};
   int behind = 0;  // query tokens of the sequence behind this one
+  // where each sequence has one row, row r is sequence r's: its length is read along with cu, not behind it
+  const int guess = r < p.N ? clamped_len(p.seq_lens, r, p.max_blocks) : 0;
   if (p.cu != nullptr) {
     const int n = sequence_of(p.cu, p.N, r), end = p.cu[n + 1];
     x.n = p.cu[n] <= r && r < end ? n : -1;
     behind = end - 1 - r;
   }
   if (x.n >= 0) {
-    const int seen = clamped_len(p.seq_lens, x.n, p.max_blocks) - behind;
+    const int seen = (x.n == r ? guess : clamped_len(p.seq_lens, x.n, p.max_blocks)) - behind;
     x.seen = seen > 0 ? seen : 0;
   }
   return x;
@@ -536,6 +538,8 @@ __global__ void __launch_bounds__(Cfg<D, P, DEAL>::THREADS, Cfg<D, P, DEAL>::CTA
     const int kvh = seg_u / geo.tiles, h0 = seg_u % geo.tiles * TILE;
     const int heads = G - h0 < TILE ? G - h0 : TILE;
     const __nv_bfloat16* q_head = p.q + (static_cast<int64_t>(seg_n) * p.Hq + kvh * G + h0) * D;
+    // for the merge of the last segment, asked here, while the first records are on their way
+    const bool lives = !LISTED || p.cu == nullptr || seg_end < count || row_info(p, seg_n).n >= 0;
 
     // ---- queries: channels 64 j + 16 t + 4 s .. + 3, in the order of the K words
     uint32_t qb[R::KJ][4][2];
@@ -774,7 +778,6 @@ __global__ void __launch_bounds__(Cfg<D, P, DEAL>::THREADS, Cfg<D, P, DEAL>::CTA
     if (seg_end == count) {  // nothing is left to do: all warps merge, in a fraction of the time that one takes
       ok = __all_sync(FULL, mbar_wait(rec_full, seg_index & 1));
       if (!ok) break;
-      const bool lives = !LISTED || p.cu == nullptr || row_info(p, seg_n).n >= 0;
       merge_states(seg_n, seg_u, first_step == 0, first_step + seg_steps == cur.ns, lives, warp * 32 + lane, NW * 32);
     }
     ++seg_index;
@@ -836,7 +839,7 @@ cudaError_t launch(const DecodeF8Params& p, cudaStream_t stream) {
   };
   if (pairs <= sms && steps <= 8) return start<D, P, LISTED, WHOLE>(p, geo, pairs, stream);
   if (pairs <= sms && steps <= (LISTED ? 14 : 33) + pairs / 2) return start<D, P, LISTED, ALONE>(p, geo, pairs, stream);
-  if (LISTED || pages <= 128) {  // a table may be far wider than most of its sequences
+  if ((LISTED || pages <= 128) && pairs < int64_t(1) << 31) {  // a table may be far wider than most of its sequences
     const int64_t many = sms * Cfg<D, P, MANY>::CTAS, rounds = (pairs + many - 1) / many;
     if (pairs <= geo.grid && lost(geo.grid) <= (LISTED ? 56 : 45)) return start<D, P, LISTED, WHOLE>(p, geo, pairs, stream);
     if (pairs > geo.grid && lost(many) <= 45 * (rounds > 2 ? rounds - 1 : 1))
