@@ -23,9 +23,9 @@
 // width takes, and the loading warp says how many tokens of each page the query sees.
 //
 // Bound by reading the records.  Measured (GB300, calls in a captured graph, copy rate 6796 GB/s): 64 sequences of 512
-// to 8192, 32/8 heads, d = 128, 96.0 us, 5.98 TB/s; 8 of 6335 to 122863, 16/2 heads, d = 256, 86.8 us, 6.11 TB/s.  The
+// to 8192, 32/8 heads, d = 128, 96.5 us, 5.95 TB/s; 8 of 6335 to 122863, 16/2 heads, d = 256, 87.0 us, 6.10 TB/s.  The
 // kernel itself reads at 6.1 TB/s with 31% of the issue slots used; start, merge and CTAs that end earlier than others
-// are the rest.  64 listed blocks of each row and head, 133 MB: 27.9 us, 4.77 TB/s, a CTA each; 1 sequence of 1009 8.3 us.
+// are the rest.  64 listed blocks of each row and head, 133 MB: 27.1 us, 4.92 TB/s, a CTA each; 1 sequence of 1009 8.5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -69,12 +69,16 @@ template <int D, int P, int DEAL>
 struct Cfg {
   // Warps that compute (one more loads), steps in flight a warp, and CTAs an SM: what shared memory holds.  SHARES, measured
   // on 64 sequences of 512 to 8192, 32/8 heads, d = 128, warps x steps x CTAs: 5 x 2 x 2 98.8 us, 3 x 2 x 3 100.4, 4 x 3 x 2
-  // 103.9, 11 x 2 x 1 102.7 (more in flight is no faster), one page a step 7 x 2 x 2 100.6.
+  // 103.9, 11 x 2 x 1 102.7 (more in flight is no faster), one page a step 7 x 2 x 2 100.6.  64 of 8704, d = 64, 64/8
+  // heads: 5 x 3 x 3 116.3, 3 x 3 x 5 (FINE) 109.7; with 32/8 heads, two pages a step, 104.0 and 105.6.  64 of 512 to 8192,
+  // 64/8 heads, d = 128: 7 x 2 x 2 105.0, 3 x 2 x 4 102.4, 3 x 3 x 4 101.0; MANY's 512 lists of 64 blocks with two steps
+  // in flight 29.0, with three 27.9.
+  static constexpr bool FINE = DEAL == SHARES && D <= 128 && P == 1;
   static constexpr int NW = DEAL == ALONE  ? (D == 256 ? 8 : D == 128 && P == 2 ? 11 : 13)
-                            : DEAL == MANY ? (D == 256 ? 2 : 3)
-                                           : (D == 256 ? 4 : D == 128 && P == 1 ? 7 : 5);
-  static constexpr int DEPTH = D == 64 ? 3 : 2;
-  static constexpr int CTAS = DEAL == ALONE ? 1 : DEAL == MANY ? (D == 64 ? 5 : 4) : D == 64 ? 3 : 2;
+                            : DEAL == MANY || FINE ? (D == 256 ? 2 : 3)
+                                                   : (D == 256 ? 4 : D == 128 && P == 1 ? 7 : 5);
+  static constexpr int DEPTH = D == 64 || FINE || (DEAL == MANY && D == 128 && P == 1) ? 3 : 2;
+  static constexpr int CTAS = DEAL == ALONE ? 1 : DEAL == MANY || FINE ? (D == 64 ? 5 : 4) : D == 64 ? 3 : 2;
   static constexpr int THREADS = (NW + 1) * 32;
   static constexpr int TILE = ROWS / P;  // query heads a tile
   static constexpr int SLOTS = NW * DEPTH;
@@ -787,14 +791,17 @@ __global__ void __launch_bounds__(Cfg<D, P, DEAL>::THREADS, Cfg<D, P, DEAL>::CTA
   if (!ok && lane == 0) set_error(&g_decode_f8_status, kDevWaitTimeout);
 }
 
-// CTAs of the grid: every SM filled
-template <int D>
-int grid_of_device() {
-  static_assert(Cfg<D, 1, SHARES>::CTAS == Cfg<D, D == 256 ? 1 : 2, SHARES>::CTAS, "one size of workspace for a head dim");
+int sms_of_device() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return sms * Cfg<D, 1, SHARES>::CTAS;
+  return sms;
+}
+// CTAs of the largest grid that leaves partials, of either number of pages a step
+template <int D>
+constexpr int most_ctas() {
+  constexpr int one = Cfg<D, 1, SHARES>::CTAS, two = Cfg<D, D == 256 ? 1 : 2, SHARES>::CTAS;
+  return one > two ? one : two;
 }
 
 template <int D, int P, bool LISTED, int DEAL>
@@ -811,8 +818,9 @@ template <int D, int P, bool LISTED>
 cudaError_t launch(const DecodeF8Params& p, cudaStream_t stream) {
   using C = Cfg<D, P, SHARES>;
   Geometry geo;
-  geo.grid = grid_of_device<D>();
-  if (geo.grid <= 0) return cudaErrorInvalidDevice;
+  const int sms = sms_of_device();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  geo.grid = sms * C::CTAS;  // every SM filled
   const int rows = LISTED ? p.T : p.N;
   geo.tile = C::TILE;
   geo.tiles = (p.Hq / p.Hkv + C::TILE - 1) / C::TILE;
@@ -832,7 +840,6 @@ cudaError_t launch(const DecodeF8Params& p, cudaStream_t stream) {
   //   1200: 64 listed blocks 63.5 89.3 66.9 57.8; 2400: 1000 tokens 104 142 111 99
   // and the other head dims and group sizes alike: over 637 cases the rule takes 0.77 of the time of SHARES alone.
   const int64_t pages = LISTED ? p.K : p.max_blocks, steps = (pages + P - 1) / P;
-  const int sms = geo.grid / C::CTAS;
   auto lost = [&](int64_t ctas) {  // with so many at a time
     const int64_t places = (pairs + ctas - 1) / ctas * ctas;
     return pages * (places - pairs) / ctas;
@@ -840,11 +847,11 @@ cudaError_t launch(const DecodeF8Params& p, cudaStream_t stream) {
   if (pairs <= sms && steps <= 8) return start<D, P, LISTED, WHOLE>(p, geo, pairs, stream);
   if (pairs <= sms && steps <= (LISTED ? 14 : 33) + pairs / 2) return start<D, P, LISTED, ALONE>(p, geo, pairs, stream);
   if ((LISTED || pages <= 128) && pairs < int64_t(1) << 31) {  // a table may be far wider than most of its sequences
-    const int64_t many = sms * Cfg<D, P, MANY>::CTAS, rounds = (pairs + many - 1) / many;
-    if (pairs <= geo.grid && lost(geo.grid) <= (LISTED ? 56 : 45)) return start<D, P, LISTED, WHOLE>(p, geo, pairs, stream);
-    if (pairs > geo.grid && lost(many) <= 45 * (rounds > 2 ? rounds - 1 : 1))
+    const int64_t fit = sms * Cfg<D, P, WHOLE>::CTAS, many = sms * Cfg<D, P, MANY>::CTAS, rounds = (pairs + many - 1) / many;
+    if (pairs <= fit && lost(fit) <= (LISTED ? 56 : 45)) return start<D, P, LISTED, WHOLE>(p, geo, pairs, stream);
+    if (pairs > fit && lost(many) <= 45 * (rounds > 2 ? rounds - 1 : 1))
       return start<D, P, LISTED, MANY>(p, geo, pairs, stream);
-    if (pairs > geo.grid && rounds <= 2 && lost(geo.grid) <= 10) return start<D, P, LISTED, WHOLE>(p, geo, pairs, stream);
+    if (pairs > fit && rounds <= 2 && lost(fit) <= 10) return start<D, P, LISTED, WHOLE>(p, geo, pairs, stream);
   }
   const cudaError_t e = start<D, P, LISTED, SHARES>(p, geo, geo.grid, stream);
   if (e != cudaSuccess) return e;
@@ -873,11 +880,8 @@ extern "C" int attn_test_drop_copy_f8(int what) {
 #endif
 
 size_t decode_f8_workspace_bytes(int d) {
-  const int grid = d == 64    ? grid_of_device<64>()
-                   : d == 128 ? grid_of_device<128>()
-                   : d == 256 ? grid_of_device<256>()
-                              : 0;
-  return workspace_bytes(grid, d);
+  const int ctas = d == 64 ? most_ctas<64>() : d == 128 ? most_ctas<128>() : d == 256 ? most_ctas<256>() : 0;
+  return workspace_bytes(sms_of_device() * ctas, d);
 }
 
 cudaError_t decode_f8_launch(int d, const DecodeF8Params& p, cudaStream_t stream) {

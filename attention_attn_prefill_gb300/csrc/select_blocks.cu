@@ -20,7 +20,7 @@
 // Measured (GB300, calls in a captured graph, copy rate 6796 GB/s): 64 rows over 512 to 8192 tokens, 32/8 heads, d = 128,
 // 27.4 us, of which the scores take 17.5 (72 MB of bounds: 10.6 at the copy rate) and the pick's chain of dependent steps
 // the rest; 8 rows over 6335 to 122863 tokens, 16/2 heads, d = 256, 29.0 (9.8), of which the scores 16.3; 512 rows of one
-// sequence of 32768, 32/8 heads, 44.3, of which the scores 20.4 (4096 rows of 2048: 33 MB written) and the pick 24.
+// sequence of 32768, 32/8 heads, 43.2, of which the scores 20.4 (4096 rows of 2048: 33 MB written) and the pick 23.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
