@@ -273,6 +273,39 @@ def test_select_of_one_row_each(attn, gpu, N, Hkv, d, width):
     assert attn.device_status() == 0
 
 
+@pytest.mark.parametrize("N,Hkv,d,width,most", [(41, 4, 128, 90, 70), (160, 1, 128, 40, 128), (20, 4, 128, 260, 5), (45, 4, 64, 60, 65),
+                                                (39, 4, 256, 33, 40), (41, 4, 128, 90, 129), (2, 2, 128, 300, 1000)])
+def test_select_of_chunks_of_many_sequences(attn, gpu, N, Hkv, d, width, most):
+    """Chunks of different lengths, some of none, and sequences shorter than their rows or their choice; what lies behind the
+    results and behind the workspace stays as it was."""
+    gen = torch.Generator(device=gpu).manual_seed(N + width)
+    rng = np.random.default_rng(N + width)
+    rows = [int(x) for x in rng.integers(0, most + 1, N)]
+    rows[0], rows[1] = most, 0
+    lens = [max(1, int(x)) for x in rng.integers(1, 16 * width + 1, N)]
+    lens[0] = 16 * width
+    K, blocks = 12, 4 * width
+    b = torch.randn((blocks, Hkv, 2, d), generator=gen, device=gpu).sort(2).values.to(torch.bfloat16)
+    table = torch.randint(0, blocks, (N, width), generator=gen, device=gpu, dtype=torch.int32)
+    cu = np.concatenate([[0], np.cumsum(rows)]).tolist()
+    T = cu[-1]
+    q = _randn((T + 3, 2 * Hkv, d), gen, gpu)
+    out = torch.full((T + 3, Hkv, K), -7, dtype=torch.int32, device=gpu)
+    need = attn.select_blocks_workspace_bytes(T + 3, N, most, Hkv, d, width)
+    ws = torch.full((need + 256,), 0x5A, dtype=torch.uint8, device=gpu)
+    attn.select_blocks(q, b, table, _i32(lens, gpu), K, cu_seqlens_q=_i32(cu, gpu), max_seqlen_q=most, out=out, workspace=ws[:need])
+    assert (ws[need:] == 0x5A).all() and (out[T:] == -7).all() and attn.device_status() == 0
+    for n in sorted({0, 2 % N, 3 % N, N // 2, N - 1}):
+        picked = sorted({0, rows[n] // 2, rows[n] - 1}) if rows[n] else []
+        for r in picked:
+            seen = lens[n] - (rows[n] - 1 - r)
+            if seen <= 0:
+                assert (out[cu[n] + r] == -1).all()
+                continue
+            want = _wanted_odd(q[cu[n] + r:cu[n] + r + 1], b, table[n:n + 1], seen, K, 1, 2)
+            assert torch.equal(out[cu[n] + r], want), (n, r)
+
+
 @pytest.mark.parametrize("rows,Hq,Hkv,d,width,K", [
     (700, 4, 2, 128, 60, 9), (1100, 3, 1, 64, 512, 40), (600, 8, 2, 256, 513, 33), (520, 4, 2, 128, 1024, 64),
     (400, 3, 3, 64, 1300, 700), (350, 15, 3, 128, 1850, 5), (260, 8, 4, 128, 2560, 90), (1050, 2, 1, 256, 2561, 20)])
