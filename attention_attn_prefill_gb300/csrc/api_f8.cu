@@ -13,7 +13,7 @@ using namespace attn::api;
 
 namespace {
 
-constexpr int kMostBlocks = 1 << 18;  // of a sequence, for block selection: a bit each in shared memory, twice
+constexpr int kMostBlocks = attn::SELECT_MOST_BLOCKS;
 
 // What both decodes over the 8-bit cache check and pass on
 attn_status_t decode_f8(attn::DecodeF8Params& p, const void* q, const void* cache, const int32_t* block_table,

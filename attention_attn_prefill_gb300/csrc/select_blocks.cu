@@ -52,6 +52,7 @@ constexpr int BINS = 512;          // of a window of scores
 constexpr int CACHED_BLOCKS = 12288;  // scores of a row that shared memory holds
 constexpr int64_t WARP_ROWS = 1024;   // rows times heads from which on a warp takes each, if its registers hold the scores
 constexpr int NARROW = 1024;       // columns of a block table up to which 128 threads take a row
+constexpr int ONE_BLOCKS = 4096;   // columns up to which select_one_kernel may be taken
 // Norms below this count as this: squares of smaller numbers may vanish, and a bound that is too large does no harm
 constexpr float LEAST_NORM = 1e-14f;
 constexpr int64_t SCORE_CTAS = 152 * 4;  // of the grid, about: a block table may be far wider than its sequences
@@ -132,9 +133,14 @@ struct FewCfg {
   static constexpr int TERMS = 2 * 2 * D * 2;        // bytes of Q- and Q+ of a row: two columns
   static constexpr int MOST_WARPS = D == 64 ? 16 : 13;
   static constexpr int warp_bytes(int rows) { return DEPTH * STAGE + rows * TERMS; }
-  static int warps(int rows) {
+  static constexpr int warps(int rows) {
     const int fit = 222 * 1024 / warp_bytes(rows);
     return fit < MOST_WARPS ? fit : MOST_WARPS;
+  }
+  static constexpr int most_bytes() {  // of a CTA, whatever the number of rows
+    int most = 0;
+    for (int rows = 1; rows <= FEW; ++rows) most = most > warps(rows) * warp_bytes(rows) ? most : warps(rows) * warp_bytes(rows);
+    return most;
   }
 };
 
@@ -667,6 +673,10 @@ __device__ __forceinline__ unsigned long long order_of(double x) {
 
 // Words of shared memory before the scores: two bits a block, in whole 16 bytes
 __host__ __device__ constexpr int cache_at(int max_blocks) { return (2 * ((max_blocks + 31) / 32) + 3) / 4 * 4; }
+// Bytes of it that picking takes, with the scores or without
+constexpr int pick_bytes(int max_blocks, bool cached) {
+  return (cache_at(max_blocks) + (cached ? (max_blocks + 31) / 32 * 32 : 0)) * 4;
+}
 
 // Every block that a row sees, and -1 behind
 template <int T>
@@ -1581,6 +1591,9 @@ __global__ void __launch_bounds__(T, 512 / T) select_one_kernel(const SelectBloc
   pick<T, true>(p, row, eps, shared, s_bits);
 }
 
+// A kernel's limit of dynamic shared memory belongs to the kernel on the device, not to the call: two host threads set it
+// between each other's setting and launch.  So every call sets the same limit, the largest that any call needs.
+
 // A launch as a programmatic dependent of the kernel before it
 template <class... Params, class... Args>
 cudaError_t launch_behind(void (*kernel)(Params...), unsigned grid, unsigned threads, int smem, cudaStream_t stream, Args... args) {
@@ -1599,8 +1612,9 @@ cudaError_t launch_behind(void (*kernel)(Params...), unsigned grid, unsigned thr
 
 template <int T, bool CACHED>
 cudaError_t select(const SelectBlocksParams& p, const Scratch& ws, cudaStream_t stream) {
-  const int smem = (cache_at(p.max_blocks) + (CACHED ? (p.max_blocks + 31) / 32 * 32 : 0)) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(select_kernel<T, CACHED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int MOST = pick_bytes(CACHED ? CACHED_BLOCKS : SELECT_MOST_BLOCKS, CACHED);
+  const int smem = pick_bytes(p.max_blocks, CACHED);
+  const cudaError_t e = cudaFuncSetAttribute(select_kernel<T, CACHED>, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST);
   if (e != cudaSuccess) return e;
   return launch_behind(select_kernel<T, CACHED>, static_cast<unsigned>(static_cast<int64_t>(p.T) * p.Hkv), T, smem, stream, p,
                        ws);
@@ -1608,17 +1622,17 @@ cudaError_t select(const SelectBlocksParams& p, const Scratch& ws, cudaStream_t 
 
 template <int NR>
 cudaError_t select_warps(const SelectBlocksParams& p, const Scratch& ws, cudaStream_t stream) {
-  const int smem = 4 * cache_at(p.max_blocks) * 4;
+  const int smem = 4 * pick_bytes(p.max_blocks, false);
   return launch_behind(select_warps_kernel<NR>, static_cast<unsigned>((static_cast<int64_t>(p.T) * p.Hkv + 3) / 4), 128, smem,
                        stream, p, ws);
 }
 
 template <int D, int T>
 cudaError_t select_one(const SelectBlocksParams& p, float eps, cudaStream_t stream) {
-  const int smem = (cache_at(p.max_blocks) + (p.max_blocks + 31) / 32 * 32) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(select_one_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  select_one_kernel<D, T><<<static_cast<unsigned>(static_cast<int64_t>(p.N) * p.Hkv), T, smem, stream>>>(p, eps);
+  // within the 48 KB that a launch may take without a limit of its own, beside sums, bins and norms
+  static_assert(pick_bytes(ONE_BLOCKS, true) + sizeof(PickShared) + 4 * 1024 <= 48 * 1024, "shared memory budget");
+  select_one_kernel<D, T><<<static_cast<unsigned>(static_cast<int64_t>(p.N) * p.Hkv), T, pick_bytes(p.max_blocks, true), stream>>>(
+      p, eps);
   return cudaGetLastError();
 }
 
@@ -1626,7 +1640,7 @@ template <int D>
 cudaError_t score_few(const SelectBlocksParams& p, const Scratch& ws, int sms, cudaStream_t stream) {
   using C = FewCfg<D>;
   const int warps = C::warps(p.max_q), smem = warps * C::warp_bytes(p.max_q);
-  const cudaError_t e = cudaFuncSetAttribute(score_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = cudaFuncSetAttribute(score_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::most_bytes());
   if (e != cudaSuccess) return e;
   score_few_kernel<D><<<sms, warps * 32, smem, stream>>>(p, ws);
   return cudaGetLastError();
@@ -1666,7 +1680,8 @@ cudaError_t launch(const SelectBlocksParams& p, Scratch& ws, cudaStream_t stream
   // 1000 26.3 and 26.1; 8 of 250 8.8 and 11.2, of 500 10.9 and 10.5, of 1000 17.2 and 12.3; 256 of 500 21.7 and 26.4.  Of
   // more, smaller CTAs: 512 of 125 12.1 and 18.3, of 250 22.0 and 26.5, of 32 to 512 30.9 and 27.5, where the longest is
   // waited for; 2048 of 125 45.0 and 43.2.
-  if (p.max_q == 1 && pairs <= 2 * sms && p.max_blocks <= 250 + 8 * pairs) return select_one<D, 256>(p, ws.eps, stream);
+  if (p.max_q == 1 && pairs <= 2 * sms && p.max_blocks <= ONE_BLOCKS && p.max_blocks <= 250 + 8 * pairs)
+    return select_one<D, 256>(p, ws.eps, stream);
   if (p.max_q == 1 && pairs <= 4 * sms && p.max_blocks <= 256) return select_one<D, 128>(p, ws.eps, stream);
   // few rows and more tiles of blocks than SMs: gathering the bounds counts, and two CTAs an SM overlap that
   const bool small = D == 128 && p.max_q <= SMALL_ROWS && pairs * ((p.max_blocks + 127) / 128) > sms;

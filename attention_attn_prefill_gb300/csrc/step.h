@@ -109,6 +109,7 @@ struct DecodeF8Params {
 size_t decode_f8_workspace_bytes(int d);  // on the current device; 0 on error
 cudaError_t decode_f8_launch(int d, const DecodeF8Params& p, cudaStream_t stream);
 
+constexpr int SELECT_MOST_BLOCKS = 1 << 18;  // of a sequence: a bit each in shared memory, twice
 struct SelectBlocksParams {
   const __nv_bfloat16* q;       // [T][Hq][d]
   const __nv_bfloat16* bounds;  // [num_blocks][Hkv][2][d]
