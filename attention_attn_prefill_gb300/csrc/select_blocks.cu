@@ -55,12 +55,14 @@ constexpr int NARROW = 1024;       // columns of a block table up to which 128 t
 constexpr int ONE_BLOCKS = 4096;   // columns up to which select_one_kernel may be taken
 // Norms below this count as this: squares of smaller numbers may vanish, and a bound that is too large does no harm
 constexpr float LEAST_NORM = 1e-14f;
+// Squared norms of a block from here on count as infinite, so that no finite norm makes a score overflow
+constexpr float MOST_SQUARES = 1e36f;
 constexpr int64_t SCORE_CTAS = 152 * 4;  // of the grid, about: a block table may be far wider than its sequences
 
 struct Scratch {
   float* scores;  // [T][Hkv][stride]
   float* q_norm;  // [T][Hkv]
-  float* b_norm;  // [N][Hkv][tiles]: a bound of the largest norm among 16 blocks
+  float* b_norm;  // [N][Hkv][tiles]: a bound of the largest norm among those of 16 blocks that compete
   uint8_t* images;  // [row tiles][Hkv]: the queries' sums, where a sequence has more than FEW rows
   int64_t stride;
   int tiles;
@@ -90,6 +92,10 @@ __device__ __forceinline__ Span span_of(const SelectBlocksParams& p, int n, bool
 __device__ __forceinline__ int blocks_seen(const Span& s, int r) {
   const int seen = s.len - (s.end - 1 - r);
   return seen <= 0 ? 0 : (seen + PAGE - 1) / PAGE;
+}
+// whether block i of nb competes: the first and the last ones are chosen, whatever their scores
+__device__ __forceinline__ bool competes(const SelectBlocksParams& p, int i, int nb) {
+  return static_cast<unsigned>(i - p.first) < static_cast<unsigned>(nb - p.last - p.first);
 }
 
 __device__ __forceinline__ float2 pair_of(uint32_t w) {
@@ -370,8 +376,8 @@ __global__ void __launch_bounds__(FewCfg<D>::MOST_WARPS * 32, 1) score_few_kerne
     for (int e = 0; e < 2; ++e) {
       norm[e] += __shfl_xor_sync(FULL, norm[e], 1);
       norm[e] += __shfl_xor_sync(FULL, norm[e], 2);
-      if (!(norm[e] < INFINITY)) norm[e] = INFINITY;  // NaN too
-      if (blk + 8 * e < at.nb) most = max(most, __float_as_uint(norm[e]));  // else page 0's
+      if (!(norm[e] < MOST_SQUARES)) norm[e] = INFINITY;  // NaN too
+      if (competes(p, blk + 8 * e, at.nb)) most = max(most, __float_as_uint(norm[e]));
       norm[e] = 0.f;
     }
     most = __reduce_max_sync(FULL, most);
@@ -601,8 +607,8 @@ __global__ void __launch_bounds__(ManyCfg<D, SMALL>::WARPS * 32, ManyCfg<D, SMAL
         const float2 y = pair_of(sum[0]), z = pair_of(sum[1]);
         norm += (y.x + y.y) + (z.x + z.y);
       }
-      if (!(norm < INFINITY)) norm = INFINITY;  // NaN too
-      uint32_t most = blk < nb ? __float_as_uint(norm) : 0u;
+      if (!(norm < MOST_SQUARES)) norm = INFINITY;  // NaN too
+      uint32_t most = competes(p, blk, nb) ? __float_as_uint(norm) : 0u;
       for (int off = 8; off > 0; off >>= 1) most = max(most, __shfl_xor_sync(FULL, most, off));
       // the sum of squares may have been an eighth too small
       if (lane % 16 == 0 && blk < nb)
@@ -701,9 +707,20 @@ struct PickShared {
 // What picking needs of a row and KV head
 struct Row {
   int r, h, n, nb;     // row, KV head, sequence; the blocks that it sees, more than it may choose
-  const float* scores;  // in global memory, rows of whole multiples of eight floats; null: in shared memory already
-  float q_norm, b_norm;  // b_norm: this thread's share of a maximum
+  float* scores;       // in global memory, rows of whole multiples of eight floats; null: in shared memory already
+  const float* norms;  // of tiles of 16 blocks: infinite where the tile is wild
+  float q_norm, b_norm;  // b_norm: this thread's share of the maximum of the others
+  bool wild;             // this thread's share of whether there are wild ones
 };
+// A tile's norm counts
+__device__ __forceinline__ void count_norm(Row& row, float norm) {
+  if (norm < INFINITY) row.b_norm = fmaxf(row.b_norm, norm);
+  else row.wild = true;
+}
+// ||Q|| as the bound takes it: not 0 beside wild tiles, whose scores may be anything all the same
+__device__ __forceinline__ float norm_of_q(const Row& row, bool wild) {
+  return wild && row.q_norm < LEAST_NORM ? LEAST_NORM : row.q_norm;
+}
 
 // All threads of a row: a warp of a CTA, or a CTA
 template <int T>
@@ -934,12 +951,83 @@ __device__ __noinline__ unsigned long long exact_keys(const SelectBlocksParams& 
   return key;
 }
 
+// The sums over heads in 64 bits, [2 d], channels begin, begin + step, ..
+__device__ __forceinline__ void sum_heads(const SelectBlocksParams& p, const Row& row, double* sums, int begin, int step) {
+  const int D = p.d, G = p.Hq / p.Hkv;
+  for (int c = begin; c < D; c += step) {
+    const __nv_bfloat16* q = p.q + (static_cast<int64_t>(row.r) * p.Hq + row.h * G) * D + c;
+    double neg = 0.0, pos = 0.0;
+    for (int e0 = 0; e0 < G; e0 += 4) {  // four heads' loads in flight
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = e0 + e < G ? __bfloat162float(q[(e0 + e) * D]) : 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        neg += x[e] > 0.f ? 0.f : x[e];
+        pos += x[e] < 0.f ? 0.f : x[e];
+      }
+    }
+    sums[c] = neg;
+    sums[D + c] = pos;
+  }
+}
+// Block i's bounds, words 32 k + lane
+__device__ __forceinline__ void load_bounds(const SelectBlocksParams& p, const Row& row, int i, uint32_t (&b)[8], int lane) {
+  int id = p.block_table[static_cast<int64_t>(row.n) * p.max_blocks + i];
+  if (id < 0 || id >= p.num_blocks) id = 0;
+  const uint32_t* from = reinterpret_cast<const uint32_t*>(p.bounds + (static_cast<int64_t>(id) * p.Hkv + row.h) * 2 * p.d) + lane;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) b[k] = 32 * k < p.d ? from[32 * k] : 0u;
+}
+// Their product with the sums, by a warp: the block's score in 64 bits
+__device__ __forceinline__ double product(const SelectBlocksParams& p, const double* sums, const uint32_t (&b)[8], int lane) {
+  double sum = 0.0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (32 * k >= p.d) break;
+    const float2 x = pair_of(b[k]);
+    const int c = 32 * k + lane;
+    sum = fma(sums[2 * c], static_cast<double>(x.x), fma(sums[2 * c + 1], static_cast<double>(x.y), sum));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+  return sum;
+}
+
+// Wild tiles, those with a bound that is no finite number or too large, would leave every score of the row unsure.  Their
+// blocks are scored in 64 bits, and take part with that score as a float, cut to what is above or below all others':
+// `most`, twice ||Q|| times the largest norm of the others.  That is off by less than the others' bound, keeps the order among wild
+// blocks, and those that it makes equal are told apart by exact scores, like all that are close to the border.  By all
+// threads of the row, between two barriers.
+template <int T>
+__device__ __noinline__ void tame(const SelectBlocksParams& p, int r, int h, int n, int nb, const float* norms, float most,
+                                  double* sums, float* scores) {
+  Row row;  // (a caller's would have to lie in memory)
+  row.r = r;
+  row.h = h;
+  row.n = n;
+  row.nb = nb;
+  const int tid = T == 32 ? threadIdx.x & 31 : threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  sum_heads(p, row, sums, tid, T);
+  sync_row<T>();
+  for (int tile = warp; 16 * tile < nb; tile += T / 32) {
+    if (norms[tile] < INFINITY) continue;
+    for (int i = 16 * tile; i < 16 * tile + 16; ++i) {
+      if (!competes(p, i, nb)) continue;
+      uint32_t b[8];
+      load_bounds(p, row, i, b, lane);
+      const double sum = product(p, sums, b, lane);
+      if (lane == 0) scores[i] = sum < most ? (sum > -most ? static_cast<float>(sum) : -most) : most;  // a NaN is the highest
+    }
+  }
+}
+
 // Picks the blocks of a row and KV head, by a CTA of T threads.  CACHED: shared memory holds its scores, else they are read
 // again and again.  s_bits: [words] chosen blocks, [words] ties; the scores from word cache_at on.
 template <int T, bool CACHED>
 __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row, float eps, PickShared& sh, uint32_t* s_bits) {
   constexpr int NW = T / 32;
-  const int D = p.d, nb = row.nb, K = p.K, r = row.r, h = row.h, n = row.n;
+  const int nb = row.nb, K = p.K, r = row.r, h = row.h, n = row.n;
   const int tid = T == 32 ? threadIdx.x & 31 : threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int32_t* out = p.blocks + (static_cast<int64_t>(r) * p.Hkv + h) * K;
   const int c0 = p.first, c1 = nb - p.last;  // the blocks that compete
@@ -950,23 +1038,23 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
   if (tid < 2) sh.open[tid] = sh.over[tid] = 0;
 
   // ---- how far a score may be off, and the scores' range
-  const float* sc = row.scores;
+  float* sc = row.scores;
   float* cache = reinterpret_cast<float*>(s_bits + cache_at(p.max_blocks));
   const float none = __uint_as_float(0x7fffffffu);  // a NaN: neither above, below nor within a window
-  auto competes = [&](int i) { return i >= c0 && i < c1; };
+  auto competing = [&](int i) { return i >= c0 && i < c1; };
   auto score = [&](int i) {  // of a block that competes, else none
     if constexpr (CACHED) return cache[i];
-    else return competes(i) ? sc[i] : none;
+    else return competing(i) ? sc[i] : none;
   };
   // four scores at a time, of blocks 4 v ..
   auto edge = [&](int v) { return 4 * v < c0 || 4 * v + 4 > c1; };
   auto read_four = [&](int v) {
     float4 x = *reinterpret_cast<const float4*>((CACHED && sc == nullptr ? cache : sc) + 4 * v);
     if (edge(v)) {
-      x.x = competes(4 * v) ? x.x : none;
-      x.y = competes(4 * v + 1) ? x.y : none;
-      x.z = competes(4 * v + 2) ? x.z : none;
-      x.w = competes(4 * v + 3) ? x.w : none;
+      x.x = competing(4 * v) ? x.x : none;
+      x.y = competing(4 * v + 1) ? x.y : none;
+      x.z = competing(4 * v + 2) ? x.z : none;
+      x.w = competing(4 * v + 3) ? x.w : none;
     }
     return x;
   };
@@ -976,71 +1064,48 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
   };
   float low = INFINITY, high = -INFINITY, off;
   {
+    auto widen = [&](const float4& x) {
+      low = fminf(fminf(low, fminf(x.x, x.y)), fminf(x.z, x.w));
+      high = fmaxf(fmaxf(high, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
+    };
+    uint32_t most, wild;
+    auto reduce = [&]() {
+      most = __reduce_max_sync(FULL, __float_as_uint(row.b_norm));  // norms by their bits
+      const uint32_t least = __reduce_min_sync(FULL, order_of(low)), top = __reduce_max_sync(FULL, order_of(high));
+      wild = __any_sync(FULL, row.wild);
+      if (lane == 0) sh.red[warp] = make_uint4(most, least, top, wild);
+      sync_row<T>();
+      const uint4 x = sh.red[lane % NW];
+      most = __reduce_max_sync(FULL, x.x);
+      low = from_order(__reduce_min_sync(FULL, x.y));
+      high = from_order(__reduce_max_sync(FULL, x.z));
+      wild = __any_sync(FULL, x.w != 0);
+    };
 #pragma unroll 2
     for (int v = tid; 4 * v < (CACHED ? 32 * words : nb); v += T) {
       const float4 x = 4 * v < nb ? read_four(v) : make_float4(none, none, none, none);
       if constexpr (CACHED) *reinterpret_cast<float4*>(cache + 4 * v) = x;
-      low = fminf(fminf(low, fminf(x.x, x.y)), fminf(x.z, x.w));
-      high = fmaxf(fmaxf(high, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
+      widen(x);
     }
-    uint32_t most = __reduce_max_sync(FULL, __float_as_uint(row.b_norm));  // norms by their bits
-    uint32_t least = __reduce_min_sync(FULL, order_of(low)), top = __reduce_max_sync(FULL, order_of(high));
-    if (lane == 0) sh.red[warp] = make_uint4(most, least, top, 0);
-    sync_row<T>();
-    const uint4 x = sh.red[lane % NW];
-    most = __reduce_max_sync(FULL, x.x);
-    least = __reduce_min_sync(FULL, x.y);
-    top = __reduce_max_sync(FULL, x.z);
-    off = eps * row.q_norm * __uint_as_float(most);
-    low = from_order(least);
-    high = from_order(top);
+    reduce();
+    const float norms = norm_of_q(row, wild) * fmaxf(__uint_as_float(most), wild ? LEAST_NORM : 0.f);
+    off = eps * norms;
+    if (wild && off < INFINITY) {
+      tame<T>(p, r, h, n, nb, row.norms, 2.f * norms, sh.q, CACHED ? cache : sc);
+      sync_row<T>();
+      for (int i = tid; i < BINS / 4; i += T) reinterpret_cast<int4*>(sh.hist[0])[i] = make_int4(0, 0, 0, 0);
+      low = INFINITY;
+      high = -INFINITY;
+      for (int v = tid; 4 * v < nb; v += T) widen(four(v));
+      reduce();
+    }
   }
-  const bool known = off < INFINITY;  // else a NaN or infinity is about, and every score is taken again
+  const bool known = off < INFINITY;  // else a NaN or infinity is among the queries, and every score is taken again
   auto choose = [&](int i) { atomicOr(&s_bits[i >> 5], 1u << (i & 31)); };
-  // the exact scores: the sums over heads, and a product with block i's bounds by a warp
-  auto sum_heads = [&](int begin, int step) {
-    const int G = p.Hq / p.Hkv;
-    for (int c = begin; c < D; c += step) {
-      const __nv_bfloat16* q = p.q + (static_cast<int64_t>(r) * p.Hq + h * G) * D + c;
-      double neg = 0.0, pos = 0.0;
-      for (int e0 = 0; e0 < G; e0 += 4) {  // four heads' loads in flight
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = e0 + e < G ? __bfloat162float(q[(e0 + e) * D]) : 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          neg += x[e] > 0.f ? 0.f : x[e];
-          pos += x[e] < 0.f ? 0.f : x[e];
-        }
-      }
-      sh.q[c] = neg;
-      sh.q[D + c] = pos;
-    }
-  };
-  auto load_bounds = [&](int i, uint32_t (&b)[8]) {  // words 32 k + lane of block i's
-    int id = p.block_table[static_cast<int64_t>(n) * p.max_blocks + i];
-    if (id < 0 || id >= p.num_blocks) id = 0;
-    const uint32_t* from = reinterpret_cast<const uint32_t*>(p.bounds + (static_cast<int64_t>(id) * p.Hkv + h) * 2 * D) + lane;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) b[k] = 32 * k < D ? from[32 * k] : 0u;
-  };
-  auto product = [&](const uint32_t (&b)[8]) {
-    double sum = 0.0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (32 * k >= D) break;
-      const float2 x = pair_of(b[k]);
-      const int c = 32 * k + lane;
-      sum = fma(sh.q[2 * c], static_cast<double>(x.x), fma(sh.q[2 * c + 1], static_cast<double>(x.y), sum));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-    return order_of(sum);
-  };
-  auto exact = [&](int i) {
+  auto exact = [&](int i) {  // block i's score in 64 bits, by a warp
     uint32_t b[8];
-    load_bounds(i, b);
-    return product(b);
+    load_bounds(p, row, i, b, lane);
+    return order_of(product(p, sh.q, b, lane));
   };
 
   // ---- Narrow the window [low, high] about the border, a bin of BINS at a time, until 32 blocks at most are in it.
@@ -1113,12 +1178,12 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
       unsigned todo = sh.among;
       for (int k = 0; k < warp && todo != 0; ++k) todo &= todo - 1;
       uint32_t b[8];
-      if (todo != 0) load_bounds(sh.at[__ffs(todo) - 1], b);
-      sum_heads(tid, T);
+      if (todo != 0) load_bounds(p, row, sh.at[__ffs(todo) - 1], b, lane);
+      sum_heads(p, row, sh.q, tid, T);
       sync_row<T>();
       for (bool first = true; todo != 0; first = false) {
         const int j = __ffs(todo) - 1;
-        const unsigned long long key = first ? product(b) : exact(sh.at[j]);
+        const unsigned long long key = first ? order_of(product(p, sh.q, b, lane)) : exact(sh.at[j]);
         if (lane == 0) sh.key[j] = key;
         for (int k = 0; k < NW && todo != 0; ++k) todo &= todo - 1;
       }
@@ -1203,9 +1268,9 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
       }
       uint32_t like[8], differs = 0;
       auto words_of = [&](int page, uint32_t (&x)[8]) {
-        const uint32_t* from = bounds + (static_cast<int64_t>(page) * p.Hkv + h) * D + lane;
+        const uint32_t* from = bounds + (static_cast<int64_t>(page) * p.Hkv + h) * p.d + lane;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = 32 * k < D ? from[32 * k] : 0u;
+        for (int k = 0; k < 8; ++k) x[k] = 32 * k < p.d ? from[32 * k] : 0u;
       };
       words_of(first, like);
       for (int w = warp; w < words; w += NW) {
@@ -1226,7 +1291,7 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
     unsigned long long key_at = 0, mask = 0;
     int left = places;
     if (score_again) {
-      sum_heads(tid, T);
+      sum_heads(p, row, sh.q, tid, T);
       for (int shift = 56; shift >= 0; shift -= 8) {
         clear();
         for (int w = warp; w < words; w += NW)
@@ -1289,13 +1354,16 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
   }
 }
 
-// The same by a warp that holds the scores in registers, 32 NR at most; `sc` may be shared memory.  False, and nothing done,
-// where there is more to it: NaN or infinities, many alike at the border, or no place but the kept blocks'.
+// The same by a warp that holds the scores in registers, 32 NR at most; wild tiles are tame.  norms: ||Q|| times the largest
+// ||b||.  False, and nothing done, where there is more to it: queries that are no finite numbers, many alike at the
+// border, or no place but the kept blocks'.
 template <int NR>
-__device__ __forceinline__ bool pick_warp(const SelectBlocksParams& p, const Row& row, const float* sc, float eps, PickShared& sh) {
+__device__ __forceinline__ bool pick_warp(const SelectBlocksParams& p, const Row& row, float norms, bool wild, float eps,
+                                          PickShared& sh) {
   constexpr int NW = (NR + 31) / 32;  // words of chosen blocks a lane: word 32 k + lane
   const int lane = threadIdx.x & 31, nb = row.nb, c0 = p.first, c1 = nb - p.last, want = p.K - p.first - p.last;
   if (want == 0) return false;
+  const float* sc = row.scores;
   const float none = __uint_as_float(0x7fffffffu);  // a NaN: neither above, below nor within a window
   float x[NR], low = INFINITY, high = -INFINITY;
 #pragma unroll
@@ -1317,7 +1385,7 @@ __device__ __forceinline__ bool pick_warp(const SelectBlocksParams& p, const Row
   }
   low = from_order(__reduce_min_sync(FULL, order_of(low)));
   high = from_order(__reduce_max_sync(FULL, order_of(high)));
-  const float off = eps * row.q_norm * __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(row.b_norm)));
+  const float off = eps * norms;
   if (!(off < INFINITY)) return false;
   unsigned bits[NW], in[NW];  // of this lane's scores: bit j % 32 of number j / 32; above the window, within it
   int open = 0, over = 0;     // how many are in the window; above it
@@ -1370,7 +1438,7 @@ __device__ __forceinline__ bool pick_warp(const SelectBlocksParams& p, const Row
 #pragma unroll
   for (int k = 0; k < NW; ++k) bits[k] = transpose_32x32(bits[k], lane);
   Border at = settle(sh, open, want - over, off, lane);
-  if (at.among != 0 && off != 0.f) refine(p, row, off / eps, at, lane);
+  if (at.among != 0 && off != 0.f && !wild) refine(p, row, norms, at, lane);  // (wild blocks are past its range)
   bool chosen = at.sure || at.close;
   if (at.among != 0) {
     // where the bound is 0 every score is
@@ -1406,7 +1474,7 @@ __device__ __forceinline__ bool pick_warp(const SelectBlocksParams& p, const Row
 
 // A warp a row and KV head, four a CTA
 template <int NR>
-__global__ void __launch_bounds__(128, NR == 16 ? 6 : NR == 32 ? 5 : 4) select_warps_kernel(const SelectBlocksParams p, const Scratch ws) {
+__global__ void __launch_bounds__(128, NR == 16 ? 6 : NR == 32 ? 5 : 4) select_warps_kernel(const __grid_constant__ SelectBlocksParams p, const Scratch ws) {
   extern __shared__ __align__(16) uint32_t s_words[];
   __shared__ PickShared shared[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1425,19 +1493,27 @@ __global__ void __launch_bounds__(128, NR == 16 ? 6 : NR == 32 ? 5 : 4) select_w
     choose_all<32>(p, at, row.nb);
     return;
   }
-  const float* norms = ws.b_norm + (static_cast<int64_t>(row.n) * p.Hkv + row.h) * ws.tiles;
+  row.norms = ws.b_norm + (static_cast<int64_t>(row.n) * p.Hkv + row.h) * ws.tiles;
   row.q_norm = ws.q_norm[at];
   row.b_norm = 0.f;
+  row.wild = false;
 #pragma unroll
   for (int k = 0; k < (NR * 2 + 31) / 32; ++k)
-    if (32 * k + lane < (row.nb + 15) / 16) row.b_norm = fmaxf(row.b_norm, norms[32 * k + lane]);
+    if (32 * k + lane < (row.nb + 15) / 16) count_norm(row, row.norms[32 * k + lane]);
   row.scores = ws.scores + at * ws.stride;
-  if (!pick_warp<NR>(p, row, row.scores, ws.eps, shared[warp]))
+  const bool wild = __any_sync(FULL, row.wild);
+  const float most = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(row.b_norm)));
+  const float norms = norm_of_q(row, wild) * fmaxf(most, wild ? LEAST_NORM : 0.f);
+  if (wild && norms < INFINITY) {
+    tame<32>(p, row.r, row.h, row.n, row.nb, row.norms, 2.f * norms, shared[warp].q, row.scores);
+    __syncwarp();
+  }
+  if (!pick_warp<NR>(p, row, norms, wild, ws.eps, shared[warp]))
     pick<32, false>(p, row, ws.eps, shared[warp], s_words + warp * cache_at(p.max_blocks));
 }
 
 template <int T, bool CACHED>
-__global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const SelectBlocksParams p, const Scratch ws) {
+__global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const __grid_constant__ SelectBlocksParams p, const Scratch ws) {
   extern __shared__ __align__(16) uint32_t s_bits[];
   __shared__ PickShared shared;
   Row row;
@@ -1452,10 +1528,11 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
     choose_all<T>(p, blockIdx.x, row.nb);
     return;
   }
-  const float* norms = ws.b_norm + (static_cast<int64_t>(row.n) * p.Hkv + row.h) * ws.tiles;
+  row.norms = ws.b_norm + (static_cast<int64_t>(row.n) * p.Hkv + row.h) * ws.tiles;
   row.q_norm = ws.q_norm[blockIdx.x];
   row.b_norm = 0.f;
-  for (int i = threadIdx.x; i < (row.nb + 15) / 16; i += T) row.b_norm = fmaxf(row.b_norm, norms[i]);
+  row.wild = false;
+  for (int i = threadIdx.x; i < (row.nb + 15) / 16; i += T) count_norm(row, row.norms[i]);
   row.scores = ws.scores + static_cast<int64_t>(blockIdx.x) * ws.stride;
   pick<T, CACHED>(p, row, ws.eps, shared, s_bits);
 }
@@ -1464,12 +1541,12 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const Sele
 // warp takes 16 blocks at a time, their bounds from HBM straight to registers, in the order of the matrix product's left
 // operand.
 template <int D, int T>
-__global__ void __launch_bounds__(T, 512 / T) select_one_kernel(const SelectBlocksParams p, float eps) {
+__global__ void __launch_bounds__(T, 512 / T) select_one_kernel(const __grid_constant__ SelectBlocksParams p, float eps) {
   constexpr int NW = T / 32, KK = 2 * D / 32, PART = KK < 8 ? KK : 8, PARTS = KK / PART;
   extern __shared__ __align__(16) uint32_t s_bits[];
   __shared__ PickShared shared;
   __shared__ __align__(16) uint32_t s_qb[KK * 2 * 16];  // Q-, Q+ as two bf16 numbers each: [KK][2 columns][16 words]
-  __shared__ float s_squares[NW];
+  __shared__ float s_squares[NW], s_norms[ONE_BLOCKS / 16];  // s_norms: infinite for wild tiles, else 0
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   Row row;
   const int n = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
@@ -1544,6 +1621,7 @@ __global__ void __launch_bounds__(T, 512 / T) select_one_kernel(const SelectBloc
 #pragma unroll
   for (int i = 0; i < NW; ++i) squares += s_squares[i];
   row.q_norm = sqrtf(squares);
+  row.norms = s_norms;
   row.b_norm = 0.f;
 
   float* cache = reinterpret_cast<float*>(s_bits + cache_at(p.max_blocks));
@@ -1580,16 +1658,46 @@ __global__ void __launch_bounds__(T, 512 / T) select_one_kernel(const SelectBloc
     for (int e = 0; e < 2; ++e) {
       norm[e] += __shfl_xor_sync(FULL, norm[e], 1);
       norm[e] += __shfl_xor_sync(FULL, norm[e], 2);
-      if (!(norm[e] < INFINITY)) norm[e] = INFINITY;  // NaN too
-      if (blk + 8 * e < nb) row.b_norm = fmaxf(row.b_norm, norm[e]);
+      if (!(norm[e] < MOST_SQUARES)) norm[e] = INFINITY;  // NaN too
+      if (competes(p, blk + 8 * e, nb)) row.b_norm = fmaxf(row.b_norm, norm[e]);
     }
     tile = next;
     id = next_id;
     if (tile * 16 < nb) load(id, 0);
   }
+  row.wild = !(row.b_norm < INFINITY);
+  if (__syncthreads_or(row.wild)) {  // rare: which tiles, and the norms of the others; a block a thread
+    for (int i = threadIdx.x; i < (nb + 15) / 16; i += T) s_norms[i] = 0.f;
+    row.b_norm = 0.f;
+    row.wild = false;
+    __syncthreads();
+    for (int i = p.first + threadIdx.x; i < nb - p.last; i += T) {
+      int page = p.block_table[static_cast<int64_t>(n) * p.max_blocks + i];
+      if (page < 0 || page >= p.num_blocks) page = 0;
+      const uint4* from = reinterpret_cast<const uint4*>(p.bounds + (static_cast<int64_t>(page) * p.Hkv + h) * 2 * D);
+      float norm = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < D / 4; ++k) {
+        const uint4 x = from[k];
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float2 y = pair_of(w[c]);
+          norm = fmaf(y.x, y.x, fmaf(y.y, y.y, norm));
+        }
+      }
+      if (norm < MOST_SQUARES) {
+        row.b_norm = fmaxf(row.b_norm, norm);
+      } else {
+        row.wild = true;
+        s_norms[i / 16] = INFINITY;
+      }
+    }
+    // a tile's blocks are wild together: the norm of one that is not by itself does no harm
+    __syncthreads();
+  }
   // the sum of squares may have been an eighth too small
   row.b_norm = fmaxf(1.1f * sqrtf(row.b_norm), LEAST_NORM);
-  __syncthreads();
   pick<T, true>(p, row, eps, shared, s_bits);
 }
 
