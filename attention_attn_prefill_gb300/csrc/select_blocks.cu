@@ -1194,9 +1194,11 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
       if (takes(at, key)) choose(at.block);
     }
   } else {
-    // ---- Many at the border, or none: NaN or infinities, pages that are alike, or no place but the kept ones'.  The
-    // border digit by digit, of the scores and then, among those that they leave open, of the exact scores, each computed
-    // again for every digit.
+    // ---- Many at the border, or none: queries that are no finite numbers, pages that are alike, or no place but the kept
+    // ones'.  The border digit by digit, of the scores and then, among those that they leave open, of the exact scores: of their
+    // upper halves, which take the scores' places, and of the lower halves of those that then tie.  512 rows of 2048 pages,
+    // 8 heads, of which one page's bounds are 10^4 times the others': 14 ms (125 where each digit had every score computed
+    // again).
     int* hist = sh.digits;
     auto digit = [&](int left) {  // the one that holds the left-th largest
       sync_row<T>();
@@ -1230,26 +1232,30 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
       }
     }
     const float at = from_order(border), most = known ? at + 2.f * off : INFINITY, least = known ? at - 2.f * off : -INFINITY;
-    auto undecided = [&](int i) { return want > 0 && i >= c0 && i < c1 && (!known || (score(i) <= most && score(i) >= least)); };
     sync_row<T>();
     if (tid == 0) sh.open[0] = sh.over[0] = 0;
     sync_row<T>();
     int ins = 0, opens = 0;
     for (int w = warp; w < words; w += NW) {
       const int i = 32 * w + lane;
-      const bool kept = i < nb && (i < c0 || i >= c1), in = known && want > 0 && i >= c0 && i < c1 && score(i) > most;
-      opens += __popc(__ballot_sync(FULL, undecided(i)));
+      const bool mine = want > 0 && competing(i), kept = i < nb && !competing(i), in = mine && known && score(i) > most;
+      const unsigned open_bits = __ballot_sync(FULL, mine && !in && (!known || score(i) >= least));
       const unsigned in_bits = __ballot_sync(FULL, in), kept_bits = __ballot_sync(FULL, kept);
       ins += __popc(in_bits);
-      if (lane == 0) s_bits[w] = in_bits | kept_bits;
+      opens += __popc(open_bits);
+      if (lane == 0) {
+        s_bits[w] = in_bits | kept_bits;
+        ties[w] = open_bits;
+      }
     }
     if (lane == 0) {
       atomicAdd(&sh.over[0], ins);
       atomicAdd(&sh.open[0], opens);
     }
     sync_row<T>();
-    const int places = want - sh.over[0];
-    bool score_again = places < sh.open[0] && !(known && off == 0.f);  // with a bound of 0 every score is 0
+    int left = want - sh.over[0];
+    // with a bound of 0 every score is 0, with a NaN among the queries' sums every score is one
+    bool score_again = left < sh.open[0] && !(known && off == 0.f) && row.q_norm == row.q_norm;
     if (score_again) {
       // Pages with the same bounds have the same score, and a cache that nothing was written to has no others: 512 rows of
       // 2048 such pages, 8 heads, took 126 ms by exact scores.
@@ -1262,10 +1268,8 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
         return id;
       };
       int first = -1;  // the lowest of them
-      for (int w = 0; first < 0; ++w) {
-        const unsigned todo = __ballot_sync(FULL, undecided(32 * w + lane));
-        if (todo != 0) first = page_of(32 * w + __ffs(todo) - 1);
-      }
+      for (int w = 0; first < 0; ++w)
+        if (ties[w] != 0) first = page_of(32 * w + __ffs(ties[w]) - 1);
       uint32_t like[8], differs = 0;
       auto words_of = [&](int page, uint32_t (&x)[8]) {
         const uint32_t* from = bounds + (static_cast<int64_t>(page) * p.Hkv + h) * p.d + lane;
@@ -1274,9 +1278,8 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
       };
       words_of(first, like);
       for (int w = warp; w < words; w += NW) {
-        const bool mine = undecided(32 * w + lane);
-        const int page = mine ? page_of(32 * w + lane) : first;
-        for (unsigned todo = __ballot_sync(FULL, mine); todo != 0; todo &= todo - 1) {
+        const int page = ties[w] >> lane & 1 ? page_of(32 * w + lane) : first;
+        for (unsigned todo = ties[w]; todo != 0; todo &= todo - 1) {
           uint32_t x[8];
           words_of(__shfl_sync(FULL, page, __ffs(todo) - 1), x);
 #pragma unroll
@@ -1288,37 +1291,38 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
       sync_row<T>();
       score_again = sh.among != 0;
     }
-    unsigned long long key_at = 0, mask = 0;
-    int left = places;
-    if (score_again) {
-      sum_heads(p, row, sh.q, tid, T);
-      for (int shift = 56; shift >= 0; shift -= 8) {
+    if (score_again) sum_heads(p, row, sh.q, tid, T);
+    uint32_t* keys = reinterpret_cast<uint32_t*>(CACHED ? cache : sc);
+    for (int half = 0; score_again && half < 2; ++half) {
+      sync_row<T>();
+      for (int w = warp; w < words; w += NW)
+        for (unsigned todo = ties[w]; todo != 0; todo &= todo - 1) {
+          const int i = 32 * w + __ffs(todo) - 1;
+          const unsigned long long key = exact(i);
+          if (lane == 0) keys[i] = static_cast<uint32_t>(half == 0 ? key >> 32 : key);
+        }
+      uint32_t key_at = 0, mask = 0;
+      for (int shift = 24; shift >= 0; shift -= 8) {
         clear();
         for (int w = warp; w < words; w += NW)
-          for (unsigned todo = __ballot_sync(FULL, undecided(32 * w + lane)); todo != 0; todo &= todo - 1) {
-            const unsigned long long key = exact(32 * w + __ffs(todo) - 1);
-            if (lane == 0 && ((key ^ key_at) & mask) == 0) atomicAdd(&hist[key >> shift & 255], 1);
+          if (ties[w] >> lane & 1) {
+            const uint32_t u = keys[32 * w + lane];
+            if (((u ^ key_at) & mask) == 0) atomicAdd(&hist[u >> shift & 255], 1);
           }
         digit(left);
-        key_at |= static_cast<unsigned long long>(sh.digit) << shift;
-        mask |= 255ull << shift;
+        key_at |= static_cast<uint32_t>(sh.digit) << shift;
+        mask |= 255u << shift;
         left -= sh.above;
       }
-    }
-    for (int w = warp; w < words; w += NW) {
-      const unsigned todo = __ballot_sync(FULL, undecided(32 * w + lane));
-      unsigned above = 0, tie = todo;
-      if (score_again) {
-        tie = 0;
-        for (unsigned x = todo; x != 0; x &= x - 1) {
-          const unsigned long long key = exact(32 * w + __ffs(x) - 1);
-          if (key > key_at) above |= x & -x;
-          else if (key == key_at) tie |= x & -x;
+      score_again = left < hist[sh.digit];  // of those that tie, or all of them have a place
+      for (int w = warp; w < words; w += NW) {
+        const bool mine = ties[w] >> lane & 1;
+        const uint32_t u = mine ? keys[32 * w + lane] : 0u;
+        const unsigned above = __ballot_sync(FULL, mine && u > key_at), tie = __ballot_sync(FULL, mine && u == key_at);
+        if (lane == 0) {
+          s_bits[w] |= above;
+          ties[w] = tie;
         }
-      }
-      if (lane == 0) {
-        s_bits[w] |= above;
-        ties[w] = tie;
       }
     }
     sync_row<T>();

@@ -87,6 +87,33 @@ def test_select_beside_odd_pages(attn, gpu, name, kind):
     assert attn.device_status() == 0
 
 
+@pytest.mark.parametrize("kind", ["one large", "two kinds", "close", "nan queries", "infinite queries"])
+@pytest.mark.parametrize("name", list(SHAPES))
+def test_select_where_many_are_close_to_the_border(attn, gpu, name, kind):
+    """More pages than a warp settles lie within the error of the border: a page so large, though no score passes its range,
+    that all are unsure; two kinds of pages, each many times; pages that differ in a part of 10^11 to 10^13 of their scores; queries whose sums
+    are no numbers, or infinite."""
+    q, b, table, lens, cu, rows, K = case = _case(name, gpu)
+    width = table.shape[1]
+    gen = torch.Generator(device=gpu).manual_seed(3)
+    if kind == "one large":
+        b[table[:, width // 3].long()] *= 2.0 ** 14
+    elif kind == "two kinds":
+        b[0::2], b[1::2] = b[0].clone(), b[1].clone()
+    elif kind == "close":
+        b[:] = b[0].clone()
+        b[:, :, :, 7] = torch.randn((b.shape[0], b.shape[1], 1), generator=gen, device=gpu).to(torch.bfloat16)
+        q[:, :, 7] = q[:, :, 7].abs().clamp(min=0.1) * 1e-10
+    elif kind == "nan queries":
+        q[::2, 0, 5] = math.nan
+    else:
+        q[::2, 0, 5], q[1::2, 1, 6] = math.inf, -math.inf
+    got = _call(attn, case)
+    for r in sorted({0, 1 % got.shape[0], rows // 2, rows - 1, got.shape[0] // 2, got.shape[0] - 1}):
+        assert torch.equal(got[r], _wanted(case, r)), r
+    assert attn.device_status() == 0
+
+
 def _micros(call):
     for _ in range(3):
         call()
@@ -115,3 +142,15 @@ def test_an_odd_page_does_not_hold_up_the_others(attn, gpu, name):
             _spoil(case, kind, where)
             taken = _micros(lambda: _call(attn, case))
             assert taken < 6 * plain + 60, (where, kind, taken, plain)
+
+
+@pytest.mark.parametrize("name", ["a warp a row, wide", "chunk"])
+def test_exact_scores_are_computed_once(attn, gpu, name):
+    """Where all pages are unsure their scores in 64 bits take 2 to 4 ns a row, head and page of a full GPU, for their upper halves
+    and for the lower ones of a few; 15 where each of eight digits took them again."""
+    case = _case(name, gpu)
+    N, rows, width, H, _, _ = SHAPES[name]
+    case[1][case[2][:, width // 3].long()] *= 2.0 ** 14
+    taken = _micros(lambda: _call(attn, case))
+    each = taken * 1e3 / (N * rows * H * width)
+    assert each < 7, each
