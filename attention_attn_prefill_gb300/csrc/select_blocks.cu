@@ -995,13 +995,13 @@ __device__ __forceinline__ double product(const SelectBlocksParams& p, const dou
 }
 
 // Wild tiles, those with a bound that is no finite number or too large, would leave every score of the row unsure.  Their
-// blocks are scored in 64 bits, and take part with that score as a float, cut to what is above or below all others':
-// `most`, twice ||Q|| times the largest norm of the others.  That is off by less than the others' bound, keeps the order among wild
-// blocks, and those that it makes equal are told apart by exact scores, like all that are close to the border.  By all
-// threads of the row, between two barriers.
+// blocks whose norm is above `limit`, the largest one of the other tiles, are scored in 64 bits, and take part with that score as a
+// float, cut to what is above or below all others': `most`, twice ||Q|| times the limit.  That is off by less than the
+// others' bound, keeps the order among wild blocks, and those that it makes equal are told apart by exact scores, like all that
+// are close to the border.  By all threads of the row, between two barriers.
 template <int T>
-__device__ __noinline__ void tame(const SelectBlocksParams& p, int r, int h, int n, int nb, const float* norms, float most,
-                                  double* sums, float* scores) {
+__device__ __noinline__ void tame(const SelectBlocksParams& p, int r, int h, int n, int nb, const float* norms, float limit,
+                                  float most, double* sums, float* scores) {
   Row row;  // (a caller's would have to lie in memory)
   row.r = r;
   row.h = h;
@@ -1016,6 +1016,15 @@ __device__ __noinline__ void tame(const SelectBlocksParams& p, int r, int h, int
       if (!competes(p, i, nb)) continue;
       uint32_t b[8];
       load_bounds(p, row, i, b, lane);
+      float squares = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 x = pair_of(b[k]);
+        squares = fmaf(x.x, x.x, fmaf(x.y, x.y, squares));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) squares += __shfl_xor_sync(FULL, squares, o);
+      if (sqrtf(squares) < 0.999f * limit) continue;  // as sure as the others' scores
       const double sum = product(p, sums, b, lane);
       if (lane == 0) scores[i] = sum < most ? (sum > -most ? static_cast<float>(sum) : -most) : most;  // a NaN is the highest
     }
@@ -1088,10 +1097,10 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
       widen(x);
     }
     reduce();
-    const float norms = norm_of_q(row, wild) * fmaxf(__uint_as_float(most), wild ? LEAST_NORM : 0.f);
+    const float b_norm = fmaxf(__uint_as_float(most), wild ? LEAST_NORM : 0.f), norms = norm_of_q(row, wild) * b_norm;
     off = eps * norms;
     if (wild && off < INFINITY) {
-      tame<T>(p, r, h, n, nb, row.norms, 2.f * norms, sh.q, CACHED ? cache : sc);
+      tame<T>(p, r, h, n, nb, row.norms, b_norm, 2.f * norms, sh.q, CACHED ? cache : sc);
       sync_row<T>();
       for (int i = tid; i < BINS / 4; i += T) reinterpret_cast<int4*>(sh.hist[0])[i] = make_int4(0, 0, 0, 0);
       low = INFINITY;
@@ -1507,9 +1516,9 @@ __global__ void __launch_bounds__(128, NR == 16 ? 6 : NR == 32 ? 5 : 4) select_w
   row.scores = ws.scores + at * ws.stride;
   const bool wild = __any_sync(FULL, row.wild);
   const float most = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(row.b_norm)));
-  const float norms = norm_of_q(row, wild) * fmaxf(most, wild ? LEAST_NORM : 0.f);
+  const float b_norm = fmaxf(most, wild ? LEAST_NORM : 0.f), norms = norm_of_q(row, wild) * b_norm;
   if (wild && norms < INFINITY) {
-    tame<32>(p, row.r, row.h, row.n, row.nb, row.norms, 2.f * norms, shared[warp].q, row.scores);
+    tame<32>(p, row.r, row.h, row.n, row.nb, row.norms, b_norm, 2.f * norms, shared[warp].q, row.scores);
     __syncwarp();
   }
   if (!pick_warp<NR>(p, row, norms, wild, ws.eps, shared[warp]))
