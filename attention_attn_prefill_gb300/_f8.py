@@ -109,6 +109,8 @@ def cache_gather_f8(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: to
     if (k_out.dtype is not _BF16 or v_out.dtype is not _BF16 or k_out.get_device() != dev
             or v_out.get_device() != dev or not k_out.is_contiguous() or not v_out.is_contiguous()):
         _explain(dev, (k_out, _BF16, "k_out"), (v_out, _BF16, "v_out"))
+    if N == 0:  # a step without sequences
+        return k_out, v_out
     _run("attn_cache_gather_f8", dev, stream, cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
          k_out.data_ptr(), v_out.data_ptr(), N, Hkv, d, PAGE_TOKENS, max_blocks, num_blocks)
     return k_out, v_out
@@ -137,6 +139,8 @@ def decode_paged_f8(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
         _explain(dev, (q, _BF16, "q"))
     out, lse, workspace = _outputs(dev, q, out, lse, (N, Hq), return_lse, workspace,
                                    _decode_ws.get((dev, d)) or decode_f8_workspace_bytes(d, dev), stream)
+    if N == 0:  # a step without sequences
+        return out, lse
     _run("attn_decode_paged_f8", dev, stream, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
          seq_lens.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), N, Hq, Hkv, d, PAGE_TOKENS,
          max_blocks, num_blocks, d ** -0.5 if scale is None else scale, workspace.data_ptr(), workspace.numel())
