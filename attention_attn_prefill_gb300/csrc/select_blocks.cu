@@ -994,14 +994,14 @@ __device__ __forceinline__ double product(const SelectBlocksParams& p, const dou
   return sum;
 }
 
-// Wild tiles, those with a bound that is no finite number or too large, would leave every score of the row unsure.  Their
+// Wild tiles, those with a bound that is no finite number or too large (of a norm from `cut` on), would leave every score of the row unsure.  Their
 // blocks whose norm is above `limit`, the largest one of the other tiles, are scored in 64 bits, and take part with that score as a
 // float, cut to what is above or below all others': `most`, twice ||Q|| times the limit.  That is off by less than the
 // others' bound, keeps the order among wild blocks, and those that it makes equal are told apart by exact scores, like all that
 // are close to the border.  By all threads of the row, between two barriers.
 template <int T>
-__device__ __noinline__ void tame(const SelectBlocksParams& p, int r, int h, int n, int nb, const float* norms, float limit,
-                                  float most, double* sums, float* scores) {
+__device__ __noinline__ void tame(const SelectBlocksParams& p, int r, int h, int n, int nb, const float* norms, float cut,
+                                  float limit, float most, double* sums, float* scores) {
   Row row;  // (a caller's would have to lie in memory)
   row.r = r;
   row.h = h;
@@ -1011,7 +1011,7 @@ __device__ __noinline__ void tame(const SelectBlocksParams& p, int r, int h, int
   sum_heads(p, row, sums, tid, T);
   sync_row<T>();
   for (int tile = warp; 16 * tile < nb; tile += T / 32) {
-    if (norms[tile] < INFINITY) continue;
+    if (norms[tile] < cut) continue;
     for (int i = 16 * tile; i < 16 * tile + 16; ++i) {
       if (!competes(p, i, nb)) continue;
       uint32_t b[8];
@@ -1031,10 +1031,52 @@ __device__ __noinline__ void tame(const SelectBlocksParams& p, int r, int h, int
   }
 }
 
+// Where too many blocks are unsure because a few tiles have norms far above the others' (16 times their geometric mean, at
+// least), those are taken for wild ones.  Returns ||Q|| times the largest norm of the others, or 0 where there are none such.
+// 512 rows of 2048 pages, 8 heads, of which one has bounds 10^4 times the others': 0.3 ms, by exact scores of all 14.4.
+template <int T>
+__device__ __noinline__ float leave_out(const SelectBlocksParams& p, int r, int h, int n, int nb, const float* norms, float q_norm,
+                                        PickShared& sh, float* scores) {
+  constexpr int NW = T / 32;
+  const int tid = T == 32 ? threadIdx.x & 31 : threadIdx.x, warp = tid >> 5, lane = tid & 31, tiles = (nb + 15) / 16;
+  auto reduce = [&](int a, int b, uint32_t most) {  // two sums and a maximum
+    a = __reduce_add_sync(FULL, a);
+    b = __reduce_add_sync(FULL, b);
+    most = __reduce_max_sync(FULL, most);
+    sync_row<T>();
+    if (lane == 0) sh.red[warp] = make_uint4(a, b, most, 0);
+    sync_row<T>();
+    const uint4 x = lane < NW ? sh.red[lane] : make_uint4(0, 0, 0, 0);
+    return make_int3(__reduce_add_sync(FULL, static_cast<int>(x.x)), __reduce_add_sync(FULL, static_cast<int>(x.y)),
+                     static_cast<int>(__reduce_max_sync(FULL, x.z)));
+  };
+  int sum = 0, count = 0, large = 0;
+  for (int i = tid; i < tiles; i += T)
+    if (norms[i] > LEAST_NORM && norms[i] < INFINITY) {
+      sum += static_cast<int>(__float_as_uint(norms[i]) >> 23);
+      ++count;
+    }
+  const int3 all = reduce(sum, count, 0);
+  if (all.y == 0) return 0.f;
+  const float cut = __uint_as_float(static_cast<uint32_t>(min(all.x / all.y + 5, 254)) << 23);
+  float most = LEAST_NORM;
+  for (int i = tid; i < tiles; i += T) {
+    if (norms[i] >= cut) large += norms[i] < INFINITY ? 1 : 0;
+    else most = fmaxf(most, norms[i]);
+  }
+  const int3 rest = reduce(large, 0, __float_as_uint(most));
+  if (rest.x == 0 || 16 * rest.x > tiles) return 0.f;
+  most = __int_as_float(rest.z);
+  const float bound = (q_norm < LEAST_NORM ? LEAST_NORM : q_norm) * most;
+  tame<T>(p, r, h, n, nb, norms, cut, most, 2.f * bound, sh.q, scores);
+  return bound;
+}
+
 // Picks the blocks of a row and KV head, by a CTA of T threads.  CACHED: shared memory holds its scores, else they are read
-// again and again.  s_bits: [words] chosen blocks, [words] ties; the scores from word cache_at on.
-template <int T, bool CACHED>
-__device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row, float eps, PickShared& sh, uint32_t* s_bits) {
+// again and again.  s_bits: [words] chosen blocks, [words] ties; the scores from word cache_at on.  EASY: false, and nothing
+// done, where there is more to it than a few blocks about the border.
+template <int T, bool CACHED, bool EASY>
+__device__ __forceinline__ bool pick(const SelectBlocksParams& p, const Row& row, float eps, PickShared& sh, uint32_t* s_bits) {
   constexpr int NW = T / 32;
   const int nb = row.nb, K = p.K, r = row.r, h = row.h, n = row.n;
   const int tid = T == 32 ? threadIdx.x & 31 : threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1072,41 +1114,46 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
     else return read_four(v);
   };
   float low = INFINITY, high = -INFINITY, off;
-  {
-    auto widen = [&](const float4& x) {
-      low = fminf(fminf(low, fminf(x.x, x.y)), fminf(x.z, x.w));
-      high = fmaxf(fmaxf(high, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
-    };
-    uint32_t most, wild;
-    auto reduce = [&]() {
-      most = __reduce_max_sync(FULL, __float_as_uint(row.b_norm));  // norms by their bits
-      const uint32_t least = __reduce_min_sync(FULL, order_of(low)), top = __reduce_max_sync(FULL, order_of(high));
-      wild = __any_sync(FULL, row.wild);
-      if (lane == 0) sh.red[warp] = make_uint4(most, least, top, wild);
-      sync_row<T>();
-      const uint4 x = sh.red[lane % NW];
-      most = __reduce_max_sync(FULL, x.x);
-      low = from_order(__reduce_min_sync(FULL, x.y));
-      high = from_order(__reduce_max_sync(FULL, x.z));
-      wild = __any_sync(FULL, x.w != 0);
-    };
-#pragma unroll 2
-    for (int v = tid; 4 * v < (CACHED ? 32 * words : nb); v += T) {
-      const float4 x = 4 * v < nb ? read_four(v) : make_float4(none, none, none, none);
-      if constexpr (CACHED) *reinterpret_cast<float4*>(cache + 4 * v) = x;
-      widen(x);
-    }
+  uint32_t most, wild;
+  auto widen = [&](const float4& x) {
+    low = fminf(fminf(low, fminf(x.x, x.y)), fminf(x.z, x.w));
+    high = fmaxf(fmaxf(high, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
+  };
+  auto reduce = [&]() {
+    most = __reduce_max_sync(FULL, __float_as_uint(row.b_norm));  // norms by their bits
+    const uint32_t least = __reduce_min_sync(FULL, order_of(low)), top = __reduce_max_sync(FULL, order_of(high));
+    wild = __any_sync(FULL, row.wild);
+    if (lane == 0) sh.red[warp] = make_uint4(most, least, top, wild);
+    sync_row<T>();
+    const uint4 x = sh.red[lane % NW];
+    most = __reduce_max_sync(FULL, x.x);
+    low = from_order(__reduce_min_sync(FULL, x.y));
+    high = from_order(__reduce_max_sync(FULL, x.z));
+    wild = __any_sync(FULL, x.w != 0);
+  };
+  auto scores_changed = [&]() {
+    sync_row<T>();
+    for (int i = tid; i < BINS / 2; i += T) reinterpret_cast<int4*>(sh.hist[0])[i] = make_int4(0, 0, 0, 0);
+    if (tid < 2) sh.open[tid] = sh.over[tid] = 0;
+    low = INFINITY;
+    high = -INFINITY;
+    for (int v = tid; 4 * v < nb; v += T) widen(four(v));
     reduce();
+  };
+#pragma unroll 2
+  for (int v = tid; 4 * v < (CACHED ? 32 * words : nb); v += T) {
+    const float4 x = 4 * v < nb ? read_four(v) : make_float4(none, none, none, none);
+    if constexpr (CACHED) *reinterpret_cast<float4*>(cache + 4 * v) = x;
+    widen(x);
+  }
+  reduce();
+  {
     const float b_norm = fmaxf(__uint_as_float(most), wild ? LEAST_NORM : 0.f), norms = norm_of_q(row, wild) * b_norm;
     off = eps * norms;
+    if (EASY && (wild || !(off < INFINITY) || want == 0)) return false;
     if (wild && off < INFINITY) {
-      tame<T>(p, r, h, n, nb, row.norms, b_norm, 2.f * norms, sh.q, CACHED ? cache : sc);
-      sync_row<T>();
-      for (int i = tid; i < BINS / 4; i += T) reinterpret_cast<int4*>(sh.hist[0])[i] = make_int4(0, 0, 0, 0);
-      low = INFINITY;
-      high = -INFINITY;
-      for (int v = tid; 4 * v < nb; v += T) widen(four(v));
-      reduce();
+      tame<T>(p, r, h, n, nb, row.norms, INFINITY, b_norm, 2.f * norms, sh.q, CACHED ? cache : sc);
+      scores_changed();
     }
   }
   const bool known = off < INFINITY;  // else a NaN or infinity is among the queries, and every score is taken again
@@ -1121,58 +1168,67 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
   // A score far from the others (a first page's, say) costs a round.
   bool few = false;
   int open = 0, over = 0;  // in the window; above it
-  for (int round = 0; known && want > 0 && !few; ++round) {
-    int* hist = sh.hist[round & 1];
-    const float range = high - low, per_step = (4 * BINS - 1) / range;
-    if (!(range < INFINITY && per_step < INFINITY)) break;  // all alike, or past float32
-    auto count = [&](float x) { count_step(hist, x, low, high, per_step); };
-    for (int v = tid; 4 * v < nb; v += T) {
-      const float4 x = four(v);
-      count(x.x);
-      count(x.y);
-      count(x.z);
-      count(x.w);
-    }
-    sync_row<T>();
-    // a warp finds the bin of the border, each for itself where they are few: lane 0 holds the highest
-    int bin = -1;
-    if (NW <= 8 || warp == 0) bin = border_bin(hist, over, want, lane);
-    if constexpr (NW > 8) {
-      if (tid == 0) sh.digit = bin;
-      sync_row<T>();
-      bin = sh.digit;
-    }
-    narrow(bin, range, off, low, high);
-    int above_high = 0;
-    for (int w = warp; w < words; w += NW) {
-      const float x = score(32 * w + lane);
-      const bool above = x > high;
-      if (x >= low && !above) {
-        const int k = atomicAdd(&sh.open[round & 1], 1);
-        if (k < 32) {
-          sh.at[k] = 32 * w + lane;
-          sh.score[k] = x;
-        }
+  for (bool tried = false; known && want > 0; tried = true) {
+    for (int round = 0; !few; ++round) {
+      int* hist = sh.hist[round & 1];
+      const float range = high - low, per_step = (4 * BINS - 1) / range;
+      if (!(range < INFINITY && per_step < INFINITY)) break;  // all alike, or past float32
+      auto count = [&](float x) { count_step(hist, x, low, high, per_step); };
+      for (int v = tid; 4 * v < nb; v += T) {
+        const float4 x = four(v);
+        count(x.x);
+        count(x.y);
+        count(x.z);
+        count(x.w);
       }
-      const unsigned bits = __ballot_sync(FULL, above);
-      above_high += __popc(bits);
-      if (lane == 0) s_bits[w] = bits;
-    }
-    if (lane == 0 && above_high > 0) atomicAdd(&sh.over[round & 1], above_high);
-    sync_row<T>();
-    open = sh.open[round & 1];
-    over = sh.over[round & 1];
-    few = open <= 32;
-    if (!few) {
-      if (!(high - low < 0.5f * range)) break;  // the error's width: they may as well be alike
-      const int other = (round & 1) ^ 1;
-      for (int i = tid; i < BINS; i += T) sh.hist[other][i] = 0;
       sync_row<T>();
-      if (tid == 0) sh.open[round & 1] = sh.over[round & 1] = 0;
+      // a warp finds the bin of the border, each for itself where they are few: lane 0 holds the highest
+      int bin = -1;
+      if (NW <= 8 || warp == 0) bin = border_bin(hist, over, want, lane);
+      if constexpr (NW > 8) {
+        if (tid == 0) sh.digit = bin;
+        sync_row<T>();
+        bin = sh.digit;
+      }
+      narrow(bin, range, off, low, high);
+      int above_high = 0;
+      for (int w = warp; w < words; w += NW) {
+        const float x = score(32 * w + lane);
+        const bool above = x > high;
+        if (x >= low && !above) {
+          const int k = atomicAdd(&sh.open[round & 1], 1);
+          if (k < 32) {
+            sh.at[k] = 32 * w + lane;
+            sh.score[k] = x;
+          }
+        }
+        const unsigned bits = __ballot_sync(FULL, above);
+        above_high += __popc(bits);
+        if (lane == 0) s_bits[w] = bits;
+      }
+      if (lane == 0 && above_high > 0) atomicAdd(&sh.over[round & 1], above_high);
+      sync_row<T>();
+      open = sh.open[round & 1];
+      over = sh.over[round & 1];
+      few = open <= 32;
+      if (!few) {
+        if (!(high - low < 0.5f * range)) break;  // the error's width: they may as well be alike
+        const int other = (round & 1) ^ 1;
+        for (int i = tid; i < BINS; i += T) sh.hist[other][i] = 0;
+        sync_row<T>();
+        if (tid == 0) sh.open[round & 1] = sh.over[round & 1] = 0;
+      }
     }
+    if (EASY || few || tried || sc == nullptr) break;  // (a row scored by its own CTA has no norms)
+    const float norms = leave_out<T>(p, r, h, n, nb, row.norms, row.q_norm, sh, CACHED ? cache : sc);
+    if (norms == 0.f) break;
+    off = eps * norms;
+    over = 0;
+    scores_changed();
   }
 
-  if (few) {
+  if (EASY && !few) return false;
+  if (EASY || few) {
     // ---- a warp settles it, a lane a block
     const int places = want - over;  // 1 <= places <= open
     for (int i = tid; i < p.first + p.last; i += T) choose(i < p.first ? i : nb - p.last + i - p.first);
@@ -1206,8 +1262,7 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
     // ---- Many at the border, or none: queries that are no finite numbers, pages that are alike, or no place but the kept
     // ones'.  The border digit by digit, of the scores and then, among those that they leave open, of the exact scores: of their
     // upper halves, which take the scores' places, and of the lower halves of those that then tie.  512 rows of 2048 pages,
-    // 8 heads, of which one page's bounds are 10^4 times the others': 14 ms (125 where each digit had every score computed
-    // again).
+    // 8 heads, of two kinds whose scores tie: 28 ms (125 where each digit had every score computed again).
     int* hist = sh.digits;
     auto digit = [&](int left) {  // the one that holds the left-th largest
       sync_row<T>();
@@ -1267,7 +1322,7 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
     bool score_again = left < sh.open[0] && !(known && off == 0.f) && row.q_norm == row.q_norm;
     if (score_again) {
       // Pages with the same bounds have the same score, and a cache that nothing was written to has no others: 512 rows of
-      // 2048 such pages, 8 heads, took 126 ms by exact scores.
+      // 2048 such pages, 8 heads, take 1.2 ms this way.
       if (tid == 0) sh.among = 0;
       sync_row<T>();
       const uint32_t* bounds = reinterpret_cast<const uint32_t*>(p.bounds);
@@ -1365,6 +1420,29 @@ __device__ __forceinline__ void pick(const SelectBlocksParams& p, const Row& row
     for (; bits != 0; bits &= bits - 1, ++place)
       if (place < K) out[place] = 32 * (w0 + lane) + __ffs(bits) - 1;
   }
+  return true;
+}
+
+// The other rows, apart: what they need of registers would cost the easy ones
+template <int T, bool CACHED>
+__device__ __noinline__ void pick_hard(const SelectBlocksParams& p, int r, int h, int n, int nb, float* scores, const float* norms,
+                                       float q_norm, float b_norm, bool wild, float eps, PickShared& sh, uint32_t* s_bits) {
+  Row row;
+  row.r = r;
+  row.h = h;
+  row.n = n;
+  row.nb = nb;
+  row.scores = scores;
+  row.norms = norms;
+  row.q_norm = q_norm;
+  row.b_norm = b_norm;
+  row.wild = wild;
+  sync_row<T>();
+  pick<T, CACHED, false>(p, row, eps, sh, s_bits);
+}
+template <int T, bool CACHED>
+__device__ __forceinline__ void pick_hard(const SelectBlocksParams& p, const Row& row, float eps, PickShared& sh, uint32_t* s_bits) {
+  pick_hard<T, CACHED>(p, row.r, row.h, row.n, row.nb, row.scores, row.norms, row.q_norm, row.b_norm, row.wild, eps, sh, s_bits);
 }
 
 // The same by a warp that holds the scores in registers, 32 NR at most; wild tiles are tame.  norms: ||Q|| times the largest
@@ -1518,11 +1596,11 @@ __global__ void __launch_bounds__(128, NR == 16 ? 6 : NR == 32 ? 5 : 4) select_w
   const float most = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(row.b_norm)));
   const float b_norm = fmaxf(most, wild ? LEAST_NORM : 0.f), norms = norm_of_q(row, wild) * b_norm;
   if (wild && norms < INFINITY) {
-    tame<32>(p, row.r, row.h, row.n, row.nb, row.norms, b_norm, 2.f * norms, shared[warp].q, row.scores);
+    tame<32>(p, row.r, row.h, row.n, row.nb, row.norms, INFINITY, b_norm, 2.f * norms, shared[warp].q, row.scores);
     __syncwarp();
   }
   if (!pick_warp<NR>(p, row, norms, wild, ws.eps, shared[warp]))
-    pick<32, false>(p, row, ws.eps, shared[warp], s_words + warp * cache_at(p.max_blocks));
+    pick_hard<32, false>(p, row, ws.eps, shared[warp], s_words + warp * cache_at(p.max_blocks));
 }
 
 template <int T, bool CACHED>
@@ -1547,7 +1625,7 @@ __global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const __gr
   row.wild = false;
   for (int i = threadIdx.x; i < (row.nb + 15) / 16; i += T) count_norm(row, row.norms[i]);
   row.scores = ws.scores + static_cast<int64_t>(blockIdx.x) * ws.stride;
-  pick<T, CACHED>(p, row, ws.eps, shared, s_bits);
+  if (!pick<T, CACHED, true>(p, row, ws.eps, shared, s_bits)) pick_hard<T, CACHED>(p, row, ws.eps, shared, s_bits);
 }
 
 // Short sequences of one row each: a CTA scores the blocks of a row and KV head and picks among them, in one launch.  A
@@ -1711,7 +1789,7 @@ __global__ void __launch_bounds__(T, 512 / T) select_one_kernel(const __grid_con
   }
   // the sum of squares may have been an eighth too small
   row.b_norm = fmaxf(1.1f * sqrtf(row.b_norm), LEAST_NORM);
-  pick<T, true>(p, row, eps, shared, s_bits);
+  if (!pick<T, true, true>(p, row, eps, shared, s_bits)) pick_hard<T, true>(p, row, eps, shared, s_bits);
 }
 
 // A kernel's limit of dynamic shared memory belongs to the kernel on the device, not to the call: two host threads set it

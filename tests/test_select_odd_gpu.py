@@ -144,13 +144,37 @@ def test_an_odd_page_does_not_hold_up_the_others(attn, gpu, name):
             assert taken < 6 * plain + 60, (where, kind, taken, plain)
 
 
+@pytest.mark.parametrize("name", [n for n in SHAPES if "one launch" not in n])
+def test_a_large_page_does_not_hold_up_the_others(attn, gpu, name):
+    """A page, and a few, with bounds 2^14 times the others': they take part with exact scores."""
+    case = _case(name, gpu)
+    plain = _micros(lambda: _call(attn, case))
+    q, b, table, lens, cu, rows, K = case
+    width = table.shape[1]
+    for odd in ([width // 3], list(range(40, width, max(600, width // 4)))):
+        case = _case(name, gpu)
+        for n in range(table.shape[0]):
+            at = case[2][n, odd].long()
+            case[1][at] = (b[at].float() * 2.0 ** 14).to(torch.bfloat16)
+        got = _call(attn, case)
+        for r in sorted({0, rows - 1, got.shape[0] // 2, got.shape[0] - 1}):
+            assert torch.equal(got[r], _wanted(case, r)), (len(odd), r)
+        if len(odd) * table.shape[0] * 16 * 16 < width:  # (pages lie in several sequences' tables)
+            taken = _micros(lambda: _call(attn, case))
+            assert taken < 8 * plain + 100, (taken, plain)
+
+
 @pytest.mark.parametrize("name", ["a warp a row, wide", "chunk"])
 def test_exact_scores_are_computed_once(attn, gpu, name):
-    """Where all pages are unsure their scores in 64 bits take 2 to 4 ns a row, head and page of a full GPU, for their upper halves
-    and for the lower ones of a few; 15 where each of eight digits took them again."""
+    """Two kinds of pages whose scores tie, but not their bounds: exact scores in 64 bits of all, upper halves and lower ones, take
+    4 ns a row, head and page of a full GPU; 15 where each of eight digits took them again."""
     case = _case(name, gpu)
     N, rows, width, H, _, _ = SHAPES[name]
-    case[1][case[2][:, width // 3].long()] *= 2.0 ** 14
+    b = case[1]
+    b[0::2], b[1::2] = b[0].clone(), b[0].clone()
+    b[1::2, :, :, 5] = 0
+    case[0][:, :, 5] = 0
     taken = _micros(lambda: _call(attn, case))
-    each = taken * 1e3 / (N * rows * H * width)
-    assert each < 7, each
+    assert taken * 1e3 / (N * rows * H * width) < 7
+    got = _call(attn, case)
+    assert torch.equal(got[0], _wanted(case, 0))
