@@ -1219,7 +1219,7 @@ __device__ __forceinline__ bool pick(const SelectBlocksParams& p, const Row& row
         if (tid == 0) sh.open[round & 1] = sh.over[round & 1] = 0;
       }
     }
-    if (EASY || few || tried || sc == nullptr) break;  // (a row scored by its own CTA has no norms)
+    if (EASY || few || tried || sc == nullptr || off == 0.f) break;  // (a row scored by its own CTA has no norms)
     const float norms = leave_out<T>(p, r, h, n, nb, row.norms, row.q_norm, sh, CACHED ? cache : sc);
     if (norms == 0.f) break;
     off = eps * norms;
