@@ -131,7 +131,8 @@ def decode_f8_workspace_bytes(d: int, device=None) -> int:
 def decode_paged_f8(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
                     scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                     return_lse: bool = True, workspace: torch.Tensor | None = None, stream=None):
-    """Single-token attention over the 8-bit cache: q [N,Hq,d] bf16 -> (o [N,Hq,d], lse [N,Hq])."""
+    """Single-token attention over the 8-bit cache: q [N,Hq,d] bf16 -> (o [N,Hq,d], lse [N,Hq]).  Few short sequences are
+    faster in a block table that is no wider than the longest of them needs."""
     dev = q.get_device()
     N, Hq, d = q.shape
     num_blocks, Hkv, max_blocks = _check_paged(dev, d, cache, block_table, seq_lens, N)
@@ -220,7 +221,9 @@ def select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tens
     [num_blocks,Hkv,2,d] allow the highest scores; all where there are no more than num_selected.
 
     cu_seqlens_q as for decode_blocks_f8, with at most max_seqlen_q rows a sequence (without it any number: a bound of
-    up to four rows takes a faster way)."""
+    up to four rows takes a faster way).  The workspace holds a score for each row, KV head and column of the table: 1.1 GB
+    for a chunk of 4096 tokens over 131072 and 8 KV heads, so give a long chunk in parts, and
+    block_table[:, :pages].contiguous() where the table is much wider than the longest sequence needs."""
     dev, N = q.get_device(), seq_lens.numel()
     T, Hq, d = q.shape
     if dev < 0 or bounds.dtype is not _BF16 or bounds.get_device() != dev or not bounds.is_contiguous():

@@ -23,9 +23,9 @@
 // width takes, and the loading warp says how many tokens of each page the query sees.
 //
 // Bound by reading the records.  Measured (GB300, calls in a captured graph, copy rate 6796 GB/s): 64 sequences of 512
-// to 8192, 32/8 heads, d = 128, 96.5 us, 5.95 TB/s; 8 of 6335 to 122863, 16/2 heads, d = 256, 87.0 us, 6.10 TB/s.  The
+// to 8192, 32/8 heads, d = 128, 96.2 us, 5.96 TB/s; 8 of 6335 to 122863, 16/2 heads, d = 256, 87.3 us, 6.08 TB/s.  The
 // kernel itself reads at 6.1 TB/s with 31% of the issue slots used; start, merge and CTAs that end earlier than others
-// are the rest.  64 listed blocks of each row and head, 133 MB: 27.1 us, 4.92 TB/s, a CTA each; 1 sequence of 1009 8.5 us.
+// are the rest.  64 listed blocks of each row and head, 133 MB: 27.1 us, 4.92 TB/s, a CTA each; 1 sequence of 1009 8.6 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -68,7 +68,8 @@ enum Deal { SHARES, WHOLE, ALONE, MANY };
 template <int D, int P, int DEAL>
 struct Cfg {
   // Warps that compute (one more loads), steps in flight a warp, and CTAs an SM: what shared memory holds.  SHARES, measured
-  // on 64 sequences of 512 to 8192, 32/8 heads, d = 128, warps x steps x CTAs: 5 x 2 x 2 98.8 us, 3 x 2 x 3 100.4, 4 x 3 x 2
+  // in one series (in which the form that is used took 98.8 us; by itself it takes 96 to 97) on 64 sequences of 512 to 8192, 32/8
+  // heads, d = 128, warps x steps x CTAs: 5 x 2 x 2 (used) 98.8 us, 3 x 2 x 3 100.4, 4 x 3 x 2
   // 103.9, 11 x 2 x 1 102.7 (more in flight is no faster), one page a step 7 x 2 x 2 100.6.  64 of 8704, d = 64, 64/8
   // heads: 5 x 3 x 3 116.3, 3 x 3 x 5 (FINE) 109.7; with 32/8 heads, two pages a step, 104.0 and 105.6.  64 of 512 to 8192,
   // 64/8 heads, d = 128: 7 x 2 x 2 105.0, 3 x 2 x 4 102.4, 3 x 3 x 4 101.0; MANY's 512 lists of 64 blocks with two steps
@@ -838,7 +839,8 @@ cudaError_t launch(const DecodeF8Params& p, cudaStream_t stream) {
   //        32.6, of 500 to 8000 93.7 98.9 109 113; 64 listed blocks 34.1 44.7 32.4 27.8, 128 54.5 65.8 52.3 47.2
   //   640: 64 listed blocks 40.2 54.6 45.1 41.7; 896: 50.9 67.7 51.0 49.4, 2000 tokens 80.1 87.5 76.0 79.5;
   //   1200: 64 listed blocks 63.5 89.3 66.9 57.8; 2400: 1000 tokens 104 142 111 99
-  // and the other head dims and group sizes alike: over 637 cases the rule takes 0.77 of the time of SHARES alone.
+  // A table that is wider than its sequences are long may lead to the slower side: 16 sequences of 1000 tokens take 8.6 us in a table
+  // of 63 columns and 13.8 in one of 513 or more, 64 of them 25.3 and 31.
   const int64_t pages = LISTED ? p.K : p.max_blocks, steps = (pages + P - 1) / P;
   auto lost = [&](int64_t ctas) {  // with so many at a time
     const int64_t places = (pairs + ctas - 1) / ctas * ctas;

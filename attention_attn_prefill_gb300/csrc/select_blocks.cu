@@ -15,12 +15,14 @@
 //   |score - exact| <= eps ||Q|| ||b||,  b = (lo, hi) of a block, by Cauchy and Schwarz on the sum of |terms| (score_error).
 // Pick: a CTA, or where there are many a warp, puts the scores of its row and head into bins over their range, gathers
 // the few in and about the bin that holds the border, and a warp settles the border among them.  Few short sequences of
-// one row each take one launch, a CTA scoring and picking: select_one_kernel.
+// one row each take one launch, a CTA scoring and picking: select_one_kernel.  Pages whose bounds are no finite numbers, or
+// far above the others', would make the bound too wide for the rest: they are scored in 64 bits and take part (tame).
 //
 // Measured (GB300, calls in a captured graph, copy rate 6796 GB/s): 64 rows over 512 to 8192 tokens, 32/8 heads, d = 128,
-// 27.4 us, of which the scores take 17.5 (72 MB of bounds: 10.6 at the copy rate) and the pick's chain of dependent steps
-// the rest; 8 rows over 6335 to 122863 tokens, 16/2 heads, d = 256, 29.0 (9.8), of which the scores 16.3; 512 rows of one
-// sequence of 32768, 32/8 heads, 43.2, of which the scores 20.4 (4096 rows of 2048: 33 MB written) and the pick 23.
+// 27.9 us, of which the scores take 17.5 (72 MB of bounds: 10.6 at the copy rate) and the pick's chain of dependent steps
+// the rest; 8 rows over 6335 to 122863 tokens, 16/2 heads, d = 256, 29.5 (9.8), of which the scores 16.3; 512 rows of one
+// sequence of 32768, 32/8 heads, 43.6, of which the scores 20.4 (4096 rows of 2048: 33 MB written) and the pick 23.
+// One page of NaN beside the others: 129 us instead of 43 for the latter, 52 instead of 25 for 64 rows.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -1563,7 +1565,8 @@ __device__ __forceinline__ bool pick_warp(const SelectBlocksParams& p, const Row
   return true;
 }
 
-// A warp a row and KV head, four a CTA
+// A warp a row and KV head, four a CTA.  The numbers of CTAs keep 20 to 90 bytes a thread of two forms (16 and 32 scores a lane) in
+// local memory, as two CTAs an SM do 50 of select_one_kernel's at d = 128: mostly of the rare ways through.
 template <int NR>
 __global__ void __launch_bounds__(128, NR == 16 ? 6 : NR == 32 ? 5 : 4) select_warps_kernel(const __grid_constant__ SelectBlocksParams p, const Scratch ws) {
   extern __shared__ __align__(16) uint32_t s_words[];

@@ -714,7 +714,8 @@ size_t attn_decode_f8_workspace_bytes(int d);
 /*
  * attn_decode_paged over the 8-bit cache: arguments, conventions, errors and
  * workspace as for attn_decode_paged_q4, with attn_decode_f8_workspace_bytes(d)
- * bytes.
+ * bytes.  The work is dealt out by the width of the block table: one as narrow
+ * as the longest sequence allows is faster for few short sequences.
  * Arithmetic: products of the codes, exact as fp16, with the queries as fp16
  * numbers times a power of two a head: their 8 bits are kept down to 2^-28 of
  * the head's largest channel, and 2^-39 of it in absolute terms below.  float32
@@ -770,6 +771,9 @@ attn_status_t attn_prefill_paged_f8(const void* q, const void* cache, const int3
  * column of the block table, and their error bounds; with more than 4 rows a
  * sequence also the queries' sums over the heads of a KV head.  0 for invalid
  * arguments (also 2^31 tiles of 16 blocks over all sequences and KV heads).
+ * Grows with num_tokens * Hkv * max_blocks_per_seq * 4: 1.1 GB for 4096 rows over
+ * 131072 tokens with 8 KV heads.  A long chunk may be given in parts of some
+ * hundred rows, whose calls share one workspace in turn.
  */
 size_t attn_select_blocks_workspace_bytes(int num_tokens, int num_seqs, int max_seqlen_q, int Hkv, int d,
                                           int max_blocks_per_seq);
@@ -790,13 +794,18 @@ size_t attn_select_blocks_workspace_bytes(int num_tokens, int num_seqs, int max_
  *   sum_c (neg_c lo_c + pos_c hi_c),  neg_c = sum_g min(q_gc, 0), pos_c = sum_g max(q_gc, 0)
  * over the channels c and the query heads g of the KV head: the largest sum of
  * q . k that a key within the bounds could have for each head.  Scores are
- * compared as 64-bit arithmetic has them; one that is not a number (a NaN or
- * infinity among its terms) counts as the highest.
+ * compared as 64-bit arithmetic has them; one that is not a number (from a NaN,
+ * or zero times an infinity, among its terms) counts as the highest, above an
+ * infinite one.  Each page with such bounds costs every row an exact score.  Where
+ * more than 32 pages differ by less than float32 arithmetic shows (pages that
+ * tie, but not by equal bounds) a row is compared in 64 bits throughout, which may
+ * take several hundred times as long.
  * Rows of q that belong to no sequence are left as they were in `blocks`.  Errors
  * on the device: 2 for a page out of range (page 0 is taken), 5 for cu_seqlens_q
  * or seq_lens that do not fit (a sequence whose rows do not fit num_tokens or
  * max_seqlen_q is skipped, a length is clamped).
  * workspace: 256-byte aligned; calls that overlap on the GPU need one each.
+ * Host threads may call at the same time.
  */
 attn_status_t attn_select_blocks(const void* q, const void* bounds, const int32_t* block_table,
                                  const int32_t* cu_seqlens_q, const int32_t* seq_lens, int32_t* blocks, int num_selected,
