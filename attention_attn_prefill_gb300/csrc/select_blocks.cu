@@ -996,11 +996,11 @@ __device__ __forceinline__ double product(const SelectBlocksParams& p, const dou
   return sum;
 }
 
-// Wild tiles, those with a bound that is no finite number or too large (of a norm from `cut` on), would leave every score of the row unsure.  Their
-// blocks whose norm is above `limit`, the largest one of the other tiles, are scored in 64 bits, and take part with that score as a
-// float, cut to what is above or below all others': `most`, twice ||Q|| times the limit.  That is off by less than the
-// others' bound, keeps the order among wild blocks, and those that it makes equal are told apart by exact scores, like all that
-// are close to the border.  By all threads of the row, between two barriers.
+// Wild tiles, those with a bound that is no finite number or too large (of a norm from `cut` on), would leave every score of
+// the row unsure.  Their blocks whose norm is above `limit`, the largest one of the other tiles, are scored in 64 bits, and
+// take part with that score as a float, cut to what is above or below all others': `most`, twice ||Q|| times the limit.  That
+// is off by less than the others' bound, keeps the order among wild blocks, and those that it makes equal are told apart by
+// exact scores, like all that are close to the border.  By all threads of the row, between two barriers.
 template <int T>
 __device__ __noinline__ void tame(const SelectBlocksParams& p, int r, int h, int n, int nb, const float* norms, float cut,
                                   float limit, float most, double* sums, float* scores) {
@@ -1565,10 +1565,11 @@ __device__ __forceinline__ bool pick_warp(const SelectBlocksParams& p, const Row
   return true;
 }
 
-// A warp a row and KV head, four a CTA.  The numbers of CTAs keep 20 to 90 bytes a thread of two forms (16 and 32 scores a lane) in
-// local memory, as two CTAs an SM do 50 of select_one_kernel's at d = 128: mostly of the rare ways through.
+// A warp a row and KV head, four a CTA.  The numbers of CTAs an SM leave 20 to 90 bytes a thread of the forms with 16 and 32
+// scores a lane in local memory, and 50 of select_one_kernel's at d = 128.
 template <int NR>
-__global__ void __launch_bounds__(128, NR == 16 ? 6 : NR == 32 ? 5 : 4) select_warps_kernel(const __grid_constant__ SelectBlocksParams p, const Scratch ws) {
+__global__ void __launch_bounds__(128, NR == 16 ? 6 : NR == 32 ? 5 : 4)
+    select_warps_kernel(const __grid_constant__ SelectBlocksParams p, const Scratch ws) {
   extern __shared__ __align__(16) uint32_t s_words[];
   __shared__ PickShared shared[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1607,7 +1608,8 @@ __global__ void __launch_bounds__(128, NR == 16 ? 6 : NR == 32 ? 5 : 4) select_w
 }
 
 template <int T, bool CACHED>
-__global__ void __launch_bounds__(T, T == 128 ? 10 : 1) select_kernel(const __grid_constant__ SelectBlocksParams p, const Scratch ws) {
+__global__ void __launch_bounds__(T, T == 128 ? 10 : 1)
+    select_kernel(const __grid_constant__ SelectBlocksParams p, const Scratch ws) {
   extern __shared__ __align__(16) uint32_t s_bits[];
   __shared__ PickShared shared;
   Row row;
@@ -1871,11 +1873,11 @@ cudaError_t score_many(const SelectBlocksParams& p, const Scratch& ws, int sms, 
 }
 
 // How far scores may be off, relative to ||Q|| ||b||: Q as two bf16 numbers 2^-18, its sums over G heads 2^-24 each, and the
-// matrix products.  Measured on sm_103a: a product aligns its terms and the accumulator to the largest one and drops what
-// lies below 2^-25 of that one's power of two, then cuts the sum to 24 bits: it is off by (terms + 4) 2^-25 of the sum of
-// |terms| at most.  mma.sync takes 8 terms at a time, two accumulators share the 2 d, and three additions join them
-// with the second parts of Q; tcgen05 takes 16, for the second parts first.  One 2^-25 a product covers those parts, which are 2^-8 of
-// the first at most.  Terms made to lose all that they can reach 0.41 to 0.63 of this with tcgen05, 0.26 to 0.46 with mma.sync;
+// matrix products.  Measured on sm_103a: a product aligns its terms and the accumulator to the largest one and drops what lies
+// below 2^-25 of that one's power of two, then cuts the sum to 24 bits: it is off by (terms + 4) 2^-25 of the sum of |terms|
+// at most.  mma.sync takes 8 terms at a time, two accumulators share the 2 d, and three additions join them with the second
+// parts of Q; tcgen05 takes 16, for the second parts first.  One 2^-25 a product covers those parts, which are 2^-8 of the
+// first at most.  Terms made to lose all that they can reach 0.41 to 0.63 of this with tcgen05, 0.26 to 0.46 with mma.sync;
 // random ones 0.03.
 template <int D, bool FEW_ROWS>
 constexpr float score_error(int heads) {
